@@ -11,6 +11,8 @@ generators (``inputs``).  The binding's names mirror the C entry points:
 * ``fa_decode_splitkv_multi`` -- the same with several query tokens per sequence;
 * ``fa_decode_splitkv_paged`` -- the same over a paged KV cache with a block table;
 * ``fa_decode_splitkv_noalloc`` -- decode with library-owned scratch (no workspace);
+* ``fa_kv_append_paged_fp8``, ``fa_decode_splitkv_paged_fp8``, ``fa_kv_read_paged_fp8`` -- an
+  8-bit paged KV cache: rows quantised as they are written, attended over, read back;
 * ``fa_decode_workspace_bytes``, ``fa_decode_default_splits``, ``fa_status_string``,
   ``fa_last_device_status``, ``fa_selftest_bounded_wait`` (the bounded-wait self-test).
 
@@ -18,12 +20,14 @@ Importing the package does not load the library; the first call does, and raises
 ``libfa.so`` has not been built.
 """
 from ._lib import (FA_BF16, FA_FP16, FaError, fa_decode_default_splits, fa_decode_splitkv,
-                   fa_decode_splitkv_multi, fa_decode_splitkv_noalloc, fa_decode_splitkv_paged, fa_decode_workspace_bytes,
-                   fa_fwd, fa_fwd_varlen, fa_last_device_status, fa_selftest_bounded_wait,
+                   fa_decode_splitkv_multi, fa_decode_splitkv_noalloc, fa_decode_splitkv_paged,
+                   fa_decode_splitkv_paged_fp8, fa_decode_workspace_bytes, fa_fwd, fa_fwd_varlen,
+                   fa_kv_append_paged_fp8, fa_kv_read_paged_fp8, fa_last_device_status, fa_selftest_bounded_wait,
                    fa_status_string, library_path, load)
 
 __all__ = [
     "FA_BF16", "FA_FP16", "FaError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_splitkv_paged",
+    "fa_decode_splitkv_paged_fp8", "fa_kv_append_paged_fp8", "fa_kv_read_paged_fp8",
     "fa_decode_splitkv_noalloc", "fa_decode_splitkv_multi", "fa_decode_workspace_bytes", "fa_decode_default_splits",
     "fa_status_string", "fa_last_device_status", "fa_selftest_bounded_wait", "library_path", "load",
 ]

@@ -377,3 +377,226 @@ def fa_decode_splitkv_multi(q, k_cache, v_cache, kv_lens, causal: bool = True,
     if st != FA_OK:
         raise FaError(st, "fa_decode_splitkv_multi")
     return out, lse
+
+
+# ---- 8-bit paged KV cache.  These run once per layer and token, so the checks below are
+# written to cost little host time: one pass over the tensors, the signatures declared once.
+_fp8_lib = None
+
+
+def _load_fp8():
+    global _fp8_lib
+    if _fp8_lib is None:
+        lib = load()
+        P, I, F, SZ, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+        lib.fa_kv_append_paged_fp8.argtypes = [P, P, L, L, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]
+        lib.fa_kv_append_paged_fp8.restype = I
+        lib.fa_kv_read_paged_fp8.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P]
+        lib.fa_kv_read_paged_fp8.restype = I
+        lib.fa_decode_splitkv_paged_fp8.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I,
+                                                    I, P, SZ, I, P]
+        lib.fa_decode_splitkv_paged_fp8.restype = I
+        _fp8_lib = lib
+    return _fp8_lib
+
+
+def _check_on(name, t, dtype, device, shape=None):
+    """t: a contiguous tensor of this type (and shape) on `device`, a CUDA device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table):
+    """Checks the pool's tensors; returns (device, num_pages, Hkv, page_size, D, B, max_pages)."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a tensor [num_pages, Hkv, page_size, D]")
+    device, shape = k_pages.device, k_pages.shape
+    _check_on("k_pages", k_pages, torch.float8_e4m3fn, device)
+    _check_on("v_pages", v_pages, torch.float8_e4m3fn, device, shape)
+    _check_on("k_scales", k_scales, torch.uint8, device, shape[:3])
+    _check_on("v_scales", v_scales, torch.uint8, device, shape[:3])
+    _check_on("block_table", block_table, torch.int32, device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages_per_seq]")
+    return (device, *shape, *block_table.shape)
+
+
+def _stream_on(device, stream):
+    """(handle of `stream` or of the device's current stream, the stream where it is not the
+    current one)."""
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return current.cuda_stream, None
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, not on {device}")
+    return stream.cuda_stream, (None if stream == current else stream)
+
+
+def _made(t, other):
+    """A tensor made for a call: its memory is not reused before `other`, the call's stream
+    where it is not the current one, is done with it."""
+    if other is not None:
+        t.record_stream(other)
+    return t
+
+
+def _call_on(device, fn, *args):
+    """Calls a C entry point with `device` current."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != FA_OK:
+        raise FaError(st, fn.__name__)
+
+
+def _new_rows(name, t, dtype, device, Hkv, D):
+    """A tensor of new rows [..., Hkv, D] with dense rows: its tokens and their stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) not in (3, 4) or shape[-2] != Hkv or shape[-1] != D:
+        raise ValueError(f"{name} must be [B, n, {Hkv}, {D}] or [total, {Hkv}, {D}], got {tuple(shape)}")
+    if t.numel() == 0:
+        return 0, Hkv * D
+    if strides[-1] != 1 or (Hkv > 1 and strides[-2] != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if len(shape) == 3:
+        return shape[0], strides[0] if shape[0] > 1 else Hkv * D
+    B, n = shape[0], shape[1]
+    if n == 1:
+        return B, strides[0] if B > 1 else Hkv * D
+    if B > 1 and strides[0] != n * strides[1]:
+        raise ValueError(f"{name}: the tokens of the batch must have one stride")
+    return B * n, strides[1]
+
+
+def fa_kv_append_paged_fp8(k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens,
+                           cu_seqlens_new=None, stream=None):
+    """Quantises new K/V rows into the 8-bit paged cache through fa_kv_append_paged_fp8.
+
+    k_new/v_new bf16 or fp16: [B, n, Hkv, D] (n new tokens for each sequence), or packed
+    [total, Hkv, D] with cu_seqlens_new int32 [B+1]; the tokens may be strided (a slice of a
+    fused projection), the heads of a token dense. k_pages/v_pages float8_e4m3fn
+    [num_pages, Hkv, page_size, D], k_scales/v_scales uint8 [num_pages, Hkv, page_size],
+    block_table int32 [B, max_pages_per_seq]; kv_lens int32 [B] counts the new tokens: they
+    become the last keys of their sequences.  Writes the pool in place; returns None."""
+    lib = _load_fp8()
+    device, num_pages, Hkv, page, D, B, max_pages = _check_fp8_pool(k_pages, v_pages, k_scales, v_scales,
+                                                                    block_table)
+    if not isinstance(k_new, torch.Tensor) or k_new.dtype not in _DTYPE:
+        raise TypeError("k_new/v_new must be bf16 or fp16 tensors")
+    total, k_stride = _new_rows("k_new", k_new, k_new.dtype, device, Hkv, D)
+    total_v, v_stride = _new_rows("v_new", v_new, k_new.dtype, device, Hkv, D)
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have one shape")
+    _check_on("kv_lens", kv_lens, torch.int32, device, (B,))
+    cu = None
+    if cu_seqlens_new is not None:
+        _check_on("cu_seqlens_new", cu_seqlens_new, torch.int32, device, (B + 1,))
+        if k_new.dim() != 3:
+            raise ValueError("with cu_seqlens_new, k_new and v_new are packed [total, Hkv, D]")
+        cu = cu_seqlens_new.data_ptr()
+    elif k_new.dim() != 4 or k_new.shape[0] != B:
+        raise ValueError("without cu_seqlens_new, k_new and v_new are [B, n, Hkv, D]")
+    handle, _ = _stream_on(device, stream)
+    _call_on(device, lib.fa_kv_append_paged_fp8, k_new.data_ptr(), v_new.data_ptr(), k_stride, v_stride, cu,
+             block_table.data_ptr(), kv_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+             k_scales.data_ptr(), v_scales.data_ptr(), B, total, Hkv, D, num_pages, page, max_pages,
+             _DTYPE[k_new.dtype], handle)
+
+
+def fa_kv_read_paged_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens, total=None,
+                         kv_starts=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Reads rows of the 8-bit paged cache back through fa_kv_read_paged_fp8.
+
+    Packed rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 receive keys kv_starts[b] (0), ... of
+    sequence b; cu_seqlens int32 [B+1], kv_starts int32 [B], on the device.  k_out/v_out
+    [total, Hkv, D] are given, or made here from ``total`` and ``dtype``; rows behind the last
+    sequence are not written.  Returns (k, v)."""
+    lib = _load_fp8()
+    device, num_pages, Hkv, page, D, B, max_pages = _check_fp8_pool(k_pages, v_pages, k_scales, v_scales,
+                                                                    block_table)
+    _check_on("cu_seqlens", cu_seqlens, torch.int32, device, (B + 1,))
+    if kv_starts is not None:
+        _check_on("kv_starts", kv_starts, torch.int32, device, (B,))
+    given = k_out if k_out is not None else v_out
+    if given is not None:
+        dtype = given.dtype
+        if total is None:
+            total = given.shape[0]
+    elif total is None:
+        raise ValueError("give total, the packed rows, or k_out and v_out")
+    if dtype not in _DTYPE:
+        raise TypeError("k/v are read as bf16 or fp16")
+    handle, other = _stream_on(device, stream)
+    shape = (int(total), Hkv, D)
+    if k_out is None:
+        k_out = _made(torch.empty(shape, dtype=dtype, device=device), other)
+    if v_out is None:
+        v_out = _made(torch.empty(shape, dtype=dtype, device=device), other)
+    _check_on("k_out", k_out, dtype, device, shape)
+    _check_on("v_out", v_out, dtype, device, shape)
+    _call_on(device, lib.fa_kv_read_paged_fp8, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+             v_scales.data_ptr(), block_table.data_ptr(), None if kv_starts is None else kv_starts.data_ptr(),
+             cu_seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, shape[0], Hkv, D, num_pages, page,
+             max_pages, _DTYPE[dtype], handle)
+    return k_out, v_out
+
+
+def fa_decode_splitkv_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens,
+                                causal: bool = True, scale: float | None = None, num_splits: int = 0,
+                                workspace=None, out=None, lse=None, stream=None):
+    """Split-KV decode over the 8-bit paged cache through fa_decode_splitkv_paged_fp8.
+
+    q [B, Sq, Hq, D] bf16 or fp16; the pool as fa_kv_append_paged_fp8 writes it; kv_lens
+    int32 [B].  workspace: a CUDA uint8 tensor of at least fa_decode_workspace_bytes(B * Sq,
+    Hq, D, num_splits) bytes, or None to allocate one.  Returns (o like q, lse fp32
+    [B, Hq, Sq])."""
+    lib = _load_fp8()
+    device, num_pages, Hkv, page, D, B, max_pages = _check_fp8_pool(k_pages, v_pages, k_scales, v_scales,
+                                                                    block_table)
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
+        raise TypeError("q must be a bf16 or fp16 tensor")
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+        raise ValueError(f"q must be [{B}, Sq, Hq, {D}], got {tuple(q.shape)}")
+    _check_on("q", q, q.dtype, device)
+    Sq, Hq = q.shape[1], q.shape[2]
+    _check_on("kv_lens", kv_lens, torch.int32, device, (B,))
+    handle, other = _stream_on(device, stream)
+    ns = int(num_splits)
+    if workspace is None:
+        if ns <= 0:
+            with torch.cuda.device(device):
+                ns = lib.fa_decode_default_splits(B, Hkv, page * max_pages, 0)
+        workspace = _made(torch.empty(max(16, lib.fa_decode_workspace_bytes(B * Sq, Hq, D, ns)),
+                                      dtype=torch.uint8, device=device), other)
+    else:
+        _check_on("workspace", workspace, torch.uint8, device)
+    if out is None:
+        out = _made(torch.empty_like(q), other)
+    else:
+        _check_on("out", out, q.dtype, device, q.shape)
+    if lse is None:
+        lse = _made(torch.empty((B, Hq, Sq), dtype=torch.float32, device=device), other)
+    else:
+        _check_on("lse", lse, torch.float32, device, (B, Hq, Sq))
+    _call_on(device, lib.fa_decode_splitkv_paged_fp8, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+             k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+             out.data_ptr(), lse.data_ptr(), B, Sq, Hq, Hkv, D, num_pages, page, max_pages,
+             float(scale) if scale is not None else 1.0 / math.sqrt(D), int(bool(causal)), ns,
+             workspace.data_ptr(), workspace.numel(), _DTYPE[q.dtype], handle)
+    return out, lse

@@ -1,0 +1,8 @@
+// fa_kv8_decode_d128.cu -- decode over the 8-bit paged cache, head dim 128.
+#include "fa_kv8_decode.cuh"
+
+namespace fa {
+
+fa_status launch_kv8_decode_d128(const Kv8DecodeArgs& a, cudaStream_t s) { return launch_kv8_decode_d<128>(a, s); }
+
+}  // namespace fa

@@ -1,7 +1,8 @@
 /*
  * fa.h -- C ABI of the exact tiled attention library for NVIDIA GB300 (sm_103a).
  *
- * Two operations, as the source pages define them:
+ * Two operations, as the source pages define them, and an 8-bit paged KV cache for the
+ * second (fa_kv_append_paged_fp8, fa_kv_read_paged_fp8, fa_decode_splitkv_paged_fp8):
  *
  *  fa_fwd             exact attention forward, O = softmax(scale * Q K^T [+ causal mask]) V,
  *                     plus the per-row log-sum-exp.  Page "flash-attention-v100", section
@@ -226,6 +227,101 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void *q, const void *k_cache,
                                            float *lse, int B, int Hq, int Hkv, int D, int Smax,
                                            float scale, int num_splits, fa_dtype dtype,
                                            fa_stream_t stream);
+
+/*
+ * 8-bit paged KV cache.  The pages' changelog quantises nothing; these three entry points
+ * are this library's own: a paged cache at half the bytes of the 16-bit one, written,
+ * attended over and read back.
+ *
+ * A row is one token's D values of one kv head, held as e4m3 codes (4 significant bits)
+ * with one power-of-two scale:
+ *   k_pages, v_pages    [num_pages, Hkv, page_size, D]  e4m3 codes
+ *   k_scales, v_scales  [num_pages, Hkv, page_size]     bytes s; the scale is 2^(s - 127)
+ * and stands for code * 2^(s - 127).  The head comes before the slot, other than in the
+ * 16-bit pools, so that what one head reads of a page is one run of memory.
+ *   block_table         device int32 [B, max_pages_per_seq]: key r of sequence b is slot
+ *                       r % page_size of page block_table[b][r / page_size]
+ * page_size is a multiple of 16; D in {64, 96, 128, 256}; B <= 1024;
+ * page_size * max_pages_per_seq < 2^31; the pools and scales are 16-byte aligned.  Table
+ * entries outside [0, num_pages) that a call meets are the caller's error: nothing is read
+ * or written outside the pool (what happens instead is said at each call).  A contiguous
+ * cache of Smax keys per sequence is the pool with page_size = Smax and block_table[b][0]
+ * = b.  `dtype` is the type of the 16-bit side; rows may be written in one and read or
+ * attended over in the other.
+ *
+ * fa_kv_append_paged_fp8 quantises new rows as it writes them.
+ *   k_new, v_new    token t, kv head h at element t * k_stride (v_stride) + h * D, so the
+ *                   rows may lie inside a fused projection's output; strides in elements,
+ *                   multiples of 8, at least Hkv * D; 16-byte aligned
+ *   cu_seqlens_new  device int32 [B + 1]: sequence b's new tokens are packed rows
+ *                   [cu_seqlens_new[b], cu_seqlens_new[b + 1]), non-decreasing, ending at
+ *                   most at total_new; rows behind the last are not written.  NULL: every
+ *                   sequence has total_new / B new tokens (B must divide total_new)
+ *   kv_lens         device int32 [B]: sequence b's keys INCLUDING the new ones: its new
+ *                   tokens become its last keys, kv_lens[b] - n .. kv_lens[b] - 1 (what a
+ *                   decode with the same kv_lens then sees)
+ * A row's scale is the least 2^e, e >= -127, with max |x| <= 448 * 2^e (448: e4m3's largest
+ * value), and its codes are x / 2^e rounded to nearest even: a value is off by at most
+ * 2^-4 of itself, or 2^(e - 10) where that is more.  A value that is not finite takes no
+ * part in the scale and becomes NaN.  total_new == 0 writes nothing (k_new and v_new may
+ * then be NULL).  Rows whose key is outside [0, page_size * max_pages_per_seq) or whose
+ * page is outside the pool are dropped.  Two tokens that name the same slot of a page in
+ * one call are the caller's error; the slot then holds one of them or a mixture.
+ */
+FA_API fa_status fa_kv_append_paged_fp8(const void *k_new, const void *v_new, int64_t k_stride,
+                                        int64_t v_stride, const int32_t *cu_seqlens_new,
+                                        const int32_t *block_table, const int32_t *kv_lens,
+                                        void *k_pages, void *v_pages, uint8_t *k_scales,
+                                        uint8_t *v_scales, int B, int total_new, int Hkv, int D,
+                                        int num_pages, int page_size, int max_pages_per_seq,
+                                        fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * Reads rows of the 8-bit paged cache back as `dtype`, packed along the sequences: the K
+ * and V of an fa_fwd_varlen over an already cached prefix.
+ *   cu_seqlens  device int32 [B + 1]: packed rows [cu_seqlens[b], cu_seqlens[b + 1]) of k
+ *               and v receive sequence b's keys kv_starts[b], kv_starts[b] + 1, ...
+ *   kv_starts   device int32 [B]; NULL: 0 for every sequence
+ *   k, v        [total, Hkv, D] (dtype)
+ * Rows that no sequence owns are left as they were; keys outside [0, page_size *
+ * max_pages_per_seq) or on a page outside the pool read as zeros.  code * 2^(s - 127) is
+ * rounded once, to nearest even: bf16 holds every normal such value exactly; a value past
+ * the type's range becomes an infinity.  total == 0 reads nothing.
+ */
+FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
+                                      const uint8_t *k_scales, const uint8_t *v_scales,
+                                      const int32_t *block_table, const int32_t *kv_starts,
+                                      const int32_t *cu_seqlens, void *k, void *v, int B, int total,
+                                      int Hkv, int D, int num_pages, int page_size,
+                                      int max_pages_per_seq, fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * Split-KV decode over the 8-bit paged cache, Sq >= 1 query tokens per sequence.
+ *   q, o      [B, Sq, Hq, D] (dtype)     lse [B, Hq, Sq] fp32 (may be NULL)
+ *   kv_lens   device int32 [B], 0 <= kv_lens[b] <= page_size * max_pages_per_seq; other
+ *             values are the caller's error and are clamped on the device
+ *   causal    as fa_decode_splitkv_multi: token s sees keys j <= kv_lens[b] - Sq + s
+ * (Hq / Hkv) * Sq <= 16.  A token that sees no key gets O = 0 and LSE = -inf.  Cached codes
+ * enter the products exactly; the probabilities are rounded to fp16 (11 bits) for P.V; O is
+ * rounded once.  What lies in the pool behind a sequence's last key is not used, NaN codes
+ * there included.  Keys on a page outside the pool count as zero rows.
+ *   num_splits  the most pieces a (sequence, kv head) pair is cut into (<= 0: the default,
+ *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0))
+ *   workspace at least fa_decode_workspace_bytes(B * Sq, Hq, D, num_splits) bytes; no
+ *             initialisation; may be NULL where num_splits is 1.  Calls that may overlap on
+ *             the GPU need one each.
+ * The result does not depend on num_splits beyond rounding; the same inputs give the same
+ * bits.
+ */
+FA_API fa_status fa_decode_splitkv_paged_fp8(const void *q, const void *k_pages, const void *v_pages,
+                                             const uint8_t *k_scales, const uint8_t *v_scales,
+                                             const int32_t *block_table, const int32_t *kv_lens,
+                                             void *o, float *lse, int B, int Sq, int Hq, int Hkv,
+                                             int D, int num_pages, int page_size,
+                                             int max_pages_per_seq, float scale, int causal,
+                                             int num_splits, void *workspace,
+                                             size_t workspace_bytes, fa_dtype dtype,
+                                             fa_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 FA_API const char *fa_status_string(fa_status s);

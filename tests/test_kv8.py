@@ -1,0 +1,626 @@
+"""The 8-bit paged KV cache on the GPU against its 64-bit reference (oracle/kv8.py).
+
+Writing and reading back are exact by definition (a power-of-two scale, one rounding), so
+codes, scales and read values are compared bit for bit.
+
+The decode's bound, per output value, from its roundings (a rounding is off by at most half
+a step: 2^-9 ... here taken as eps / 2 of the type):
+    |dO| <= u_o |O| + c A,   A = sum_j p_j |v_j|
+    u_o  one rounding of the output: 2^-8 (bf16), 2^-11 (fp16); of a subnormal, half of its step
+    c    2^-11 (P rounded to fp16) + 2 e_s + 2^-21 + N 2^-23
+    e_s  error of a score, in its exponent: (D + 8) 2^-22 max_j scale sum_d |q_d k_jd| (a sum of
+         D products in 32 bits in any order, each step allowed a truncation, and the scale
+         factors), twice because it enters the numerator and the denominator; 2^-21 is
+         exp2's and the division's; N = n / 4 + 64 sums over the n keys (at least four
+         partial sums run side by side in any split)
+and |dLSE| <= e_s + (2^-21 + N 2^-23) + 2^-22 |LSE|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+U_O = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def fa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import exact_tiled_attention_20_gb300 as fa_mod
+    from exact_tiled_attention_20_gb300 import build
+
+    build.build_library()
+    fa_mod.load()
+    return fa_mod
+
+
+class Pool:
+    """A pool on the GPU filled with random bytes (NaN codes and scale byte 255 among them:
+    nothing outside the sequences may matter), its copy in numpy and a scattered table."""
+
+    def __init__(self, pages, Hkv, page, D, B, max_pages, seed=0):
+        rng = np.random.default_rng(seed)
+        self.np = [rng.integers(0, 256, (pages, Hkv, page, D), dtype=np.uint8) for _ in range(2)] + \
+                  [rng.integers(0, 256, (pages, Hkv, page), dtype=np.uint8) for _ in range(2)]
+        self.table_np = rng.permutation(pages)[:B * max_pages].reshape(B, max_pages).astype(np.int32)
+        self.upload()
+
+    def upload(self):
+        t = [torch.from_numpy(a.copy()).to(DEV) for a in self.np]
+        self.k, self.v = t[0].view(torch.float8_e4m3fn), t[1].view(torch.float8_e4m3fn)
+        self.ks, self.vs = t[2], t[3]
+        self.table = torch.from_numpy(self.table_np).to(DEV)
+
+    @property
+    def args(self):
+        return self.k, self.v, self.ks, self.vs, self.table
+
+    def host(self):
+        return [t.view(torch.uint8).cpu().numpy() for t in (self.k, self.v, self.ks, self.vs)]
+
+    def fill(self, rng, lens, spread=3):
+        """Ordinary rows for the first lens[b] keys of every sequence, in numpy and on the GPU."""
+        k, v, ks, vs = self.np
+        page = k.shape[2]
+        for b, n in enumerate(lens):
+            for j in range(n):
+                p = self.table_np[b, j // page]
+                if not 0 <= p < k.shape[0]:
+                    continue
+                for codes, scales in ((k, ks), (v, vs)):
+                    x = rng.standard_normal(codes.shape[1::2]) * 2.0 ** rng.uniform(-spread, spread, (codes.shape[1], 1))
+                    codes[p, :, j % page], scales[p, :, j % page] = kv8.quantise(x)
+        self.upload()
+
+
+def _int(x):
+    return torch.tensor([int(i) for i in x], dtype=torch.int32, device=DEV)
+
+
+def _cu(counts):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(int)
+
+
+def _same(got, want):
+    for g, w in zip(got, want):
+        assert np.array_equal(g, w), f"{np.count_nonzero(g != w)} of {w.size} bytes differ"
+
+
+def _rows(rng, n, Hkv, D, dtype):
+    x = rng.standard_normal((n, Hkv, D)) * 2.0 ** rng.uniform(-6, 6, (n, Hkv, 1))
+    return torch.from_numpy(x).to(DT[dtype])
+
+
+# ------------------------------------------------------------------------ append ----
+@pytest.mark.parametrize("D,Hkv,page,counts,pasts,dtype", [
+    (64, 2, 16, [1], [0], "bf16"),
+    (64, 1, 16, [16, 17], [15, 0], "fp16"),
+    (96, 3, 48, [0, 33, 1, 0], [5, 40, 47, 0], "bf16"),
+    (128, 8, 32, [7, 70], [60, 0], "bf16"),
+    (128, 1, 64, [1, 0, 1, 1, 5], [63, 64, 65, 0, 127], "fp16"),
+    (256, 4, 16, [31, 2], [1, 16], "bf16"),
+    (96, 16, 16, [3, 3], [0, 29], "fp16"),
+])
+def test_append_packed(fa, D, Hkv, page, counts, pasts, dtype):
+    rng = np.random.default_rng(D + Hkv)
+    B, cu = len(counts), _cu(counts)
+    lens = [c + p for c, p in zip(counts, pasts)]
+    mp = -(-max(lens) // page) + 1
+    pool = Pool(B * mp + 2, Hkv, page, D, B, mp, seed=7)
+    extra = 3                                   # rows behind the last sequence: not written
+    k, v = _rows(rng, cu[-1] + extra, Hkv, D, dtype), _rows(rng, cu[-1] + extra, Hkv, D, dtype)
+    want = [a.copy() for a in pool.np]
+    kv8.append(want, k.double().numpy(), v.double().numpy(), pool.table_np, lens, cu)
+    fa.fa_kv_append_paged_fp8(k.to(DEV), v.to(DEV), *pool.args, _int(lens), cu_seqlens_new=_int(cu))
+    _same(pool.host(), want)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("n", [1, 3])
+def test_append_equal_counts_from_a_fused_projection(fa, D, n):
+    """[B, n, Hkv, D] slices of one [B, n, (Hq + 2 Hkv) D] buffer: strided tokens."""
+    rng = np.random.default_rng(n)
+    B, Hq, Hkv, page = 5, 4, 2, 16
+    lens = [n, n + 1, 15 + n, 16 + n, 40 + n]
+    pool = Pool(24, Hkv, page, D, B, 4, seed=8)
+    qkv = torch.from_numpy(rng.standard_normal((B, n, Hq + 2 * Hkv, D))).to(torch.bfloat16)
+    want = [a.copy() for a in pool.np]
+    flat = qkv.view(B * n, Hq + 2 * Hkv, D).double().numpy()
+    kv8.append(want, flat[:, Hq:Hq + Hkv], flat[:, Hq + Hkv:], pool.table_np, lens, _cu([n] * B))
+    dev = qkv.to(DEV)
+    fa.fa_kv_append_paged_fp8(dev[:, :, Hq:Hq + Hkv], dev[:, :, Hq + Hkv:], *pool.args, _int(lens))
+    _same(pool.host(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_edge_values(fa, dtype):
+    """Rows at the border of a scale (448 2^e and its neighbours), zeros, subnormals, the
+    type's largest values, infinities and NaN among and instead of finite ones."""
+    D, dt = 64, DT[dtype]
+    big = torch.finfo(dt).max
+    tops = [448.0, 7.0, 0.875 * 2.0 ** -10, 448 * 2.0 ** 4, 1.0, 1.75, 0.0, float(torch.finfo(dt).tiny), big]
+    rows = []
+    for top in tops:
+        t = torch.tensor(top).to(dt)
+        for a in (t, torch.nextafter(t, torch.tensor(0.0, dtype=dt)), torch.nextafter(t, torch.tensor(big, dtype=dt))):
+            row = torch.linspace(-1, 1, D).to(dt) * a * 0.99
+            row[7] = -a
+            rows.append(row)
+    sub = torch.tensor(float(torch.finfo(dt).smallest_normal)).to(dt) * torch.linspace(0, 1, D).to(dt)
+    rows += [sub, torch.zeros(D, dtype=dt), -torch.zeros(D, dtype=dt)]
+    for bad in (math.inf, -math.inf, math.nan):
+        mixed = torch.linspace(-3, 3, D).to(dt)
+        mixed[11] = bad
+        rows += [mixed, torch.full((D,), bad, dtype=dt)]
+    x = torch.stack(rows)[:, None]
+    n = len(rows)
+    mp = -(-n // 16)
+    pool = Pool(mp + 1, 1, 16, D, 1, mp, seed=9)
+    want = [a.copy() for a in pool.np]
+    kv8.append(want, x.double().numpy(), -x.double().numpy(), pool.table_np, [n], [0, n])
+    fa.fa_kv_append_paged_fp8(x.to(DEV), -x.to(DEV), *pool.args, _int([n]), cu_seqlens_new=_int([0, n]))
+    _same(pool.host(), want)
+
+
+def test_append_drops_rows_without_a_place(fa):
+    """Keys before 0, behind the table's capacity, on pages outside the pool: nothing of the
+    pool changes but the rows that have a place."""
+    rng = np.random.default_rng(2)
+    Hkv, page, D = 2, 16, 128
+    pool = Pool(9, Hkv, page, D, 5, 1, seed=10)
+    pool.table_np[2, 0], pool.table_np[3, 0] = -5, 9
+    pool.upload()
+    counts, lens = [4, 6, 5, 3, 2], [2, 20, 5, 3, -7]
+    cu = _cu(counts)
+    k, v = _rows(rng, cu[-1], Hkv, D, "bf16"), _rows(rng, cu[-1], Hkv, D, "bf16")
+    want = [a.copy() for a in pool.np]
+    kv8.append(want, k.double().numpy(), v.double().numpy(), pool.table_np, lens, cu)
+    assert not np.array_equal(want[0], pool.np[0])
+    fa.fa_kv_append_paged_fp8(k.to(DEV), v.to(DEV), *pool.args, _int(lens), cu_seqlens_new=_int(cu))
+    _same(pool.host(), want)
+
+
+def test_append_of_nothing(fa):
+    pool = Pool(3, 2, 16, 64, 2, 1)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    fa.fa_kv_append_paged_fp8(none, none, *pool.args, _int([5, 5]), cu_seqlens_new=_int([0, 0, 0]))
+    none = torch.empty(2, 0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    fa.fa_kv_append_paged_fp8(none, none, *pool.args, _int([5, 5]))
+    _same(pool.host(), pool.np)
+
+
+def test_append_many_sequences(fa):
+    """1024 sequences (the most), most of them with no new token."""
+    rng = np.random.default_rng(4)
+    B, Hkv, page, D = 1024, 1, 16, 64
+    counts = rng.integers(0, 3, B) * (rng.random(B) < 0.3)
+    lens = counts + rng.integers(0, 30, B)
+    cu = _cu(counts)
+    pool = Pool(2 * B, Hkv, page, D, B, 2, seed=11)
+    k, v = _rows(rng, cu[-1], Hkv, D, "bf16"), _rows(rng, cu[-1], Hkv, D, "bf16")
+    want = [a.copy() for a in pool.np]
+    kv8.append(want, k.double().numpy(), v.double().numpy(), pool.table_np, lens, cu)
+    fa.fa_kv_append_paged_fp8(k.to(DEV), v.to(DEV), *pool.args, _int(lens), cu_seqlens_new=_int(cu))
+    _same(pool.host(), want)
+
+
+# -------------------------------------------------------------------------- read ----
+@pytest.mark.parametrize("D,Hkv,page,counts,starts,dtype", [
+    (64, 2, 16, [1], None, "bf16"),
+    (64, 1, 16, [0, 33, 16, 0], [3, 5, 16, 0], "fp16"),
+    (96, 3, 48, [50, 1], [47, 0], "bf16"),
+    (128, 8, 32, [7, 70], None, "bf16"),
+    (256, 4, 16, [31, 2], [1, 16], "fp16"),
+])
+def test_read(fa, D, Hkv, page, counts, starts, dtype):
+    rng = np.random.default_rng(D)
+    B, cu = len(counts), _cu(counts)
+    first = starts or [0] * B
+    ends = [c + s for c, s in zip(counts, first)]
+    mp = -(-max(ends) // page) + 1
+    pool = Pool(B * mp + 1, Hkv, page, D, B, mp, seed=12)
+    pool.fill(rng, ends, spread=20)             # past fp16's range at both ends
+    extra = 2
+    dt = DT[dtype]
+    k, v = (torch.full((cu[-1] + extra, Hkv, D), 7.0, dtype=dt, device=DEV) for _ in range(2))
+    out = fa.fa_kv_read_paged_fp8(*pool.args, _int(cu), kv_starts=None if starts is None else _int(starts), k_out=k,
+                                  v_out=v)
+    assert out[0] is k and out[1] is v
+    for got, codes, scales in ((k, pool.np[0], pool.np[2]), (v, pool.np[1], pool.np[3])):
+        want = np.concatenate([kv8.cached(codes, scales, pool.table_np, b, first[b], counts[b]) for b in range(B)])
+        want = torch.from_numpy(want).float().to(dt)       # 4 significant bits: exact in fp32, rounded once
+        assert torch.equal(got[:cu[-1]].cpu().view(torch.int16), want.view(torch.int16))
+        assert (got[cu[-1]:] == 7).all()
+
+
+def test_read_every_code_and_scale(fa):
+    """All 256 codes at all 256 scale bytes, NaN codes, infinite results and byte 255 included."""
+    pool = Pool(32, 1, 16, 256, 1, 32)
+    pool.np[0][:] = pool.np[1][:] = np.arange(256, dtype=np.uint8)
+    pool.table_np[0] = np.arange(32)
+    pool.np[2][:, 0] = np.minimum(np.arange(512), 255).reshape(32, 16)
+    pool.np[3][:] = pool.np[2]
+    pool.upload()
+    for dt in (torch.bfloat16, torch.float16):
+        k, v = fa.fa_kv_read_paged_fp8(*pool.args, _int([0, 255]), total=255, dtype=dt)
+        want = torch.from_numpy(kv8.values(pool.np[0], pool.np[2]).reshape(512, 1, 256)[:255]).float().to(dt)
+        for got in (k, v):
+            assert torch.equal(got.cpu().isnan(), want.isnan())
+            assert torch.equal(got.cpu().nan_to_num(0).view(torch.int16), want.nan_to_num(0).view(torch.int16))
+
+
+def test_read_zeros_where_there_is_no_page(fa):
+    rng = np.random.default_rng(6)
+    pool = Pool(7, 2, 16, 64, 3, 2, seed=13)
+    pool.table_np[0, 1], pool.table_np[1, 0] = 7, -2147483648
+    pool.fill(rng, [32, 32, 32])
+    counts, starts = [32, 20, 30], [0, 4, 20]   # the last runs past the table's capacity
+    cu = _cu(counts)
+    k, v = fa.fa_kv_read_paged_fp8(*pool.args, _int(cu), kv_starts=_int(starts), total=int(cu[-1]))
+    want = np.concatenate([kv8.cached(pool.np[0], pool.np[2], pool.table_np, b, starts[b], counts[b]) for b in range(3)])
+    assert np.array_equal(k.double().cpu().numpy(), want)
+    assert (want[16:32] == 0).all() and (want[32:44] == 0).all() and (want[-18:] == 0).all()
+    k, _ = fa.fa_kv_read_paged_fp8(*pool.args, _int(cu), kv_starts=_int([-40, -2147483648, 2147483647]), total=int(cu[-1]))
+    assert (k == 0).all()
+
+
+# ------------------------------------------------------------------------ decode ----
+def _check(o, lse, ref, n, D, dtype):
+    o_ref, lse_ref, o_abs, s_abs = ref
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    e_s = (D + 8) * 2.0 ** -22 * s_abs                                     # [B, Hq, Sq]
+    sums = 2.0 ** -21 + (n / 4 + 64) * 2.0 ** -23
+    c = np.transpose(2.0 ** -11 + 2 * e_s + sums, (0, 2, 1))[..., None]
+    step = float(torch.finfo(DT[dtype]).smallest_normal) * float(torch.finfo(DT[dtype]).eps)
+    bound = U_O[dtype] * np.abs(o_ref) + c * o_abs + step / 2
+    assert np.isfinite(o).all()
+    off = np.abs(o - o_ref)
+    assert (off <= bound).all(), f"|dO| {off.max():.3e}, {np.max(off / bound):.2f} of its bound"
+    fin = np.isfinite(lse_ref)
+    assert np.array_equal(fin, np.isfinite(lse)) and (lse[~fin] == -np.inf).all()
+    e_s, lse, lse_ref = e_s[fin], lse[fin], lse_ref[fin]
+    assert (np.abs(lse - lse_ref) <= e_s + sums + 2.0 ** -22 * np.abs(lse_ref)).all()
+
+
+def _decode_case(fa, D, Hq, Hkv, Sq, page, lens, dtype="bf16", causal=True, ns=0, seed=0, qscale=1.0, spread=3, table=None,
+                 fill=None):
+    rng = np.random.default_rng(seed + D + Hq)
+    B = len(lens)
+    mp = max(1, -(-max(lens) // page)) + 1
+    pool = Pool(B * mp + 3, Hkv, page, D, B, mp, seed=seed)
+    if table:
+        table(pool.table_np)
+    pool.fill(rng, lens, spread)
+    if fill:
+        fill(pool)
+    q = torch.from_numpy(rng.standard_normal((B, Sq, Hq, D)) * qscale).to(DT[dtype])
+    o, lse = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int(lens), causal=causal, num_splits=ns)
+    ref = kv8.decode(q.double().numpy(), pool.np, pool.table_np, lens, 1 / math.sqrt(D), causal)
+    _check(o, lse, ref, max(lens), D, dtype)
+    return pool, q, o, lse
+
+
+HEAD_DIMS = [64, 96, 128, 256]
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("ns", [0, 1, 3])
+def test_decode_lengths(fa, D, ns):
+    """Lengths around the pages, the 16-key runs and the 128-key tiles; empty and single keys;
+    everything behind them is random bytes."""
+    _decode_case(fa, D, 4, 2, 1, 16, [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 257, 300], ns=ns)
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("group,Sq,Hkv", [(1, 1, 3), (8, 1, 2), (9, 1, 1), (16, 1, 2), (1, 16, 2), (4, 4, 2), (3, 5, 1),
+                                          (2, 7, 5)])
+def test_decode_columns(fa, D, group, Sq, Hkv):
+    """1..16 query rows a kv head, of heads and of tokens; causal rows that see no key."""
+    _decode_case(fa, D, group * Hkv, Hkv, Sq, 32, [200, 3, 77, 0, 1], seed=group)
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+def test_decode_without_the_mask(fa, D):
+    _decode_case(fa, D, 4, 2, 4, 48, [2, 130, 0, 49], causal=False)
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("page", [16, 80, 512])
+def test_decode_split_long(fa, D, dtype, page):
+    """Pairs cut into many pieces beside short ones."""
+    _decode_case(fa, D, 6, 2, 1, page, [2111, 40, 700], dtype=dtype, ns=64)
+
+
+def test_decode_one_sequence_many_pieces(fa):
+    _decode_case(fa, 128, 8, 1, 2, 16, [6001], ns=400)
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+def test_decode_wide_scales(fa, D):
+    """Rows whose magnitudes are 2^-20 .. 2^20: a probability's weight is that of its value too."""
+    _decode_case(fa, D, 4, 2, 1, 16, [150, 400], spread=20, qscale=2.0 ** -18)
+
+
+def test_decode_large_scores(fa):
+    """Scores in the hundreds: one key takes all; queries past fp16's range."""
+    _decode_case(fa, 64, 4, 2, 1, 16, [333, 64], qscale=40.0)
+    _decode_case(fa, 64, 4, 2, 1, 16, [333, 64], qscale=2.0 ** 20, spread=0)
+    _decode_case(fa, 64, 4, 2, 1, 16, [333, 64], qscale=2.0 ** -100, spread=0)
+
+
+def test_decode_rising_scores(fa):
+    """Every key scores higher than the one before: the running maximum moves all the time."""
+    def fill(pool):
+        k = pool.np[0]
+        page = k.shape[2]
+        for j in range(500):
+            p = pool.table_np[0, j // page]
+            k[p, :, j % page], pool.np[2][p, :, j % page] = kv8.quantise(np.full((k.shape[1], k.shape[3]), 0.02 * (j + 1)))
+        pool.upload()
+    for q in (2.0, -2.0):
+        _decode_case(fa, 128, 2, 1, 1, 16, [500], fill=fill, qscale=q)
+
+
+def test_decode_pages_outside_the_pool_are_zero_rows(fa):
+    def table(t):
+        t[0, 1], t[0, 3], t[1, 0], t[2, :] = -1, 2147483647, 10 ** 6, -2147483648
+    _decode_case(fa, 128, 4, 2, 1, 16, [100, 40, 30], table=table)
+
+
+def test_decode_shared_pages(fa):
+    """Two sequences with a common prefix on the same pages; a page twice in one sequence."""
+    def table(t):
+        t[1, :4] = t[0, :4]
+        t[2, 1] = t[2, 0]
+    _decode_case(fa, 64, 4, 2, 1, 16, [90, 77, 32], table=table)
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+def test_decode_nan_key_reaches_its_rows_only(fa, D):
+    """A NaN code of a visible key makes that kv head's rows NaN and no others."""
+    pool, q, o, lse = _decode_case(fa, D, 4, 2, 1, 16, [200, 150], seed=3)
+    p = pool.table_np[0, 3]
+    pool.np[0][p, 1, 5, 17] = 0x7F
+    pool.upload()
+    o2, lse2 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([200, 150]))
+    assert o2[0, 0, 2:].isnan().all() and lse2[0, 2:].isnan().all()
+    assert torch.equal(o2[0, 0, :2], o[0, 0, :2]) and torch.equal(o2[1], o[1])
+    pool.np[0][p, 1, 5, 17] = 0
+    pool.np[1][p, 1, 5, 17] = 0xFF                # a NaN value: that dimension alone
+    pool.upload()
+    o3, lse3 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([200, 150]))
+    assert o3[0, 0, 2:, 17].isnan().all() and o3[0].isnan().sum() == 2 and lse3.isfinite().all()
+
+
+def test_decode_clamps_lengths_and_takes_all_empty(fa):
+    pool, q, o, lse = _decode_case(fa, 128, 4, 2, 1, 16, [64, 64], seed=4)
+    # max_pages is one more than needed: fill it too, then ask for more keys than there are
+    pool.fill(np.random.default_rng(1), [80, 80])
+    o1, l1 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([80, 80]))
+    o2, l2 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([2 ** 31 - 1, 81]))
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    o3, l3 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([-5, 0]))
+    assert (o3 == 0).all() and (l3 == -math.inf).all()
+
+
+def test_decode_many_sequences(fa):
+    """1024 sequences, many of them empty."""
+    rng = np.random.default_rng(8)
+    lens = (rng.integers(0, 40, 1024) * (rng.random(1024) < 0.5)).tolist()
+    _decode_case(fa, 64, 2, 1, 1, 16, lens)
+
+
+def test_decode_contiguous_cache_is_one_page_each(fa):
+    """page_size = the whole capacity and an identity table: the same bits as small pages."""
+    pool, q, o, lse = _decode_case(fa, 96, 4, 2, 2, 16, [300, 222], ns=5)
+    B, mp = pool.table_np.shape
+    big = [np.ascontiguousarray(np.moveaxis(a[pool.table_np], 2, 1).reshape(B, a.shape[1], mp * 16, *a.shape[3:]))
+           for a in pool.np]
+    t = [torch.from_numpy(a).to(DEV) for a in big]
+    table = _int(range(B)).view(B, 1)
+    o2, lse2 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), t[0].view(torch.float8_e4m3fn), t[1].view(torch.float8_e4m3fn),
+                                              t[2], t[3], table, _int([300, 222]), num_splits=5)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_guard_bands_and_no_lse(fa):
+    """Writes stay inside O, LSE and the workspace; LSE may be absent at the C entry."""
+    B, Hq, Hkv, D, Sq, ns, pad = 3, 8, 2, 96, 2, 7, 4096
+    lens = [900, 0, 129]
+    pool, q, o_ref, lse_ref = _decode_case(fa, D, Hq, Hkv, Sq, 16, lens, ns=ns)
+    need = fa.fa_decode_workspace_bytes(B * Sq, Hq, D, ns)
+    ob = torch.full((2 * pad + q.numel(),), 7.0, dtype=torch.bfloat16, device=DEV)
+    lb = torch.full((2 * pad + B * Hq * Sq,), 7.0, device=DEV)
+    wb = torch.full((2 * pad + need,), 0xA5, dtype=torch.uint8, device=DEV)
+    o, lse = ob[pad:-pad].view(B, Sq, Hq, D), lb[pad:-pad].view(B, Hq, Sq)
+    fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int(lens), num_splits=ns, workspace=wb[pad:-pad], out=o, lse=lse)
+    assert torch.equal(o, o_ref) and torch.equal(lse, lse_ref)
+    for buf, fill in ((ob, 7.0), (lb, 7.0), (wb, 0xA5)):
+        assert (buf[:pad] == fill).all() and (buf[-pad:] == fill).all()
+    from exact_tiled_attention_20_gb300 import _lib
+
+    o.zero_()
+    qd, kl = q.to(DEV), _int(lens)
+    num_pages, _, page, _ = pool.k.shape
+    st = _lib._load_fp8().fa_decode_splitkv_paged_fp8(
+        qd.data_ptr(), pool.k.data_ptr(), pool.v.data_ptr(), pool.ks.data_ptr(), pool.vs.data_ptr(), pool.table.data_ptr(),
+        kl.data_ptr(), o.data_ptr(), None, B, Sq, Hq, Hkv, D, num_pages, page, pool.table.shape[1], 1 / math.sqrt(D), 1,
+        ns, wb[pad:].data_ptr(), need, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(o, o_ref)
+
+
+@pytest.mark.parametrize("D", HEAD_DIMS)
+def test_decode_is_deterministic_and_independent_of_the_split(fa, D):
+    pool, q, o, lse = _decode_case(fa, D, 8, 2, 1, 16, [1500, 200, 801], ns=1, seed=5)
+    for ns in (2, 5, 64):
+        a = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([1500, 200, 801]), num_splits=ns)
+        b = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int([1500, 200, 801]), num_splits=ns)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        # 2 u_o: both sides are rounded; 2^-10: P's roundings on both sides
+        assert ((a[0] - o).float().abs() <= 2.0 ** -7 * o.float().abs() + 2.0 ** -6 * 1.0).all()
+        assert ((a[1] - lse).abs() <= 1e-4).all()
+
+
+# -------------------------------------------------------------- used as a program ----
+def test_prompt_then_steps(fa):
+    """A chunked prefill and decode steps as a serving loop runs them: each chunk is appended,
+    the prefix is read back for fa_fwd_varlen, then single tokens are appended and decoded.
+    The decode's last step agrees with fa_fwd_varlen over the rows read back."""
+    rng = np.random.default_rng(9)
+    B, Hq, Hkv, D, page, mp = 3, 8, 2, 128, 32, 8
+    pool = Pool(B * mp, Hkv, page, D, B, mp, seed=14)
+    ref = [a.copy() for a in pool.np]
+    lens = np.zeros(B, int)
+    for counts in ([50, 0, 129], [33, 7, 64], [1, 1, 1], [1, 1, 1]):
+        cu = _cu(counts)
+        lens = lens + counts
+        k, v = _rows(rng, cu[-1], Hkv, D, "bf16") / 8, _rows(rng, cu[-1], Hkv, D, "bf16")
+        kv8.append(ref, k.double().numpy(), v.double().numpy(), pool.table_np, lens, cu)
+        step = counts[0] == 1
+        if step:
+            fa.fa_kv_append_paged_fp8(k.view(B, 1, Hkv, D).to(DEV), v.view(B, 1, Hkv, D).to(DEV), *pool.args, _int(lens))
+        else:
+            fa.fa_kv_append_paged_fp8(k.to(DEV), v.to(DEV), *pool.args, _int(lens), cu_seqlens_new=_int(cu))
+        q = torch.from_numpy(rng.standard_normal((cu[-1], Hq, D))).to(torch.bfloat16).to(DEV)
+        cu_k = _cu(lens)
+        kr, vr = fa.fa_kv_read_paged_fp8(*pool.args, _int(cu_k), total=int(cu_k[-1]))
+        o, lse = fa.fa_fwd_varlen(q, kr, vr, _int(cu), _int(cu_k), causal=True)
+        if step:
+            od, ld = fa.fa_decode_splitkv_paged_fp8(q.view(B, 1, Hq, D), *pool.args, _int(lens))
+            want = kv8.decode(q.view(B, 1, Hq, D).double().cpu().numpy(), ref, pool.table_np, lens, 1 / math.sqrt(D))
+            _check(od, ld, want, int(max(lens)), D, "bf16")
+            # fa_fwd_varlen rounds P to bf16 as well: 2^-8 of A beside both outputs' roundings
+            bound = 2.0 ** -7 * np.abs(want[0]) + 2.0 ** -7 * want[2]
+            assert (np.abs(od.double().cpu().numpy()[:, 0] - o.double().cpu().numpy()) <= bound[:, 0]).all()
+            assert ((ld[:, :, 0].T - lse).abs() <= 1e-3).all()
+    _same(pool.host(), ref)
+
+
+def test_captured_step_replays_with_new_lengths(fa):
+    """Append and decode captured into one graph; replays follow kv_lens and the new rows."""
+    rng = np.random.default_rng(10)
+    B, Hq, Hkv, D, page, mp = 4, 8, 2, 64, 16, 6
+    pool = Pool(B * mp, Hkv, page, D, B, mp, seed=15)
+    lens0 = [20, 0, 47, 80]
+    pool.fill(rng, lens0)
+    ref = [a.copy() for a in pool.np]
+    k, v, q = (torch.zeros(B, 1, h, D, dtype=torch.bfloat16, device=DEV) for h in (Hkv, Hkv, Hq))
+    kl = _int(lens0)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(B, Hq, D, 8), dtype=torch.uint8, device=DEV)
+    o, lse = torch.empty_like(q), torch.empty(B, Hq, 1, device=DEV)
+
+    def step():
+        kl.add_(1)
+        fa.fa_kv_append_paged_fp8(k, v, *pool.args, kl)
+        fa.fa_decode_splitkv_paged_fp8(q, *pool.args, kl, num_splits=8, workspace=ws, out=o, lse=lse)
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    lens = np.array(lens0)
+    for _ in range(5):
+        for t, h in ((k, Hkv), (v, Hkv), (q, Hq)):
+            t.copy_(torch.from_numpy(rng.standard_normal((B, 1, h, D))).to(torch.bfloat16))
+        graph.replay()
+        lens = lens + 1
+        kv8.append(ref, k.view(B, Hkv, D).double().cpu().numpy(), v.view(B, Hkv, D).double().cpu().numpy(),
+                   pool.table_np, lens, _cu([1] * B))
+        _check(o, lse, kv8.decode(q.double().cpu().numpy(), ref, pool.table_np, lens, 1 / math.sqrt(D)), int(max(lens)), D,
+               "bf16")
+    _same(pool.host(), ref)
+
+
+def test_two_streams_at_once(fa):
+    """Two decodes with a workspace each on two streams give what each gives alone."""
+    pool, q, o, lse = _decode_case(fa, 128, 8, 2, 1, 16, [1800, 900], ns=16, seed=6)
+    qd, kl = q.to(DEV), _int([1800, 900])
+    q2 = -qd
+    alone = fa.fa_decode_splitkv_paged_fp8(q2, *pool.args, kl, num_splits=16)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s, x in zip(streams, (qd, q2)):
+            got.append(fa.fa_decode_splitkv_paged_fp8(x, *pool.args, kl, num_splits=16, stream=s))
+    torch.cuda.synchronize()
+    for i, (oo, ll) in enumerate(got):
+        assert torch.equal(oo, (o, alone[0])[i % 2]) and torch.equal(ll, (lse, alone[1])[i % 2])
+
+
+def test_offsets_past_32_bits(fa):
+    """A pool of more than 2^32 bytes of codes: the last pages are written, read and decoded."""
+    Hkv, page, D, B = 8, 64, 128, 2
+    pages = (1 << 32) // (Hkv * page * D) + 40
+    k = torch.empty(pages, Hkv, page, D, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    v = torch.empty(pages, Hkv, page, D, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    ks, vs = (torch.empty(pages, Hkv, page, dtype=torch.uint8, device=DEV) for _ in range(2))
+    high = torch.arange(pages - 6, pages, dtype=torch.int32, device=DEV).view(B, 3)
+    low = torch.arange(6, dtype=torch.int32, device=DEV).view(B, 3)
+    g = torch.Generator(DEV).manual_seed(3)
+    kn, vn = (torch.randn(B, 150, Hkv, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(B, 1, 32, D, generator=g, device=DEV).to(torch.bfloat16)
+    kl = _int([150, 150])
+    outs = []
+    for table in (low, high):
+        fa.fa_kv_append_paged_fp8(kn, vn, k, v, ks, vs, table, kl)
+        outs.append((*fa.fa_kv_read_paged_fp8(k, v, ks, vs, table, _int([0, 150, 300]), total=300),
+                     *fa.fa_decode_splitkv_paged_fp8(q, k, v, ks, vs, table, kl, num_splits=3)))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    off = (outs[1][0].view(B, 150, Hkv, D) - kn).float().abs()
+    assert (off <= kn.float().abs() * 2.0 ** -4 + 2.0 ** -16).all()
+
+
+# ---------------------------------------------------------------------- refusals ----
+def test_binding_refuses(fa):
+    pool = Pool(8, 2, 16, 64, 2, 2)
+    kl, cu = _int([5, 5]), _int([0, 1, 2])
+    x = torch.zeros(2, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    k, v, ks, vs, t = pool.args
+    app, dec, rd = fa.fa_kv_append_paged_fp8, fa.fa_decode_splitkv_paged_fp8, fa.fa_kv_read_paged_fp8
+    for bad in ((k.view(torch.uint8), v, ks, vs, t), (k, v[:7], ks, vs, t), (k, v, ks[:, :, :8], vs, t),
+                (k, v, ks.int(), vs, t), (k, v, ks, vs, t.long()), (k, v, ks, vs, t[0]), (k.transpose(1, 2), v, ks, vs, t),
+                (k[0], v[0], ks, vs, t), (k.cpu(), v, ks, vs, t), (k, v, ks, vs, t.cpu())):
+        for call in (lambda: app(x, x, *bad, kl), lambda: dec(q, *bad, kl), lambda: rd(*bad, cu, total=2)):
+            with pytest.raises((TypeError, ValueError)):
+                call()
+    for call in (lambda: app(x.float(), x.float(), *pool.args, kl), lambda: app(x, x.half(), *pool.args, kl),
+                 lambda: app(x[:1], x[:1], *pool.args, kl), lambda: app(x[:, 0], x[:, 0], *pool.args, kl),
+                 lambda: app(x, x, *pool.args, kl, cu_seqlens_new=cu), lambda: app(x, x, *pool.args, kl.long()),
+                 lambda: app(x[:, 0], x[:, 0], *pool.args, kl, cu_seqlens_new=cu[:2]),
+                 lambda: app(x[..., :32], x[..., :32], *pool.args, kl),
+                 lambda: app(x.transpose(2, 3), x.transpose(2, 3), *pool.args, kl),
+                 lambda: app(x, x, *pool.args, kl[:1]),
+                 lambda: dec(q[:1], *pool.args, kl), lambda: dec(q[..., :32], *pool.args, kl),
+                 lambda: dec(q.float(), *pool.args, kl), lambda: dec(q[:, 0], *pool.args, kl),
+                 lambda: dec(q, *pool.args, kl, out=q[:, :, :2]), lambda: dec(q, *pool.args, kl, lse=torch.empty(2, 4, device=DEV)),
+                 lambda: dec(q, *pool.args, kl, workspace=torch.empty(4, device=DEV)),
+                 lambda: rd(*pool.args, cu), lambda: rd(*pool.args, cu, total=2, dtype=torch.float32),
+                 lambda: rd(*pool.args, cu, k_out=x[:, 0], v_out=x[:, 0].half()),
+                 lambda: rd(*pool.args, cu, total=3, k_out=x[:, 0], v_out=x[:, 0]),
+                 lambda: rd(*pool.args, cu[:2], total=2), lambda: rd(*pool.args, cu, total=2, kv_starts=kl[:1])):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    for call, status in ((lambda: dec(q, *pool.args, kl, num_splits=4, workspace=torch.empty(64, dtype=torch.uint8, device=DEV)), 3),
+                         (lambda: dec(torch.zeros(2, 9, 4, 64, dtype=torch.bfloat16, device=DEV), *pool.args, kl), 2),
+                         (lambda: dec(torch.zeros(2, 1, 3, 64, dtype=torch.bfloat16, device=DEV), *pool.args, kl), 1),
+                         (lambda: dec(q, *pool.args, kl, scale=math.nan), 1)):
+        with pytest.raises(fa.FaError) as e:
+            call()
+        assert e.value.status == status
+    strided = torch.zeros(2, 1, 2 * 64 + 4, dtype=torch.bfloat16, device=DEV)[..., :128].unflatten(-1, (2, 64))
+    with pytest.raises(fa.FaError) as e:          # a token stride that breaks the 16-byte alignment
+        app(strided, strided, *pool.args, kl)
+    assert e.value.status == 1
