@@ -18,7 +18,9 @@ fa_status check_pool(const void* k_pages, const void* v_pages, const void* k_sca
     if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
     if (D != 64 && D != 96 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;
     if (page_size % 16 != 0 || B > 1024) return FA_ERR_UNSUPPORTED;
-    if ((long long)page_size * max_pages > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    // The kernels count keys (a little past the last one) and the pool's 16-key runs in 32 bits.
+    if ((long long)page_size * max_pages > 0x7fffffffLL - 4095) return FA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * Hkv > 0x7fffffffLL / (page_size / 16)) return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 

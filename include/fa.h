@@ -242,7 +242,8 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void *q, const void *k_cache,
  *   block_table         device int32 [B, max_pages_per_seq]: key r of sequence b is slot
  *                       r % page_size of page block_table[b][r / page_size]
  * page_size is a multiple of 16; D in {64, 96, 128, 256}; B <= 1024;
- * page_size * max_pages_per_seq < 2^31; the pools and scales are 16-byte aligned.  Table
+ * page_size * max_pages_per_seq <= 2^31 - 4096; num_pages * Hkv * page_size / 16 < 2^31; the
+ * pools and scales are 16-byte aligned.  Table
  * entries outside [0, num_pages) that a call meets are the caller's error: nothing is read
  * or written outside the pool (what happens instead is said at each call).  A contiguous
  * cache of Smax keys per sequence is the pool with page_size = Smax and block_table[b][0]

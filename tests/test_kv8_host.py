@@ -31,7 +31,8 @@ POOL = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(ks=None), INVALI
         (dict(page=-16), INVALID), (dict(max_pages=0), INVALID), (dict(page=24), UNSUPPORTED),
         (dict(page=1), UNSUPPORTED), (dict(D=80), UNSUPPORTED), (dict(D=0), UNSUPPORTED), (dict(D=512), UNSUPPORTED),
         (dict(dtype=2), UNSUPPORTED), (dict(B=1026), UNSUPPORTED),
-        (dict(page=1 << 20, max_pages=1 << 11), UNSUPPORTED)]
+        (dict(page=1 << 20, max_pages=1 << 11), UNSUPPORTED),
+        (dict(page=16, max_pages=(1 << 27) - 1), UNSUPPORTED), (dict(num_pages=1 << 28), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("change,code", POOL + [
