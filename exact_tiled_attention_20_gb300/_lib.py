@@ -379,8 +379,11 @@ def fa_decode_splitkv_multi(q, k_cache, v_cache, kv_lens, causal: bool = True,
     return out, lse
 
 
-# ---- 8-bit paged KV cache.  These run once per layer and token, so the checks below are
-# written to cost little host time: one pass over the tensors, the signatures declared once.
+# ---- 8-bit paged KV cache.  A decode step runs these for every layer and token and its
+# kernels take a few microseconds, so a call asks for all it checks in one expression; only
+# where that fails does _refuse find out what to say.
+_F8, _U8, _I32, _F32 = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream
 _fp8_lib = None
 
 
@@ -400,44 +403,60 @@ def _load_fp8():
     return _fp8_lib
 
 
-def _check_on(name, t, dtype, device, shape=None):
-    """t: a contiguous tensor of this type (and shape) on `device`, a CUDA device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _refuse(*wanted):
+    """Raises for the first of (name, tensor, dtype, device index, shape or None) that is not
+    a contiguous CUDA tensor of that type and shape on that device."""
+    for name, t, dtype, device, shape in wanted:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise AssertionError("a check failed that finds nothing wrong")
 
 
-def _check_fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table):
-    """Checks the pool's tensors; returns (device, num_pages, Hkv, page_size, D, B, max_pages)."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("k_pages must be a tensor [num_pages, Hkv, page_size, D]")
-    device, shape = k_pages.device, k_pages.shape
-    _check_on("k_pages", k_pages, torch.float8_e4m3fn, device)
-    _check_on("v_pages", v_pages, torch.float8_e4m3fn, device, shape)
-    _check_on("k_scales", k_scales, torch.uint8, device, shape[:3])
-    _check_on("v_scales", v_scales, torch.uint8, device, shape[:3])
-    _check_on("block_table", block_table, torch.int32, device)
-    if block_table.dim() != 2:
+def _fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table):
+    """Checks the pool's tensors; returns (device index, num_pages, Hkv, page_size, D, B, max_pages)."""
+    for t in (k_pages, v_pages, k_scales, v_scales, block_table):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("the pool, its scales and block_table must be CUDA tensors")
+    device, shape, table = k_pages.get_device(), k_pages.shape, block_table.shape
+    if len(shape) != 4:
+        raise ValueError("k_pages must be [num_pages, Hkv, page_size, D]")
+    if len(table) != 2:
         raise ValueError("block_table must be [B, max_pages_per_seq]")
-    return (device, *shape, *block_table.shape)
+    rows = shape[:3]
+    if not (device >= 0 and v_pages.get_device() == device and k_scales.get_device() == device
+            and v_scales.get_device() == device and block_table.get_device() == device
+            and k_pages.dtype is _F8 and v_pages.dtype is _F8 and k_scales.dtype is _U8 and v_scales.dtype is _U8
+            and block_table.dtype is _I32 and v_pages.shape == shape and k_scales.shape == rows
+            and v_scales.shape == rows and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and k_scales.is_contiguous() and v_scales.is_contiguous() and block_table.is_contiguous()):
+        _refuse(("k_pages", k_pages, _F8, device, shape), ("v_pages", v_pages, _F8, device, shape),
+                ("k_scales", k_scales, _U8, device, rows), ("v_scales", v_scales, _U8, device, rows),
+                ("block_table", block_table, _I32, device, table))
+    return (device, *shape, *table)
+
+
+def _is(t, dtype, device, shape):
+    """Whether t is a contiguous tensor of this type and shape (None: any) on this device."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+            and (shape is None or t.shape == shape) and t.is_contiguous())
 
 
 def _stream_on(device, stream):
     """(handle of `stream` or of the device's current stream, the stream where it is not the
     current one)."""
-    current = torch.cuda.current_stream(device)
     if stream is None:
-        return current.cuda_stream, None
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, not on {device}")
-    return stream.cuda_stream, (None if stream == current else stream)
+        return _raw_stream(device), None
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, not on cuda:{device}")
+    return stream.cuda_stream, (None if stream.cuda_stream == _raw_stream(device) else stream)
 
 
 def _made(t, other):
@@ -449,8 +468,8 @@ def _made(t, other):
 
 
 def _call_on(device, fn, *args):
-    """Calls a C entry point with `device` current."""
-    if torch.cuda.current_device() == device.index:
+    """Calls a C entry point with the device of this index current."""
+    if torch._C._cuda_getDevice() == device:
         st = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -460,28 +479,29 @@ def _call_on(device, fn, *args):
 
 
 def _new_rows(name, t, dtype, device, Hkv, D):
-    """A tensor of new rows [..., Hkv, D] with dense rows: its tokens and their stride."""
+    """A tensor of new rows [..., Hkv, D] whose heads are dense: (its tokens, their stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    shape, strides = t.shape, t.stride()
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    shape = t.shape
     if len(shape) not in (3, 4) or shape[-2] != Hkv or shape[-1] != D:
         raise ValueError(f"{name} must be [B, n, {Hkv}, {D}] or [total, {Hkv}, {D}], got {tuple(shape)}")
-    if t.numel() == 0:
-        return 0, Hkv * D
+    tokens = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    if t.is_contiguous():
+        return tokens, Hkv * D
+    strides = t.stride()
     if strides[-1] != 1 or (Hkv > 1 and strides[-2] != D):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    if len(shape) == 3:
-        return shape[0], strides[0] if shape[0] > 1 else Hkv * D
-    B, n = shape[0], shape[1]
-    if n == 1:
-        return B, strides[0] if B > 1 else Hkv * D
-    if B > 1 and strides[0] != n * strides[1]:
+    if tokens <= 1:
+        return tokens, Hkv * D
+    if len(shape) == 3 or shape[1] == 1:
+        return tokens, strides[0]
+    if shape[0] > 1 and strides[0] != shape[1] * strides[1]:
         raise ValueError(f"{name}: the tokens of the batch must have one stride")
-    return B * n, strides[1]
+    return tokens, strides[1]
 
 
 def fa_kv_append_paged_fp8(k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens,
@@ -494,29 +514,31 @@ def fa_kv_append_paged_fp8(k_new, v_new, k_pages, v_pages, k_scales, v_scales, b
     [num_pages, Hkv, page_size, D], k_scales/v_scales uint8 [num_pages, Hkv, page_size],
     block_table int32 [B, max_pages_per_seq]; kv_lens int32 [B] counts the new tokens: they
     become the last keys of their sequences.  Writes the pool in place; returns None."""
-    lib = _load_fp8()
-    device, num_pages, Hkv, page, D, B, max_pages = _check_fp8_pool(k_pages, v_pages, k_scales, v_scales,
-                                                                    block_table)
-    if not isinstance(k_new, torch.Tensor) or k_new.dtype not in _DTYPE:
+    lib = _fp8_lib or _load_fp8()
+    device, num_pages, Hkv, page, D, B, max_pages = _fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table)
+    dtype = k_new.dtype if isinstance(k_new, torch.Tensor) else None
+    if dtype not in _DTYPE:
         raise TypeError("k_new/v_new must be bf16 or fp16 tensors")
-    total, k_stride = _new_rows("k_new", k_new, k_new.dtype, device, Hkv, D)
-    total_v, v_stride = _new_rows("v_new", v_new, k_new.dtype, device, Hkv, D)
-    if v_new.shape != k_new.shape:
+    total, k_stride = _new_rows("k_new", k_new, dtype, device, Hkv, D)
+    v_stride = _new_rows("v_new", v_new, dtype, device, Hkv, D)[1]
+    shape = k_new.shape
+    if v_new.shape != shape:
         raise ValueError("k_new and v_new must have one shape")
-    _check_on("kv_lens", kv_lens, torch.int32, device, (B,))
+    if not _is(kv_lens, _I32, device, (B,)):
+        _refuse(("kv_lens", kv_lens, _I32, device, (B,)))
     cu = None
     if cu_seqlens_new is not None:
-        _check_on("cu_seqlens_new", cu_seqlens_new, torch.int32, device, (B + 1,))
-        if k_new.dim() != 3:
+        if not _is(cu_seqlens_new, _I32, device, (B + 1,)):
+            _refuse(("cu_seqlens_new", cu_seqlens_new, _I32, device, (B + 1,)))
+        if len(shape) != 3:
             raise ValueError("with cu_seqlens_new, k_new and v_new are packed [total, Hkv, D]")
         cu = cu_seqlens_new.data_ptr()
-    elif k_new.dim() != 4 or k_new.shape[0] != B:
+    elif len(shape) != 4 or shape[0] != B:
         raise ValueError("without cu_seqlens_new, k_new and v_new are [B, n, Hkv, D]")
-    handle, _ = _stream_on(device, stream)
     _call_on(device, lib.fa_kv_append_paged_fp8, k_new.data_ptr(), v_new.data_ptr(), k_stride, v_stride, cu,
              block_table.data_ptr(), kv_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), B, total, Hkv, D, num_pages, page, max_pages,
-             _DTYPE[k_new.dtype], handle)
+             _DTYPE[dtype], _stream_on(device, stream)[0])
 
 
 def fa_kv_read_paged_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens, total=None,
@@ -527,12 +549,12 @@ def fa_kv_read_paged_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_s
     sequence b; cu_seqlens int32 [B+1], kv_starts int32 [B], on the device.  k_out/v_out
     [total, Hkv, D] are given, or made here from ``total`` and ``dtype``; rows behind the last
     sequence are not written.  Returns (k, v)."""
-    lib = _load_fp8()
-    device, num_pages, Hkv, page, D, B, max_pages = _check_fp8_pool(k_pages, v_pages, k_scales, v_scales,
-                                                                    block_table)
-    _check_on("cu_seqlens", cu_seqlens, torch.int32, device, (B + 1,))
-    if kv_starts is not None:
-        _check_on("kv_starts", kv_starts, torch.int32, device, (B,))
+    lib = _fp8_lib or _load_fp8()
+    device, num_pages, Hkv, page, D, B, max_pages = _fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table)
+    if not _is(cu_seqlens, _I32, device, (B + 1,)):
+        _refuse(("cu_seqlens", cu_seqlens, _I32, device, (B + 1,)))
+    if kv_starts is not None and not _is(kv_starts, _I32, device, (B,)):
+        _refuse(("kv_starts", kv_starts, _I32, device, (B,)))
     given = k_out if k_out is not None else v_out
     if given is not None:
         dtype = given.dtype
@@ -545,11 +567,11 @@ def fa_kv_read_paged_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_s
     handle, other = _stream_on(device, stream)
     shape = (int(total), Hkv, D)
     if k_out is None:
-        k_out = _made(torch.empty(shape, dtype=dtype, device=device), other)
+        k_out = _made(torch.empty(shape, dtype=dtype, device=k_pages.device), other)
     if v_out is None:
-        v_out = _made(torch.empty(shape, dtype=dtype, device=device), other)
-    _check_on("k_out", k_out, dtype, device, shape)
-    _check_on("v_out", v_out, dtype, device, shape)
+        v_out = _made(torch.empty(shape, dtype=dtype, device=k_pages.device), other)
+    if not (_is(k_out, dtype, device, shape) and _is(v_out, dtype, device, shape)):
+        _refuse(("k_out", k_out, dtype, device, shape), ("v_out", v_out, dtype, device, shape))
     _call_on(device, lib.fa_kv_read_paged_fp8, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
              v_scales.data_ptr(), block_table.data_ptr(), None if kv_starts is None else kv_starts.data_ptr(),
              cu_seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, shape[0], Hkv, D, num_pages, page,
@@ -566,16 +588,17 @@ def fa_decode_splitkv_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_t
     int32 [B].  workspace: a CUDA uint8 tensor of at least fa_decode_workspace_bytes(B * Sq,
     Hq, D, num_splits) bytes, or None to allocate one.  Returns (o like q, lse fp32
     [B, Hq, Sq])."""
-    lib = _load_fp8()
-    device, num_pages, Hkv, page, D, B, max_pages = _check_fp8_pool(k_pages, v_pages, k_scales, v_scales,
-                                                                    block_table)
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
+    lib = _fp8_lib or _load_fp8()
+    device, num_pages, Hkv, page, D, B, max_pages = _fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table)
+    dtype = q.dtype if isinstance(q, torch.Tensor) else None
+    if dtype not in _DTYPE:
         raise TypeError("q must be a bf16 or fp16 tensor")
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
-        raise ValueError(f"q must be [{B}, Sq, Hq, {D}], got {tuple(q.shape)}")
-    _check_on("q", q, q.dtype, device)
-    Sq, Hq = q.shape[1], q.shape[2]
-    _check_on("kv_lens", kv_lens, torch.int32, device, (B,))
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
+        raise ValueError(f"q must be [{B}, Sq, Hq, {D}], got {tuple(shape)}")
+    Sq, Hq = shape[1], shape[2]
+    if not (_is(q, dtype, device, shape) and _is(kv_lens, _I32, device, (B,))):
+        _refuse(("q", q, dtype, device, shape), ("kv_lens", kv_lens, _I32, device, (B,)))
     handle, other = _stream_on(device, stream)
     ns = int(num_splits)
     if workspace is None:
@@ -583,20 +606,20 @@ def fa_decode_splitkv_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_t
             with torch.cuda.device(device):
                 ns = lib.fa_decode_default_splits(B, Hkv, page * max_pages, 0)
         workspace = _made(torch.empty(max(16, lib.fa_decode_workspace_bytes(B * Sq, Hq, D, ns)),
-                                      dtype=torch.uint8, device=device), other)
-    else:
-        _check_on("workspace", workspace, torch.uint8, device)
+                                      dtype=_U8, device=q.device), other)
+    elif not _is(workspace, _U8, device, None):
+        _refuse(("workspace", workspace, _U8, device, None))
     if out is None:
         out = _made(torch.empty_like(q), other)
-    else:
-        _check_on("out", out, q.dtype, device, q.shape)
+    elif not _is(out, dtype, device, shape):
+        _refuse(("out", out, dtype, device, shape))
     if lse is None:
-        lse = _made(torch.empty((B, Hq, Sq), dtype=torch.float32, device=device), other)
-    else:
-        _check_on("lse", lse, torch.float32, device, (B, Hq, Sq))
+        lse = _made(torch.empty((B, Hq, Sq), dtype=_F32, device=q.device), other)
+    elif not _is(lse, _F32, device, (B, Hq, Sq)):
+        _refuse(("lse", lse, _F32, device, (B, Hq, Sq)))
     _call_on(device, lib.fa_decode_splitkv_paged_fp8, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
              k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
              out.data_ptr(), lse.data_ptr(), B, Sq, Hq, Hkv, D, num_pages, page, max_pages,
-             float(scale) if scale is not None else 1.0 / math.sqrt(D), int(bool(causal)), ns,
-             workspace.data_ptr(), workspace.numel(), _DTYPE[q.dtype], handle)
+             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, ns,
+             workspace.data_ptr(), workspace.numel(), _DTYPE[dtype], handle)
     return out, lse

@@ -639,16 +639,19 @@ fa_status launch_kv8_split(const Kv8DecParams& p, cudaStream_t s) {
     return launch_overlapped(kv8_split_kernel<D, NT, kBF16>, p.grid, kKv8Threads, bytes, s, p);
 }
 
-// Joins the pieces of each row (b, token, head): lse = log sum exp(lse_c), and the outputs
-// weighted with exp(lse_c - lse), in the order of the pieces.  One warp per row.
-template <int D, bool kBF16>
-__global__ void __launch_bounds__(128) kv8_merge_kernel(const Kv8DecParams p) {
-    constexpr int V = D / 32;
+// Joins the pieces of each row (b, token, head): lse = log sum_c exp(lse_c), and the outputs
+// weighted with exp(lse_c - lse).  WPR warps share a row, each taking every WPR-th piece; a
+// lane holds D / 32 dims.  It moves few bytes: its time is the launch and two or three
+// dependent trips to L2, so the pieces of a warp are loaded several at a time.
+template <int D, int WPR, bool kBF16>
+__global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
+    constexpr int V = D / 32, Rows = 8 / WPR, NB = V <= 4 ? 8 : 4;
+    __shared__ float s_acc[WPR > 1 ? 8 : 1][D], s_sum[8];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= p.B * p.Sq * p.Hq) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * Rows + warp / WPR, part = warp % WPR;
+    if (row >= p.B * p.Sq * p.Hq) return;  // whole CTAs where WPR = 8
     const int b = row / (p.Sq * p.Hq), tok = row / p.Hq % p.Sq, h = row % p.Hq;
     int before = 0, sum = 0, most = 0;
     for (int i = lane; i < p.B; i += 32) {
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(128) kv8_merge_kernel(const Kv8DecParams p) {
     const int tb = kv8_tiles(kv8_len(p, b));
     const int W = kv8_width(p, sum, most);
     const int n = kv8_pieces(p.pool.Hkv * before + h / p.group * tb, tb, W);
-    if (n < 2) return;  // the split kernel has written this row
+    if (n < 2) return;  // the split kernel has written this row (n is the same in all of a row's warps)
     const float kNegInf = -__int_as_float(0x7f800000);
     const float* lrow = p.lse_part + (size_t)row * p.ns;
     const float* orow = p.o_part + (size_t)row * p.ns * D + lane;
@@ -678,18 +681,55 @@ __global__ void __launch_bounds__(128) kv8_merge_kernel(const Kv8DecParams p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     if (m != kNegInf) {
-        for (int c = 0; c < n; ++c) {
-            const float w = ex2_approx((lrow[c] - m) / kLn2);
-            s += w;
+        for (int c0 = part; c0 < n; c0 += WPR * NB) {
+            float w[NB], v[NB][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += w * orow[(size_t)c * D + i * 32];
+            for (int u = 0; u < NB; ++u) {  // pieces past n: the last one, with weight 0
+                const int c = min(c0 + u * WPR, n - 1);
+                w[u] = c0 + u * WPR < n ? lrow[c] : kNegInf;
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[u][i] = orow[(size_t)c * D + i * 32];
+            }
+#pragma unroll
+            for (int u = 0; u < NB; ++u) {
+                const float f = ex2_approx((w[u] - m) * (1.f / kLn2));
+                s += f;
+                // a piece without a visible key has weight 0 and an output of 0; a weight of 0
+                // that pads the batch must not meet a NaN or an infinity
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(f, w[u] == kNegInf ? 0.f : v[u][i], acc[i]);
+            }
         }
     }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
+        if (lane == 0) s_sum[warp] = s;
+        __syncthreads();
+        if (warp != 0) return;
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+            s += s_sum[w];
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += s_acc[w][lane + i * 32];
+        }
+    }
+    const float inv = 1.f / s;
     uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane;
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i * 32] = float_to16<kBF16>(m == kNegInf ? 0.f : acc[i] / s);
+    for (int i = 0; i < V; ++i) out[i * 32] = float_to16<kBF16>(m == kNegInf ? 0.f : acc[i] * inv);
     if (p.lse && lane == 0)
         p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = m == kNegInf ? kNegInf : m + lg2_approx(s) * kLn2;
+}
+
+template <int D, int WPR>
+fa_status launch_kv8_merge(const Kv8DecParams& p, bool bf16, cudaStream_t s) {
+    const unsigned rows = (unsigned)(p.B * p.Sq * p.Hq), grid = (rows + 8 / WPR - 1) / (8 / WPR);
+    return bf16 ? launch_overlapped(kv8_merge_kernel<D, WPR, true>, grid, 256, 0, s, p)
+                : launch_overlapped(kv8_merge_kernel<D, WPR, false>, grid, 256, 0, s, p);
 }
 
 template <int D>
@@ -719,9 +759,9 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     else
         st = a.bf16 ? launch_kv8_split<D, 2, true>(p, s) : launch_kv8_split<D, 2, false>(p, s);
     if (st != FA_OK || p.ns < 2) return st;
-    const unsigned rows = (unsigned)(a.B * a.Sq * a.Hq);
-    return a.bf16 ? launch_overlapped(kv8_merge_kernel<D, true>, (rows + 3) / 4, 128, 0, s, p)
-                  : launch_overlapped(kv8_merge_kernel<D, false>, (rows + 3) / 4, 128, 0, s, p);
+    // Few rows are cut into many pieces: eight warps each.
+    return a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_kv8_merge<D, 8>(p, a.bf16, s)
+                                              : launch_kv8_merge<D, 1>(p, a.bf16, s);
 }
 
 }  // namespace fa
