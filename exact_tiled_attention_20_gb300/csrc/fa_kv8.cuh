@@ -63,9 +63,10 @@ struct Kv8DecodeArgs {
     const int32_t* kv_lens;
     int B, Sq, Hq, D;
     float scale;
-    int causal, num_splits;
-    float* o_part;    // [B, Sq, Hq, num_splits, D]
-    float* lse_part;  // [B, Sq, Hq, num_splits]
+    int causal;
+    long long slots;  // room in the workspace: partial results of one pair; 0: cut no pair
+    float* o_part;    // [slots, Hq / Hkv * Sq, D]
+    float* lse_part;  // [slots, Hq / Hkv * Sq]
     bool bf16;
     int num_sms;
 };

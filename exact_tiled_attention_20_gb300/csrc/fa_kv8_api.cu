@@ -97,22 +97,25 @@ fa_status fa_decode_splitkv_paged_fp8(const void* q, const void* k_pages, const 
     const fa_status chk =
         decode_check_args(q, k_pages, v_pages, kv_lens, o, lse, B, Sq, Hq, Hkv, D, capacity, scale, dtype);
     if (chk != FA_OK) return chk;
+    // The plan counts 64-key units, and one more for each (sequence, kv head) pair, in 32 bits.
+    if ((long long)B * Hkv > 0x7fffffffLL / (capacity / 64 + 2)) return FA_ERR_UNSUPPORTED;
     if ((long long)B * Sq * Hq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const int sms = device_sms();
     if (sms <= 0) return FA_ERR_CUDA;
+    const bool whole = num_splits == 1;
     if (num_splits <= 0) num_splits = fa_decode_default_splits(B, Hkv, capacity, sms);
-    if (num_splits > capacity) num_splits = capacity;
-    const size_t rows = (size_t)B * Sq * Hq * num_splits;
     const size_t need = fa_decode_workspace_bytes(B * Sq, Hq, D, num_splits);
-    if (num_splits > 1 && (!workspace || workspace_bytes < need || misaligned(workspace, 16)))
-        return FA_ERR_WORKSPACE;
+    if (!whole && (!workspace || workspace_bytes < need || misaligned(workspace, 16))) return FA_ERR_WORKSPACE;
+    // The workspace holds num_splits partial results of every pair: [slots, Hq / Hkv * Sq, D] and
+    // their log-sum-exps.
+    const size_t rows = (size_t)B * Sq * Hq * num_splits;
     float* o_part = static_cast<float*>(workspace);
     float* lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                                ((rows * D * sizeof(float) + 255) & ~size_t(255)));
     const Kv8DecodeArgs a{make_pool(k_pages, v_pages, k_scales, v_scales, block_table, Hkv, num_pages, page_size,
                                     max_pages_per_seq),
-                          q, o, lse, kv_lens, B, Sq, Hq, D, scale, causal, num_splits, o_part, lse_part,
-                          dtype == FA_BF16, sms};
+                          q, o, lse, kv_lens, B, Sq, Hq, D, scale, causal,
+                          whole ? 0 : (long long)B * Hkv * num_splits, o_part, lse_part, dtype == FA_BF16, sms};
     switch (D) {
         case 64: return launch_kv8_decode_d64(a, reinterpret_cast<cudaStream_t>(stream));
         case 96: return launch_kv8_decode_d96(a, reinterpret_cast<cudaStream_t>(stream));

@@ -5,12 +5,17 @@
 //                                                     j <= len_b - Sq + i
 //     o   = sum_j softmax(s)_j 2^(vs_j - 127) vcode_j,    lse = log sum_j exp(s_j)
 //
-// Plan: the keys of every (sequence, kv head) pair, in 128-key tiles, lie end to end in the
-// order (b, hk), and CTA c takes tiles [c W, (c + 1) W): every CTA streams the same number
-// of bytes whatever the mix of lengths.  W also keeps a pair within num_splits pieces.  A
-// pair that lies in one range is finished by its CTA; one that is cut leaves a partial
-// output and its log-sum-exp per piece, which the merge kernel joins.
+// Plan: the keys of every (sequence, kv head) pair, in units of 64 keys, lie end to end in
+// the order (b, hk), each pair led by kKv8Lead units that hold no keys and stand for what
+// starting and finishing a pair costs.  CTA c takes the range of units [c W, (c + 1) W):
+// every CTA gets the same work whatever the mix of lengths.  A pair whose keys lie in one
+// range is finished by its CTA.  One that is cut leaves a partial output and its log-sum-exp
+// in each range, which the merge kernel joins; a range meets at most two such pairs, one
+// that began before it and one that goes on behind it, so two slots a range hold them all.
+// Without room for that (`whole`), a CTA takes the pairs that begin in its range, uncut.
 #pragma once
+
+#include <algorithm>
 
 #include "fa_kv8.cuh"
 
@@ -22,37 +27,43 @@ struct Kv8DecParams {
     void* o;
     float* lse;
     const int32_t* kv_lens;
-    float* o_part;
-    float* lse_part;
-    int B, Sq, Hq, group, capacity, ns, causal;
-    int grid;  // CTAs of the split kernel
+    float* o_part;    // [2 grid, group * Sq, D]: slot 2 r, 2 r + 1 of range r
+    float* lse_part;  // [2 grid, group * Sq]
+    int B, Sq, Hq, group, capacity, causal, whole;
+    int grid;  // ranges, and CTAs of the split kernel
     float scale_log2;
 };
 
-constexpr int kKv8Tile = 128;  // keys per tile of the plan
+constexpr int kKv8Unit = 64;  // keys per unit of the plan
+constexpr int kKv8Lead = 4;   // units charged to each pair beside its keys
 constexpr int kKv8Threads = 128;
 constexpr int kKv8Warps = kKv8Threads / 32;
 constexpr int kKv8MaxB = 1024;
+constexpr int kTableLines = 8;  // lines of the block table that a CTA prefetches
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ int kv8_len(const Kv8DecParams& p, int b) {
     return min(max(p.kv_lens[b], 0), p.capacity);
 }
 
-__device__ __forceinline__ int kv8_tiles(int len) { return (len + kKv8Tile - 1) / kKv8Tile; }
-
-// W, from the tiles of one pair of each sequence summed, and the longest pair's.
-__device__ __forceinline__ int kv8_width(const Kv8DecParams& p, int sum_tiles, int max_tiles) {
-    const int total = p.pool.Hkv * sum_tiles;
-    int w = (int)(((long long)total + p.grid - 1) / p.grid);
-    w = max(w, p.ns >= 2 ? (max_tiles + p.ns - 2) / (p.ns - 1) : total);
-    return max(w, 1);
+// Units of one pair of a sequence.
+__device__ __forceinline__ int kv8_units(int len) {
+    return len > 0 ? (len + kKv8Unit - 1) / kKv8Unit + kKv8Lead : 0;
 }
 
-// Pieces of the pair whose tb tiles begin at tile `start`.
-__device__ __forceinline__ int kv8_pieces(int start, int tb, int w) {
-    return tb > 0 ? (start + tb - 1) / w - start / w + 1 : 0;
+// W, from the units of one pair of each sequence summed.
+__device__ __forceinline__ int kv8_width(const Kv8DecParams& p, int sum_units) {
+    return max((int)(((long long)p.pool.Hkv * sum_units + p.grid - 1) / p.grid), 1);
 }
+
+// The ranges that hold keys of the pair of `units` units beginning at unit `start`: the first
+// of them, and how many.
+__device__ __forceinline__ int kv8_first_piece(int start, int w) { return (start + kKv8Lead) / w; }
+__device__ __forceinline__ int kv8_pieces(int start, int units, int w) {
+    return units > 0 ? (start + units - 1) / w - kv8_first_piece(start, w) + 1 : 0;
+}
+// The slot of a pair's piece in range r, `first` of its pieces or not.
+__device__ __forceinline__ int kv8_slot(int r, bool first) { return 2 * r + (first ? 1 : 0); }
 
 template <bool kBF16>
 __device__ __forceinline__ uint16_t float_to16(float x) {
@@ -70,24 +81,28 @@ __device__ __forceinline__ float float_from16(uint16_t x) {
     }
 }
 
+// The plan in shared memory: the units of one pair of each sequence summed over the
+// sequences before b, and what the last unit of b lacks to be full, so that
+// len = (units - kKv8Lead) * kKv8Unit - pad.
 struct Kv8Plan {
-    int lens[kKv8MaxB];
-    int prefix[kKv8MaxB + 1];  // tiles of one pair of each sequence before b
-    int warp_sum[kKv8Warps], warp_max[kKv8Warps];
+    int* prefix;   // [B + 1]
+    uint8_t* pad;  // [B]
+    static __host__ __device__ constexpr int bytes(int B) { return (B + 1) * 4 + ((B + 15) & ~15); }
 };
 
 // Fills the plan from kv_lens (all threads; ends with a barrier) and returns W.
-__device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, Kv8Plan& t) {
+__device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Plan& t) {
+    __shared__ int warp_sum[kKv8Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.B + kKv8Threads - 1) / kKv8Threads;
-    int sum = 0, most = 0;
+    int sum = 0;
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
         if (b < p.B) {
-            const int len = kv8_len(p, b);
-            t.lens[b] = len;
-            sum += kv8_tiles(len);
-            most = max(most, kv8_tiles(len));
+            const int len = kv8_len(p, b), units = kv8_units(len);
+            t.prefix[b] = units;
+            t.pad[b] = (uint8_t)(len > 0 ? (units - kKv8Lead) * kKv8Unit - len : 0);
+            sum += units;
         }
     }
     int incl = sum;
@@ -95,52 +110,87 @@ __device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, Kv8Plan& t) 
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
-    if (lane == 31) {
-        t.warp_sum[warp] = incl;
-        t.warp_max[warp] = most;
-    }
+    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int run = incl - sum;
-    most = 0;
-    for (int w = 0; w < kKv8Warps; ++w) {
-        if (w < warp) run += t.warp_sum[w];
-        most = max(most, t.warp_max[w]);
-    }
+    for (int w = 0; w < warp; ++w) run += warp_sum[w];
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
         if (b < p.B) {
+            const int units = t.prefix[b];
             t.prefix[b] = run;
-            run += kv8_tiles(t.lens[b]);
+            run += units;
         }
     }
     if (threadIdx.x == kKv8Threads - 1) t.prefix[p.B] = run;
     __syncthreads();
-    return kv8_width(p, t.prefix[p.B], most);
+    return kv8_width(p, t.prefix[p.B]);
+}
+
+// The part of one pair that lies in one range.
+struct Kv8Seg {
+    int b, hk, len, k0, k1;  // keys k0 .. k1 - 1 of `len`
+    int slot;
+    bool cut;
+};
+
+// The next segment of range `rng` from unit x on (x advances past it); false where none is left.
+__device__ __forceinline__ bool kv8_next_segment(const Kv8DecParams& p, const Kv8Plan& t, int rng, int W, int& x,
+                                                 int x_end, Kv8Seg& s) {
+    const int Hkv = p.pool.Hkv;
+    while (x < x_end) {
+        int lo = 0, hi = p.B;  // largest b with Hkv * prefix[b] <= x: it has keys
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (Hkv * t.prefix[mid] <= x) lo = mid; else hi = mid;
+        }
+        const int first = Hkv * t.prefix[lo], units = t.prefix[lo + 1] - t.prefix[lo];
+        s.b = lo;
+        s.hk = (x - first) / units;
+        const int start = first + s.hk * units;
+        if (p.whole && x > start) {  // the range before has it
+            x = start + units;
+            continue;
+        }
+        const int end = p.whole ? start + units : min(x_end, start + units);
+        s.len = (units - kKv8Lead) * kKv8Unit - t.pad[lo];
+        s.k0 = max(x - start - kKv8Lead, 0) * kKv8Unit;
+        s.k1 = min((end - start - kKv8Lead) * kKv8Unit, s.len);
+        s.slot = kv8_slot(rng, rng == kv8_first_piece(start, W));
+        s.cut = !p.whole && kv8_pieces(start, units, W) > 1;
+        x = end;
+        if (s.k1 > s.k0) return true;  // else the range ends within the lead
+    }
+    return false;
 }
 
 // ------------------------------------------------------------------ shared layout ----
 // Each warp streams its own tiles of KT keys through a ring of NST stages in shared memory:
-// K codes, V codes, K scales, V scales.  A row is split into a part of WA bytes and, at
-// D = 96, one of 32; each part's rows lie in 128-byte lines whose 16-byte units are permuted
-// so that the reads below, K by (row g, unit t) and V by (row 2 t, unit g), meet no bank
-// twice.
-template <int D_>
+// K codes and V codes, and the scales of both beside the ring.  A row is split into a part of
+// WA bytes and, at D = 96, one of 32; each part's rows lie in 128-byte lines whose 16-byte
+// units are permuted so that the reads below, K by (row g, unit t) and V by (row 2 t, unit g),
+// meet no bank twice.
+template <int D_, int NT_>
 struct Kv8Cfg {
-    static constexpr int D = D_;
-    static constexpr int KT = D == 64 ? 64 : (D == 256 ? 16 : 32);
+    static constexpr int D = D_, NT = NT_;
+    static constexpr int KT = D == 64 || D == 256 ? (D == 64 ? 32 : 16) : 32;
+    static constexpr int NST = D == 64 ? 4 : D == 256 && NT == 1 ? 3 : 2;
+    static constexpr int CTAS = D == 256 || NT == 2 ? 2 : 3;  // resident on an SM
     static constexpr int NSUB = KT / 16;  // runs of 16 keys
-    static constexpr int NST = D == 96 ? 4 : 3;
     static constexpr int TileBytes = KT * D;
-    static constexpr int StageBytes = 2 * TileBytes + 128;
-    static constexpr int RingBytes = NST * StageBytes;
-    static constexpr int SmemBytes = kKv8Warps * RingBytes + 128;
+    static constexpr int RingBytes = NST * 2 * TileBytes;  // a warp's
+    static constexpr int ScaleBytes = NST * 2 * KT;
+    // Row of the exchange in floats: pair (block k, row g) of dims at 2 (8 k + g); a half-warp's
+    // 4 g and 4 t, two query rows apart, then lie in 32 different banks.
+    static constexpr int XD = D + 4;
+    static constexpr int ExchBytes = 2 * NT * 8 * XD * 4;      // two buffers
+    static constexpr bool QRegs = D / 16 * NT <= 16;           // query fragments in registers, else shared
+    static constexpr int QBytes = QRegs ? 0 : D / 16 * NT * 32 * 8;
+    static constexpr int FixedBytes = 128 + kKv8Warps * (RingBytes + ScaleBytes) + ExchBytes + QBytes;
     static constexpr int WA = D == 96 ? 64 : D;
     static constexpr int KS = D / 16;        // steps of 16 dims, and 16-dim blocks of O^T
     static constexpr int Copies = D / 32;    // 16-byte copies of a lane per run and tensor
-    static_assert(2 * KT <= 128, "scales of a stage");
-
     // Byte offset of 16-byte unit c of row `row` in a tile of codes.
     static __device__ __forceinline__ uint32_t unit(int row, int c) {
         if constexpr (WA == 64) {
@@ -223,110 +273,141 @@ constexpr float kLowest = -3.402823466e38f;
 
 // NT: blocks of 8 query rows (tokens x heads of one kv head; column token * group + head).
 template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecParams p) {
-    using C = Kv8Cfg<D>;
-    constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS;
-    constexpr bool kQRegs = KS * NT <= 16;  // query fragments in registers, else in shared memory
-    extern __shared__ uint8_t ring_raw[];
-    __shared__ Kv8Plan plan;
+__global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_kernel(const Kv8DecParams p) {
+    using C = Kv8Cfg<D, NT>;
+    constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS, XD = C::XD;
+    extern __shared__ uint8_t smem_raw[];
     __shared__ float s_mo[kKv8Warps][16], s_ms[kKv8Warps][16], s_l[kKv8Warps][16];
-    __shared__ uint2 s_q[kQRegs ? 1 : KS * NT][32];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int W = kv8_make_plan(p, plan);
+    __shared__ float s_f[16], s_finv[16], s_lse[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const float kNegInf = -__int_as_float(0x7f800000);
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 127u) & ~127u;
+    const uint32_t ring = base + warp * C::RingBytes;
+    const uint32_t scales = base + kKv8Warps * C::RingBytes + warp * C::ScaleBytes;
+    uint8_t* rest = smem_raw + (base - raw) + kKv8Warps * (C::RingBytes + C::ScaleBytes);
+    float* exch = reinterpret_cast<float*>(rest);
+    uint2* s_q = reinterpret_cast<uint2*>(rest + C::ExchBytes);
+    Kv8Plan plan;
+    plan.prefix = reinterpret_cast<int*>(rest + C::ExchBytes + C::QBytes);
+    plan.pad = reinterpret_cast<uint8_t*>(plan.prefix + p.B + 1);
+
+    grid_dependency_wait();
+    {
+        // The plan takes a trip to memory (kv_lens), and what it says to look up in the table would
+        // take another: the table's lines are sent for now, a few by each CTA.
+        const long long lines = ((long long)p.B * p.pool.max_pages + 31) / 32;
+        const long long line = (long long)blockIdx.x * kTableLines + tid;
+        if (tid < kTableLines && line < lines) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pool.table + line * 32));
+    }
+    const int W = kv8_make_plan(p, plan);
     uint16_t* o16 = static_cast<uint16_t*>(p.o);
     const uint16_t* q16 = static_cast<const uint16_t*>(p.q);
     const int rows = p.Sq * p.Hq;
     for (int b = blockIdx.x; b < p.B; b += p.grid) {  // sequences without keys
-        if (plan.lens[b] > 0) continue;
+        if (plan.prefix[b + 1] > plan.prefix[b]) continue;
         for (int i = tid; i < rows * D; i += kKv8Threads) o16[(size_t)b * rows * D + i] = 0;
         if (p.lse)
             for (int i = tid; i < rows; i += kKv8Threads) p.lse[(size_t)b * rows + i] = kNegInf;
     }
-    const uint32_t raw = smem_u32(ring_raw), base = (raw + 127u) & ~127u;
-    const uint32_t ring = base + warp * C::RingBytes;
-    float* exch = reinterpret_cast<float*>(ring_raw + (base - raw));
-    constexpr int XD = D + 4;  // row of the exchange
-    static_assert(kKv8Warps * 16 * XD * 4 <= kKv8Warps * C::RingBytes, "exchange fits the ring");
 
-    // This lane's units of a run of 16 rows: unit i * 32 + lane of the run's 16 D bytes.
+    // This lane's 16-byte units of a run of 16 rows: unit i * 32 + lane of the run's 16 D bytes.
     uint32_t dst[C::Copies], step[C::Copies];
 #pragma unroll
     for (int i = 0; i < C::Copies; ++i) {
         const int u = i * 32 + lane, row = u / (D / 16), c = u % (D / 16);
-        dst[i] = C::unit(row, c);
+        dst[i] = ring + C::unit(row, c);
         step[i] = C::run_step(c);
     }
     const int Hkv = p.pool.Hkv, cols = p.group * p.Sq;
-    const int runs_per_page = p.pool.page_size / 16;
     const int total = Hkv * plan.prefix[p.B];
-    int x = (int)min((long long)blockIdx.x * W, (long long)total);
-    const int x_end = (int)min((long long)x + W, (long long)total);
-    while (x < x_end) {
-        int lo = 0, hi = p.B;  // largest b with Hkv * prefix[b] <= x
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (Hkv * plan.prefix[mid] <= x) lo = mid; else hi = mid;
-        }
-        const int b = lo, len = plan.lens[b], tb = kv8_tiles(len);
-        const int hk = (x - Hkv * plan.prefix[b]) / tb;
-        const int start = Hkv * plan.prefix[b] + hk * tb;
-        const int seg_end = min(x_end, start + tb);
-        const int slot = (int)blockIdx.x - start / W, pieces = kv8_pieces(start, tb, W);
-        const int k0 = (x - start) * kKv8Tile, k1 = min((seg_end - start) * kKv8Tile, len);
-        x = seg_end;
-        const int tiles = (k1 - k0 + KT - 1) / KT;  // warp w takes tiles w, w + kKv8Warps, ...
-        const int32_t* table = p.pool.table + (size_t)b * p.pool.max_pages;
+    const int x0 = (int)min((long long)blockIdx.x * W, (long long)total);
+    const int x_end = (int)min((long long)x0 + W, (long long)total);
 
-        // The 16-key run of the pool that holds run lane % NSUB of tile j: its index, -1 where
-        // there is none (behind k1, or a page outside the pool).
-        auto find_run = [&](int j) -> int {
-            const int key = k0 + j * KT + (lane % NSUB) * 16;
-            if (key >= k1) return -1;
+    // The loader walks the warp's tiles (w, w + kKv8Warps, ... of each segment) up to NST - 1
+    // ahead of the products, across the ends of segments.
+    Kv8Seg ls;
+    int lx = x0, lj = 0, ltiles = 0, run = -1;
+    // Steps to the next tile and looks up the 16-key run of the pool that holds run lane % NSUB
+    // of it: -1 where there is none (behind k1, or a page outside the pool).
+    auto next_tile = [&]() {
+        lj += kKv8Warps;
+        while (lj >= ltiles) {
+            if (!kv8_next_segment(p, plan, (int)blockIdx.x, W, lx, x_end, ls)) {
+                ltiles = 0;
+                lj = 0;
+                grid_launch_dependents();  // only now: the merge's CTAs would take room from this grid's
+                return;
+            }
+            // the segment's queries, which are read when its products begin, on their way to L2
+            for (int i = lane; i < cols * (D / 32); i += 32) {
+                const int col = i / (D / 32);
+                const size_t row = ((size_t)ls.b * p.Sq + col / p.group) * p.Hq + ls.hk * p.group + col % p.group;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q16 + row * D + i % (D / 32) * 32));
+            }
+            ltiles = (ls.k1 - ls.k0 + KT - 1) / KT;
+            lj = warp;
+        }
+        const int key = ls.k0 + lj * KT + (lane % NSUB) * 16;
+        run = -1;
+        if (key < ls.k1) {
             const unsigned pi = (unsigned)key / (unsigned)p.pool.page_size;
-            const int page = table[pi];
-            if (page < 0 || page >= p.pool.num_pages) return -1;
-            return (page * Hkv + hk) * runs_per_page + (int)((unsigned)key - pi * (unsigned)p.pool.page_size) / 16;
-        };
-        // Starts the copies of tile j into stage st; rows without a key become zeros.
-        auto issue = [&](int j, int st, int run) {
-            const uint32_t sk = ring + st * C::StageBytes, sv = sk + C::TileBytes, ss = sv + C::TileBytes;
+            const int page = p.pool.table[(size_t)ls.b * p.pool.max_pages + pi];
+            if (page >= 0 && page < p.pool.num_pages)
+                run = (page * Hkv + ls.hk) * (p.pool.page_size / 16) +
+                      (int)((unsigned)key - pi * (unsigned)p.pool.page_size) / 16;
+        }
+    };
+    // Starts the copies of the loader's tile into stage st; rows without a key become zeros.
+    auto issue = [&](int st) {
+        const uint32_t ok = st * 2 * C::TileBytes, ov = ok + C::TileBytes;
 #pragma unroll
-            for (int s = 0; s < NSUB; ++s) {
-                const int r = __shfl_sync(0xffffffffu, run, s);
-                const int key = k0 + j * KT + s * 16;
-                const int valid = r < 0 ? 0 : min(16, k1 - key) * D;
-                const size_t off = (size_t)max(r, 0) * (16 * D) + lane * 16;
+        for (int s = 0; s < NSUB; ++s) {
+            const int r = NSUB > 1 ? __shfl_sync(0xffffffffu, run, s) : run;
+            const int left = ls.k1 - (ls.k0 + lj * KT + s * 16);
+            const size_t off = (size_t)max(r, 0) * (16 * D) + lane * 16;
+            const uint8_t *k = p.pool.k + off, *v = p.pool.v + off;
+            if (r >= 0 && left >= 16) {
+#pragma unroll
+                for (int i = 0; i < C::Copies; ++i) {
+                    cp_async16(dst[i] + ok + s * step[i], k + i * 512, 16);
+                    cp_async16(dst[i] + ov + s * step[i], v + i * 512, 16);
+                }
+            } else {
+                const int valid = r < 0 ? 0 : left * D;
 #pragma unroll
                 for (int i = 0; i < C::Copies; ++i) {
                     const int n = i * 512 + lane * 16 < valid ? 16 : 0;
-                    const uint32_t d = dst[i] + s * step[i];
-                    cp_async16(sk + d, p.pool.k + off + i * 512, n);
-                    cp_async16(sv + d, p.pool.v + off + i * 512, n);
+                    cp_async16(dst[i] + ok + s * step[i], k + i * 512, n);
+                    cp_async16(dst[i] + ov + s * step[i], v + i * 512, n);
                 }
             }
-            if (lane < 2 * NSUB) {
-                const uint8_t* src = (lane < NSUB ? p.pool.ks : p.pool.vs) + (size_t)max(run, 0) * 16;
-                cp_async16(ss + (lane / NSUB) * KT + (lane % NSUB) * 16, src, run < 0 ? 0 : 16);
-            }
-        };
-
-        int run = find_run(warp);
-#pragma unroll
-        for (int i = 0; i < NST - 1; ++i) {
-            const int j = warp + i * kKv8Warps;
-            if (j < tiles) issue(j, i, run);
-            cp_async_commit();
-            run = find_run(j + kKv8Warps);
         }
+        if (lane < 2 * NSUB) {
+            const uint8_t* src = (lane < NSUB ? p.pool.ks : p.pool.vs) + (size_t)max(run, 0) * 16;
+            cp_async16(scales + st * 2 * KT + lane * 16, src, run < 0 ? 0 : 16);
+        }
+    };
+    next_tile();
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) {
+        if (lj < ltiles) {
+            issue(i);
+            next_tile();
+        }
+        cp_async_commit();
+    }
+
+    int st = 0, x = x0;
+    Kv8Seg sg;
+    while (kv8_next_segment(p, plan, (int)blockIdx.x, W, x, x_end, sg)) {
+        const int b = sg.b, hk = sg.hk, len = sg.len, k0 = sg.k0, k1 = sg.k1;
+        const int tiles = (k1 - k0 + KT - 1) / KT;
 
         // Query fragments: row n of a block as f16, times a power of two that brings its largest
         // magnitude to [2^13, 2^14).  fp16's subnormals are then 2^-38 of it, so bf16 and fp16
         // queries enter exactly but for values that far below their row's largest.
-        uint2 qr[kQRegs ? KS * NT : 1];
+        uint2 qr[C::QRegs ? KS * NT : 1];
         float qf[NT][2];
         int lim[NT][2];
 #pragma unroll
@@ -358,10 +439,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
                                             float_from16<kBF16>((uint16_t)(w[ks].x >> 16)) * up),
                                  pack_f16x2(float_from16<kBF16>((uint16_t)w[ks].y) * up,
                                             float_from16<kBF16>((uint16_t)(w[ks].y >> 16)) * up)};
-                if constexpr (kQRegs)
+                if constexpr (C::QRegs)
                     qr[ks * NT + nt] = f;
                 else if (warp == 0)
-                    s_q[ks * NT + nt][lane] = f;
+                    s_q[(ks * NT + nt) * 32 + lane] = f;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -370,7 +451,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
                 lim[nt][e] = p.causal ? min(k1, len - p.Sq + tk + 1) : k1;
             }
         }
-        if constexpr (!kQRegs) __syncthreads();
+        if constexpr (!C::QRegs) __syncthreads();
 
         float o[KS][NT][4], ms[NT][2], mo[NT][2], l[NT][2];
 #pragma unroll
@@ -386,17 +467,15 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
             }
         }
 
-        int st = 0;
         for (int j = warp; j < tiles; j += kKv8Warps) {
             cp_async_wait<NST - 2>();
             __syncwarp();
-            {
-                const int jn = j + (NST - 1) * kKv8Warps;
-                if (jn < tiles) issue(jn, st == 0 ? NST - 1 : st - 1, run);
-                cp_async_commit();
-                run = find_run(jn + kKv8Warps);
+            if (lj < ltiles) {
+                issue(st == 0 ? NST - 1 : st - 1);
+                next_tile();
             }
-            const uint32_t sk = ring + st * C::StageBytes, sv = sk + C::TileBytes, ss = sv + C::TileBytes;
+            cp_async_commit();
+            const uint32_t sk = ring + st * 2 * C::TileBytes, sv = sk + C::TileBytes, ss = scales + st * 2 * KT;
             st = st == NST - 1 ? 0 : st + 1;
 
             // S^T = K Q^T: 16 keys x 8 query rows at a time, the dims in an order that gives each
@@ -418,10 +497,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint2 q;
-                        if constexpr (kQRegs)
+                        if constexpr (C::QRegs)
                             q = qr[ks * NT + nt];
                         else
-                            q = s_q[ks * NT + nt][lane];
+                            q = s_q[(ks * NT + nt) * 32 + lane];
                         mma_16816(acc[ks & 1][nt], a0, a1, a2, a3, q.x, q.y);
                     }
                 };
@@ -446,8 +525,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
                     for (int i = 0; i < 4; ++i) sc[s][nt][i] = acc[0][nt][i] + acc[1][nt][i];
             }
 
-            // Softmax in base 2.  ms, l: this lane's own maximum and sum of exp2(s - ms) (joined at
-            // the end); mo: the reference of P = exp2(s + log2 V scale - mo), one for all lanes.
+            // Softmax in base 2.  l: this lane's own sum of exp2(s - ms) (joined at the end); mo: the
+            // reference of P = exp2(s + log2 V scale - mo), one for all lanes.  Both references
+            // move only when a score passes them by a margin: ms by 2^64, which fp32 has room for,
+            // mo by kPSlack.
             float lv[NSUB][2];
             bool grow = false;
 #pragma unroll
@@ -463,37 +544,27 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
                         for (int e = 0; e < 2; ++e) {
                             float& v = sc[s][nt][i * 2 + e];
                             v = key < lim[nt][e] ? v * (kf * qf[nt][e]) : kNegInf;
-                            grow |= v + lv[s][i] > mo[nt][e] + kPSlack;
+                            grow |= v + lv[s][i] > mo[nt][e] + kPSlack || v > ms[nt][e] + 64.f;
                         }
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float m = ms[nt][e];
-#pragma unroll
-                    for (int s = 0; s < NSUB; ++s) m = fmaxf(m, fmaxf(sc[s][nt][e], sc[s][nt][2 + e]));
-                    float sum = l[nt][e] * ex2_approx(ms[nt][e] - m);
-#pragma unroll
-                    for (int s = 0; s < NSUB; ++s)
-                        sum += ex2_approx(sc[s][nt][e] - m) + ex2_approx(sc[s][nt][2 + e] - m);
-                    l[nt][e] = sum;
-                    ms[nt][e] = m;
-                }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = mo[nt][e];
+                        float m = ms[nt][e], r = mo[nt][e];
 #pragma unroll
-                        for (int s = 0; s < NSUB; ++s)
-                            m = fmaxf(m, fmaxf(sc[s][nt][e] + lv[s][0], sc[s][nt][2 + e] + lv[s][1]));
+                        for (int s = 0; s < NSUB; ++s) {
+                            m = fmaxf(m, fmaxf(sc[s][nt][e], sc[s][nt][2 + e]));
+                            r = fmaxf(r, fmaxf(sc[s][nt][e] + lv[s][0], sc[s][nt][2 + e] + lv[s][1]));
+                        }
+                        l[nt][e] *= ex2_approx(ms[nt][e] - m);
+                        ms[nt][e] = m;
 #pragma unroll
-                        for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-                        const float f = ex2_approx(mo[nt][e] - m);
-                        mo[nt][e] = m;
+                        for (int w = 4; w < 32; w <<= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, w));
+                        const float f = ex2_approx(mo[nt][e] - r);
+                        mo[nt][e] = r;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             o[k][nt][e] *= f;
@@ -501,6 +572,13 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
                         }
                     }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int s = 0; s < NSUB; ++s)
+                        l[nt][e] += ex2_approx(sc[s][nt][e] - ms[nt][e]) + ex2_approx(sc[s][nt][2 + e] - ms[nt][e]);
 
             // O^T += V^T P^T: 16 dims x 8 query rows over 16 keys.  A lane's units of keys 2 t,
             // 2 t + 1 (and + 8) are interleaved into pairs of keys.
@@ -561,9 +639,8 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
         }
 
         // Join the warps: per query row the maxima and sums over the lanes of one t, then the four
-        // warps through shared memory (the ring, which nobody reads any more).
-        cp_async_wait<0>();
-        __syncthreads();
+        // warps' through shared memory; the outputs, brought to one reference, are added up in two
+        // buffers, warps 2 and 3 onto what 0 and 1 have left there.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -574,159 +651,221 @@ __global__ void __launch_bounds__(kKv8Threads, 2) kv8_split_kernel(const Kv8DecP
                 float sum = l[nt][e] * ex2_approx(ms[nt][e] - m);
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                const int col = nt * 8 + 2 * t + e;
                 if (g == 0) {
+                    const int col = nt * 8 + 2 * t + e;
                     s_mo[warp][col] = mo[nt][e];
                     s_ms[warp][col] = m;
                     s_l[warp][col] = sum;
                 }
-                if (col < cols) {
-                    float* row = exch + (warp * 16 + col) * XD;
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        int d;  // dims d, d + 1: rows g and g + 8 of block k
-                        if constexpr (C::WA == 64)
-                            d = k < 4 ? g * 8 + k * 2 : 64 + g * 4 + (k - 4) * 2;
-                        else
-                            d = (k >> 3) * 128 + g * 16 + (k & 7) * 2;
-                        *reinterpret_cast<float2*>(row + d) = make_float2(o[k][nt][e], o[k][nt][2 + e]);
-                    }
-                }
             }
         __syncthreads();
-        for (int i = tid; i < cols * (D / 2); i += kKv8Threads) {
-            const int col = i / (D / 2), d = i % (D / 2) * 2;
-            float Mo = s_mo[0][col], Ms = s_ms[0][col];
+        auto leave = [&](bool add) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = nt * 8 + 2 * t + e;
+                    if (col >= cols) continue;
+                    float m = s_mo[0][col];
+#pragma unroll
+                    for (int w = 1; w < kKv8Warps; ++w) m = fmaxf(m, s_mo[w][col]);
+                    const float f = ex2_approx(mo[nt][e] - m);
+                    float* row = exch + ((warp & 1) * NT * 8 + col) * XD;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        float2* at = reinterpret_cast<float2*>(row) + k * 8 + g;
+                        float2 v = make_float2(o[k][nt][e] * f, o[k][nt][2 + e] * f);
+                        if (add) {
+                            const float2 u = *at;
+                            v = make_float2(u.x + v.x, u.y + v.y);
+                        }
+                        *at = v;
+                    }
+                }
+        };
+        if (warp < 2) leave(false);
+        if (tid >= 64 && tid < 64 + cols) {
+            // O = (sum of the outputs) 2^(Mo - kPShift - Ms) / L.  The power is taken in two halves:
+            // V scales go down to 2^-127.
+            const int col = tid - 64;
+            float Mo = s_mo[0][col], Ms = s_ms[0][col], L = 0.f;
 #pragma unroll
             for (int w = 1; w < kKv8Warps; ++w) {
                 Mo = fmaxf(Mo, s_mo[w][col]);
                 Ms = fmaxf(Ms, s_ms[w][col]);
             }
-            float L = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll
-            for (int w = 0; w < kKv8Warps; ++w) {
-                const float f = ex2_approx(s_mo[w][col] - Mo);
-                const float2 v = *reinterpret_cast<const float2*>(exch + (w * 16 + col) * XD + d);
-                a0 = fmaf(f, v.x, a0);
-                a1 = fmaf(f, v.y, a1);
-                L = fmaf(ex2_approx(s_ms[w][col] - Ms), s_l[w][col], L);
-            }
-            // O = a 2^(Mo - kPShift - Ms) / L, the power in two halves (V scales go down to 2^-127)
+            for (int w = 0; w < kKv8Warps; ++w) L = fmaf(ex2_approx(s_ms[w][col] - Ms), s_l[w][col], L);
             const float f = ex2_approx((Mo - kPShift - Ms) * 0.5f);
-            const float inv = 1.f / L;
-            a0 = L == 0.f ? 0.f : a0 * inv * f * f;
-            a1 = L == 0.f ? 0.f : a1 * inv * f * f;
+            s_f[col] = f;
+            s_finv[col] = L == 0.f ? 0.f : f / L;  // no visible key: O = 0
+            s_lse[col] = L == 0.f ? kNegInf : (Ms + lg2_approx(L)) * kLn2;
+        }
+        __syncthreads();
+        if (warp >= 2) leave(true);
+        __syncthreads();
+        for (int i = tid; i < cols * (D / 2); i += kKv8Threads) {
+            // Pair u of dims is block k, row g of the products; four threads of one g take
+            // neighbouring pairs.
+            const int col = i / (D / 2), u = i % (D / 2);
+            int k, gg, d;
+            if constexpr (C::WA == 64) {
+                k = u < 32 ? u & 3 : 4 + (u & 1);
+                gg = u < 32 ? u >> 2 : (u - 32) >> 1;
+                d = u < 32 ? gg * 8 + k * 2 : 64 + gg * 4 + (k - 4) * 2;
+            } else {
+                k = (u & 3) + (u >> 5) * 4;
+                gg = (u >> 2) & 7;
+                d = (k >> 3) * 128 + gg * 16 + (k & 7) * 2;
+            }
+            const float2 v0 = *reinterpret_cast<const float2*>(exch + col * XD + (k * 8 + gg) * 2);
+            const float2 v1 = *reinterpret_cast<const float2*>(exch + (NT * 8 + col) * XD + (k * 8 + gg) * 2);
+            const float f = s_f[col], finv = s_finv[col];
+            const float a0 = (v0.x + v1.x) * finv * f, a1 = (v0.y + v1.y) * finv * f;
             const int tok = col / p.group, h = hk * p.group + col % p.group;
             const size_t row = ((size_t)b * p.Sq + tok) * p.Hq + h;
-            const float lse = L == 0.f ? kNegInf : (Ms + lg2_approx(L)) * kLn2;
-            if (pieces == 1) {
+            if (!sg.cut) {
                 *reinterpret_cast<uint32_t*>(o16 + row * D + d) = pack2<kBF16>(a0, a1);
-                if (d == 0 && p.lse) p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = lse;
+                if (d == 0 && p.lse) p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s_lse[col];
             } else {
-                *reinterpret_cast<float2*>(p.o_part + (row * p.ns + slot) * D + d) = make_float2(a0, a1);
-                if (d == 0) p.lse_part[row * p.ns + slot] = lse;
+                const size_t part = (size_t)sg.slot * cols + col;
+                *reinterpret_cast<float2*>(p.o_part + part * D + d) = make_float2(a0, a1);
+                if (d == 0) p.lse_part[part] = s_lse[col];
             }
         }
-        __syncthreads();  // before the ring and the plan's next segment
+        __syncthreads();  // before the next segment's exchange
     }
 }
 
 template <int D, int NT, bool kBF16>
 fa_status launch_kv8_split(const Kv8DecParams& p, cudaStream_t s) {
+    using C = Kv8Cfg<D, NT>;
     static int attr[64] = {0};
-    constexpr int bytes = Kv8Cfg<D>::SmemBytes;
-    if (!ensure_smem_attr((const void*)kv8_split_kernel<D, NT, kBF16>, bytes, attr)) return FA_ERR_CUDA;
-    return launch_overlapped(kv8_split_kernel<D, NT, kBF16>, p.grid, kKv8Threads, bytes, s, p);
+    constexpr int most = C::FixedBytes + Kv8Plan::bytes(kKv8MaxB);
+    static_assert(most <= 227 * 1024 - 1024, "shared memory of a CTA");
+    if (!ensure_smem_attr((const void*)kv8_split_kernel<D, NT, kBF16>, most, attr)) return FA_ERR_CUDA;
+    return launch_overlapped(kv8_split_kernel<D, NT, kBF16>, p.grid, kKv8Threads,
+                             C::FixedBytes + Kv8Plan::bytes(p.B), s, p);
+}
+
+// An SM divides its memory into L1 and shared memory anew only when it is idle: a kernel that
+// prefers L1, still resident, would keep the split kernel's CTAs from fitting beside it.
+inline bool prefer_shared(const void* f, const void* g, int* done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) return true;
+    for (const void* k : {f, g})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+            cudaSuccess)
+            return false;
+    __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
+    return true;
 }
 
 // Joins the pieces of each row (b, token, head): lse = log sum_c exp(lse_c), and the outputs
 // weighted with exp(lse_c - lse).  WPR warps share a row, each taking every WPR-th piece; a
-// lane holds D / 32 dims.  It moves few bytes: its time is the launch and two or three
-// dependent trips to L2, so the pieces of a warp are loaded several at a time.
+// lane holds D / 32 dims.  It moves few bytes: its time is the launch and the dependent trips
+// to L2.  So where the pieces lie is worked out before the split kernel is done (kv_lens is
+// older than that kernel), and a warp then loads the log-sum-exps and outputs of NB pieces
+// together.
 template <int D, int WPR, bool kBF16>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     constexpr int V = D / 32, Rows = 8 / WPR, NB = V <= 4 ? 8 : 4;
-    __shared__ float s_acc[WPR > 1 ? 8 : 1][D], s_sum[8];
-    grid_dependency_wait();
-    grid_launch_dependents();
+    __shared__ float s_acc[WPR > 1 ? 8 : 1][D], s_sum[8], s_max[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * Rows + warp / WPR, part = warp % WPR;
-    if (row >= p.B * p.Sq * p.Hq) return;  // whole CTAs where WPR = 8
+    const float kNegInf = -__int_as_float(0x7f800000);
     const int b = row / (p.Sq * p.Hq), tok = row / p.Hq % p.Sq, h = row % p.Hq;
-    int before = 0, sum = 0, most = 0;
+    int before = 0, sum = 0, units = 0;
     for (int i = lane; i < p.B; i += 32) {
-        const int t = kv8_tiles(kv8_len(p, i));
+        const int t = kv8_units(kv8_len(p, i));
         before += i < b ? t : 0;
+        units += i == b ? t : 0;
         sum += t;
-        most = max(most, t);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
-    const int tb = kv8_tiles(kv8_len(p, b));
-    const int W = kv8_width(p, sum, most);
-    const int n = kv8_pieces(p.pool.Hkv * before + h / p.group * tb, tb, W);
-    if (n < 2) return;  // the split kernel has written this row (n is the same in all of a row's warps)
-    const float kNegInf = -__int_as_float(0x7f800000);
-    const float* lrow = p.lse_part + (size_t)row * p.ns;
-    const float* orow = p.o_part + (size_t)row * p.ns * D + lane;
-    float m = kNegInf;
-    for (int c = lane; c < n; c += 32) m = fmaxf(m, lrow[c]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[V], s = 0.f;
+    const int W = kv8_width(p, sum), start = p.pool.Hkv * before + h / p.group * units;
+    const int n = kv8_pieces(start, units, W), first = kv8_first_piece(start, W);
+    const int cols = p.group * p.Sq, col = tok * p.group + h % p.group;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // Rows with one piece or none have been written by the split kernel.  n is the same in all of
+    // a row's warps.
+    if (row >= p.B * p.Sq * p.Hq || n < 2) return;
+    float acc[V], s = 0.f, m = kNegInf;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    if (m != kNegInf) {
-        for (int c0 = part; c0 < n; c0 += WPR * NB) {
-            float w[NB], v[NB][V];
+    for (int c0 = part; c0 < n; c0 += WPR * NB) {
+        float w[NB], v[NB][V], top = m;
 #pragma unroll
-            for (int u = 0; u < NB; ++u) {  // pieces past n: the last one, with weight 0
-                const int c = min(c0 + u * WPR, n - 1);
-                w[u] = c0 + u * WPR < n ? lrow[c] : kNegInf;
+        for (int u = 0; u < NB; ++u) {  // pieces past n: the last one, with weight 0
+            const int c = min(c0 + u * WPR, n - 1);
+            const size_t at = (size_t)kv8_slot(first + c, c == 0) * cols + col;
+            w[u] = p.lse_part[at];
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[u][i] = orow[(size_t)c * D + i * 32];
-            }
+            for (int i = 0; i < V; ++i) v[u][i] = p.o_part[at * D + lane + i * 32];
+        }
 #pragma unroll
-            for (int u = 0; u < NB; ++u) {
-                const float f = ex2_approx((w[u] - m) * (1.f / kLn2));
-                s += f;
-                // a piece without a visible key has weight 0 and an output of 0; a weight of 0
-                // that pads the batch must not meet a NaN or an infinity
+        for (int u = 0; u < NB; ++u) {
+            if (c0 + u * WPR >= n) w[u] = kNegInf;
+            top = fmaxf(top, w[u]);
+        }
+        const float ref = top == kNegInf ? 0.f : top;
+        const float f = ex2_approx((m - ref) * (1.f / kLn2));
+        m = top;
+        s *= f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(f, w[u] == kNegInf ? 0.f : v[u][i], acc[i]);
-            }
+        for (int i = 0; i < V; ++i) acc[i] *= f;
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+            const float e = ex2_approx((w[u] - ref) * (1.f / kLn2));
+            s += e;
+            // a weight of 0 must not meet a NaN or an infinity of a piece read twice
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(e, w[u] == kNegInf ? 0.f : v[u][i], acc[i]);
         }
     }
     if constexpr (WPR > 1) {
 #pragma unroll
         for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
-        if (lane == 0) s_sum[warp] = s;
+        if (lane == 0) {
+            s_sum[warp] = s;
+            s_max[warp] = m;
+        }
         __syncthreads();
         if (warp != 0) return;
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) m = fmaxf(m, s_max[w]);
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        const float ref = m == kNegInf ? 0.f : m;
 #pragma unroll
         for (int w = 0; w < WPR; ++w) {
-            s += s_sum[w];
+            const float f = ex2_approx((s_max[w] - ref) * (1.f / kLn2));
+            s += f * s_sum[w];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += s_acc[w][lane + i * 32];
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(f, s_acc[w][lane + i * 32], acc[i]);
         }
     }
-    const float inv = 1.f / s;
+    const float inv = 1.f / s;  // s == 0: no piece holds a visible key
     uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane;
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i * 32] = float_to16<kBF16>(m == kNegInf ? 0.f : acc[i] * inv);
+    for (int i = 0; i < V; ++i) out[i * 32] = float_to16<kBF16>(s == 0.f ? 0.f : acc[i] * inv);
     if (p.lse && lane == 0)
-        p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = m == kNegInf ? kNegInf : m + lg2_approx(s) * kLn2;
+        p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kLn2;
 }
 
 template <int D, int WPR>
 fa_status launch_kv8_merge(const Kv8DecParams& p, bool bf16, cudaStream_t s) {
+    static int attr[64] = {0};
+    if (!prefer_shared((const void*)kv8_merge_kernel<D, WPR, true>, (const void*)kv8_merge_kernel<D, WPR, false>, attr))
+        return FA_ERR_CUDA;
     const unsigned rows = (unsigned)(p.B * p.Sq * p.Hq), grid = (rows + 8 / WPR - 1) / (8 / WPR);
     return bf16 ? launch_overlapped(kv8_merge_kernel<D, WPR, true>, grid, 256, 0, s, p)
                 : launch_overlapped(kv8_merge_kernel<D, WPR, false>, grid, 256, 0, s, p);
@@ -747,21 +886,27 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     p.Hq = a.Hq;
     p.group = a.Hq / a.pool.Hkv;
     p.capacity = a.pool.page_size * a.pool.max_pages;
-    p.ns = a.num_splits;
     p.causal = a.causal ? 1 : 0;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    // No more CTAs than the cache could ever hold tiles.
-    const long long most = (long long)a.B * a.pool.Hkv * ((p.capacity + kKv8Tile - 1) / kKv8Tile);
-    p.grid = (int)(most < 2LL * a.num_sms ? most : 2LL * a.num_sms);
+    // As many ranges as CTAs are resident at once, where the workspace's slots (one partial
+    // result each of one pair) allow it: two a range.  If they allow fewer ranges than there are
+    // pairs to spread, no pair is cut.
+    const int per_sm = p.group * p.Sq <= 8 ? Kv8Cfg<D, 1>::CTAS : Kv8Cfg<D, 2>::CTAS;
+    const long long pairs = (long long)a.B * a.pool.Hkv, resident = (long long)per_sm * a.num_sms;
+    const long long most = pairs * ((p.capacity + kKv8Unit - 1) / kKv8Unit);
+    const long long ranges = std::min({resident, most, a.slots / 2});
+    p.whole = a.slots == 0 || ranges < std::min(resident, pairs);
+    p.grid = (int)(p.whole ? std::min(resident, pairs) : ranges);
     fa_status st;
     if (p.group * p.Sq <= 8)
         st = a.bf16 ? launch_kv8_split<D, 1, true>(p, s) : launch_kv8_split<D, 1, false>(p, s);
     else
         st = a.bf16 ? launch_kv8_split<D, 2, true>(p, s) : launch_kv8_split<D, 2, false>(p, s);
-    if (st != FA_OK || p.ns < 2) return st;
+    if (st != FA_OK || p.whole) return st;
     // Few rows are cut into many pieces: eight warps each.
     return a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_kv8_merge<D, 8>(p, a.bf16, s)
                                               : launch_kv8_merge<D, 1>(p, a.bf16, s);
 }
 
 }  // namespace fa
+

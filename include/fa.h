@@ -306,11 +306,15 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  * enter the products exactly; the probabilities are rounded to fp16 (11 bits) for P.V; O is
  * rounded once.  What lies in the pool behind a sequence's last key is not used, NaN codes
  * there included.  Keys on a page outside the pool count as zero rows.
- *   num_splits  the most pieces a (sequence, kv head) pair is cut into (<= 0: the default,
- *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0))
- *   workspace at least fa_decode_workspace_bytes(B * Sq, Hq, D, num_splits) bytes; no
- *             initialisation; may be NULL where num_splits is 1.  Calls that may overlap on
- *             the GPU need one each.
+ *   num_splits  sizes the workspace, which holds B * Hkv * num_splits partial results (<= 0:
+ *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0)).  The keys of
+ *             all (sequence, kv head) pairs are laid end to end and cut into equal ranges, one
+ *             per CTA that can be resident, but at most half as many as that, since a range
+ *             leaves up to two partial results; where this gives fewer ranges than pairs to
+ *             spread, and where num_splits is 1, pairs are not cut and a CTA takes whole ones.
+ *   workspace at least fa_decode_workspace_bytes(B * Sq, Hq, D, num_splits) bytes (after the
+ *             default is applied); no initialisation; not used, and may be NULL, where
+ *             num_splits is 1.  Calls that may overlap on the GPU need one each.
  * The result does not depend on num_splits beyond rounding; the same inputs give the same
  * bits.
  */
