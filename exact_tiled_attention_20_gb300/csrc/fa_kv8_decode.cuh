@@ -171,10 +171,14 @@ __device__ __forceinline__ bool kv8_next_segment(const Kv8DecParams& p, const Kv
 // WA bytes and, at D = 96, one of 32; each part's rows lie in 128-byte lines whose 16-byte
 // units are permuted so that the reads below, K by (row g, unit t) and V by (row 2 t, unit g),
 // meet no bank twice.
-template <int D_, int NT_>
+//
+// HB: query rows in blocks of four (1, 2 or 4 blocks; a row is a (token, head) of one kv head).
+template <int D_, int HB_>
 struct Kv8Cfg {
-    static constexpr int D = D_, NT = NT_;
-    static constexpr int KT = D == 64 || D == 256 ? (D == 64 ? 32 : 16) : 32;
+    static constexpr int D = D_, HB = HB_;
+    static constexpr int NT = (HB + 1) / 2;     // 8-column blocks of P
+    static constexpr int E = HB == 1 ? 1 : 2;   // columns of a lane in use
+    static constexpr int KT = D == 256 ? 16 : 32;
     static constexpr int NST = D == 64 ? 4 : D == 256 && NT == 1 ? 3 : 2;
     static constexpr int CTAS = D == 256 || NT == 2 ? 2 : 3;  // resident on an SM
     static constexpr int NSUB = KT / 16;  // runs of 16 keys
@@ -182,9 +186,9 @@ struct Kv8Cfg {
     static constexpr int RingBytes = NST * 2 * TileBytes;  // a warp's
     static constexpr int ScaleBytes = NST * 2 * KT;
     // Row of the exchange in floats: pair (block k, row g) of dims at 2 (8 k + g); a half-warp's
-    // 4 g and 4 t, two query rows apart, then lie in 32 different banks.
-    static constexpr int XD = D + 4;
-    static constexpr int ExchBytes = 2 * NT * 8 * XD * 4;      // two buffers
+    // 4 g and 4 t, one query row apart, then lie in 32 different banks.
+    static constexpr int XD = D + 8;
+    static constexpr int ExchBytes = 2 * HB * 4 * XD * 4;      // two buffers
     static constexpr bool QRegs = D / 16 * NT <= 16;           // query fragments in registers, else shared
     static constexpr int QBytes = QRegs ? 0 : D / 16 * NT * 32 * 8;
     static constexpr int FixedBytes = 128 + kKv8Warps * (RingBytes + ScaleBytes) + ExchBytes + QBytes;
@@ -271,11 +275,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 constexpr float kPShift = 11.f, kPSlack = 4.f;
 constexpr float kLowest = -3.402823466e38f;
 
-// NT: blocks of 8 query rows (tokens x heads of one kv head; column token * group + head).
-template <int D, int NT, bool kBF16>
-__global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_kernel(const Kv8DecParams p) {
-    using C = Kv8Cfg<D, NT>;
-    constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS, XD = C::XD;
+// Query row c (token * group + head) of the kv head belongs to block c / 4; lane t of four has
+// rows 4 hb + t of the blocks hb = 2 nt + e, e < E.
+template <int D, int HB, bool kBF16>
+__global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_kernel(const Kv8DecParams p) {
+    using C = Kv8Cfg<D, HB>;
+    constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS, XD = C::XD, NT = C::NT, E = C::E;
     extern __shared__ uint8_t smem_raw[];
     __shared__ float s_mo[kKv8Warps][16], s_ms[kKv8Warps][16], s_l[kKv8Warps][16];
     __shared__ float s_f[16], s_finv[16], s_lse[16];
@@ -404,23 +409,25 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
         const int b = sg.b, hk = sg.hk, len = sg.len, k0 = sg.k0, k1 = sg.k1;
         const int tiles = (k1 - k0 + KT - 1) / KT;
 
-        // Query fragments: row n of a block as f16, times a power of two that brings its largest
-        // magnitude to [2^13, 2^14).  fp16's subnormals are then 2^-38 of it, so bf16 and fp16
-        // queries enter exactly but for values that far below their row's largest.
+        // Query fragments as f16, column 2 t + e of block nt being row (2 nt + e) * 4 + t.  A row is
+        // multiplied by a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's
+        // subnormals are then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values
+        // that far below their row's largest.
         uint2 qr[C::QRegs ? KS * NT : 1];
-        float qf[NT][2];
-        int lim[NT][2];
+        float qf[NT][E];
+        int lim[NT][E];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int col = nt * 8 + g;
-            const int tok = col / p.group, h = hk * p.group + col % p.group;
+            const int c = (nt * 2 + (g & 1)) * 4 + (g >> 1);
+            const bool in = c < cols && (g & 1) < E;
+            const int tok = c / p.group, h = hk * p.group + c % p.group;
             const uint16_t* src = q16 + (((size_t)b * p.Sq + tok) * p.Hq + h) * D;
             uint2 w[KS];
             float amax = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int d = ks * 16 < C::WA ? (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 : 64 + t * 8 + (ks - 4) * 4;
-                w[ks] = col < cols ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
+                w[ks] = in ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(float_from16<kBF16>((uint16_t)w[ks].x)),
                                                fabsf(float_from16<kBF16>((uint16_t)(w[ks].x >> 16)))),
                                          fmaxf(fabsf(float_from16<kBF16>((uint16_t)w[ks].y)),
@@ -445,15 +452,14 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
                     s_q[(ks * NT + nt) * 32 + lane] = f;
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 qf[nt][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
-                const int tk = (nt * 8 + 2 * t + e) / p.group;
-                lim[nt][e] = p.causal ? min(k1, len - p.Sq + tk + 1) : k1;
+                lim[nt][e] = p.causal ? min(k1, len - p.Sq + ((nt * 2 + e) * 4 + t) / p.group + 1) : k1;
             }
         }
         if constexpr (!C::QRegs) __syncthreads();
 
-        float o[KS][NT][4], ms[NT][2], mo[NT][2], l[NT][2];
+        float o[KS][NT][4], ms[NT][E], mo[NT][E], l[NT][E];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[m][nt][i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 ms[nt][e] = mo[nt][e] = kLowest;
                 l[nt][e] = 0.f;
             }
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 
             // S^T = K Q^T: 16 keys x 8 query rows at a time, the dims in an order that gives each
             // lane whole 16-byte units of its rows.
-            float sc[NSUB][NT][4];
+            float sc[NSUB][2][NT][E];  // keys g, g + 8 of a run
 #pragma unroll
             for (int s = 0; s < NSUB; ++s) {
                 float acc[2][NT][4];  // two chains of dependent products
@@ -522,7 +528,9 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[s][nt][i] = acc[0][nt][i] + acc[1][nt][i];
+                    for (int e = 0; e < E; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) sc[s][i][nt][e] = acc[0][nt][i * 2 + e] + acc[1][nt][i * 2 + e];
             }
 
             // Softmax in base 2.  l: this lane's own sum of exp2(s - ms) (joined at the end); mo: the
@@ -541,8 +549,8 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& v = sc[s][nt][i * 2 + e];
+                        for (int e = 0; e < E; ++e) {
+                            float& v = sc[s][i][nt][e];
                             v = key < lim[nt][e] ? v * (kf * qf[nt][e]) : kNegInf;
                             grow |= v + lv[s][i] > mo[nt][e] + kPSlack || v > ms[nt][e] + 64.f;
                         }
@@ -552,12 +560,12 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < E; ++e) {
                         float m = ms[nt][e], r = mo[nt][e];
 #pragma unroll
                         for (int s = 0; s < NSUB; ++s) {
-                            m = fmaxf(m, fmaxf(sc[s][nt][e], sc[s][nt][2 + e]));
-                            r = fmaxf(r, fmaxf(sc[s][nt][e] + lv[s][0], sc[s][nt][2 + e] + lv[s][1]));
+                            m = fmaxf(m, fmaxf(sc[s][0][nt][e], sc[s][1][nt][e]));
+                            r = fmaxf(r, fmaxf(sc[s][0][nt][e] + lv[s][0], sc[s][1][nt][e] + lv[s][1]));
                         }
                         l[nt][e] *= ex2_approx(ms[nt][e] - m);
                         ms[nt][e] = m;
@@ -575,10 +583,10 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < E; ++e)
 #pragma unroll
                     for (int s = 0; s < NSUB; ++s)
-                        l[nt][e] += ex2_approx(sc[s][nt][e] - ms[nt][e]) + ex2_approx(sc[s][nt][2 + e] - ms[nt][e]);
+                        l[nt][e] += ex2_approx(sc[s][0][nt][e] - ms[nt][e]) + ex2_approx(sc[s][1][nt][e] - ms[nt][e]);
 
             // O^T += V^T P^T: 16 dims x 8 query rows over 16 keys.  A lane's units of keys 2 t,
             // 2 t + 1 (and + 8) are interleaved into pairs of keys.
@@ -589,10 +597,10 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float v[2];
+                        float v[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            v[e] = ex2_approx((sc[s][nt][i * 2 + e] + lv[s][i]) - (mo[nt][e] - kPShift));
+                        for (int e = 0; e < E; ++e)
+                            v[e] = ex2_approx((sc[s][i][nt][e] + lv[s][i]) - (mo[nt][e] - kPShift));
                         pb[nt][i] = transpose8x8(pack_f16x2(v[0], v[1]));
                     }
                 // words of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9: dims 4 i .. 4 i + 3 of the unit
@@ -644,7 +652,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 float m = ms[nt][e];
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
@@ -652,7 +660,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
                 if (g == 0) {
-                    const int col = nt * 8 + 2 * t + e;
+                    const int col = (nt * 2 + e) * 4 + t;
                     s_mo[warp][col] = mo[nt][e];
                     s_ms[warp][col] = m;
                     s_l[warp][col] = sum;
@@ -663,14 +671,14 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int col = nt * 8 + 2 * t + e;
+                for (int e = 0; e < E; ++e) {
+                    const int col = (nt * 2 + e) * 4 + t;
                     if (col >= cols) continue;
                     float m = s_mo[0][col];
 #pragma unroll
                     for (int w = 1; w < kKv8Warps; ++w) m = fmaxf(m, s_mo[w][col]);
                     const float f = ex2_approx(mo[nt][e] - m);
-                    float* row = exch + ((warp & 1) * NT * 8 + col) * XD;
+                    float* row = exch + ((warp & 1) * HB * 4 + col) * XD;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         float2* at = reinterpret_cast<float2*>(row) + k * 8 + g;
@@ -719,7 +727,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
                 d = (k >> 3) * 128 + gg * 16 + (k & 7) * 2;
             }
             const float2 v0 = *reinterpret_cast<const float2*>(exch + col * XD + (k * 8 + gg) * 2);
-            const float2 v1 = *reinterpret_cast<const float2*>(exch + (NT * 8 + col) * XD + (k * 8 + gg) * 2);
+            const float2 v1 = *reinterpret_cast<const float2*>(exch + (HB * 4 + col) * XD + (k * 8 + gg) * 2);
             const float f = s_f[col], finv = s_finv[col];
             const float a0 = (v0.x + v1.x) * finv * f, a1 = (v0.y + v1.y) * finv * f;
             const int tok = col / p.group, h = hk * p.group + col % p.group;
@@ -737,14 +745,14 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, NT>::CTAS) kv8_split_ke
     }
 }
 
-template <int D, int NT, bool kBF16>
+template <int D, int HB, bool kBF16>
 fa_status launch_kv8_split(const Kv8DecParams& p, cudaStream_t s) {
-    using C = Kv8Cfg<D, NT>;
+    using C = Kv8Cfg<D, HB>;
     static int attr[64] = {0};
     constexpr int most = C::FixedBytes + Kv8Plan::bytes(kKv8MaxB);
     static_assert(most <= 227 * 1024 - 1024, "shared memory of a CTA");
-    if (!ensure_smem_attr((const void*)kv8_split_kernel<D, NT, kBF16>, most, attr)) return FA_ERR_CUDA;
-    return launch_overlapped(kv8_split_kernel<D, NT, kBF16>, p.grid, kKv8Threads,
+    if (!ensure_smem_attr((const void*)kv8_split_kernel<D, HB, kBF16>, most, attr)) return FA_ERR_CUDA;
+    return launch_overlapped(kv8_split_kernel<D, HB, kBF16>, p.grid, kKv8Threads,
                              C::FixedBytes + Kv8Plan::bytes(p.B), s, p);
 }
 
@@ -891,17 +899,19 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     // As many ranges as CTAs are resident at once, where the workspace's slots (one partial
     // result each of one pair) allow it: two a range.  If they allow fewer ranges than there are
     // pairs to spread, no pair is cut.
-    const int per_sm = p.group * p.Sq <= 8 ? Kv8Cfg<D, 1>::CTAS : Kv8Cfg<D, 2>::CTAS;
+    const int per_sm = p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::CTAS : Kv8Cfg<D, 4>::CTAS;
     const long long pairs = (long long)a.B * a.pool.Hkv, resident = (long long)per_sm * a.num_sms;
     const long long most = pairs * ((p.capacity + kKv8Unit - 1) / kKv8Unit);
     const long long ranges = std::min({resident, most, a.slots / 2});
     p.whole = a.slots == 0 || ranges < std::min(resident, pairs);
     p.grid = (int)(p.whole ? std::min(resident, pairs) : ranges);
     fa_status st;
-    if (p.group * p.Sq <= 8)
+    if (p.group * p.Sq <= 4)
         st = a.bf16 ? launch_kv8_split<D, 1, true>(p, s) : launch_kv8_split<D, 1, false>(p, s);
-    else
+    else if (p.group * p.Sq <= 8)
         st = a.bf16 ? launch_kv8_split<D, 2, true>(p, s) : launch_kv8_split<D, 2, false>(p, s);
+    else
+        st = a.bf16 ? launch_kv8_split<D, 4, true>(p, s) : launch_kv8_split<D, 4, false>(p, s);
     if (st != FA_OK || p.whole) return st;
     // Few rows are cut into many pieces: eight warps each.
     return a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_kv8_merge<D, 8>(p, a.bf16, s)
