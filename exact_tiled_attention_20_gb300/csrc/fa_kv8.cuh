@@ -43,6 +43,7 @@ struct Kv8AppendArgs {
     const int32_t* kv_lens;
     int B, total, D;
     bool bf16;
+    int num_sms;
 };
 
 struct Kv8ReadArgs {
@@ -53,6 +54,7 @@ struct Kv8ReadArgs {
     const int32_t* starts;  // [B] or null: 0
     int B, total, D;
     bool bf16;
+    int num_sms;
 };
 
 struct Kv8DecodeArgs {
@@ -112,21 +114,26 @@ __device__ __forceinline__ float kv8_scale(uint32_t s) {
     return __uint_as_float(s ? s << 23 : 0x00400000u);
 }
 
-// The scale byte of a row whose largest finite magnitude is amax: the least e >= -127 with
-// amax <= 448 * 2^e, plus 127.  448 = 1.75 * 2^8 is e4m3's largest value, so with
-// amax = f * 2^x, 1 <= f < 2, e = x - 8, and one more where f > 1.75.  amax comes from 16-bit
-// values: its fp32 form is normal, but for bf16's own subnormals, whose x is at most -127
-// and whose e is therefore -127.
-__device__ __forceinline__ uint32_t kv8_scale_byte(float amax) {
-    const uint32_t bits = __float_as_uint(amax);
-    const int byte = (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return (uint32_t)max(byte, 0);
+// The scale byte of a row from the 16 bits of its largest finite magnitude: the least
+// e >= -127 with amax <= 448 * 2^e, plus 127.  448 = 1.75 * 2^8 is e4m3's largest value, so with
+// amax = f * 2^x, 1 <= f < 2, e = x - 8, and one more where f > 1.75: adding a quarter less one
+// step to the fraction carries into the exponent just then.  (bf16's own subnormals have a zero
+// exponent field and e = -127; fp16's are normal in fp32.)
+template <bool kBF16>
+__device__ __forceinline__ uint32_t kv8_scale_byte(uint32_t amax16) {
+    int x;
+    if constexpr (kBF16) {
+        x = (int)((amax16 + 0x1fu) >> 7);
+    } else {
+        float f;
+        asm("{\n.reg .b16 a;\ncvt.u16.u32 a, %1;\ncvt.f32.f16 %0, a;\n}" : "=f"(f) : "r"(amax16));
+        x = (int)((__float_as_uint(f) + 0x1fffffu) >> 23);
+    }
+    return (uint32_t)max(x - 8, 0);
 }
 
-// 2^(127 - s), the exact factor that the codes are taken at.
-__device__ __forceinline__ float kv8_inv_scale(uint32_t s) {
-    return __uint_as_float(s < 254u ? (254u - s) << 23 : 0x00400000u);
-}
+// 2^(127 - s), the exact factor that the codes are taken at; s <= 247.
+__device__ __forceinline__ float kv8_inv_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
 // Two e4m3 codes (low byte first) -> f16x2, exactly (NaN codes become NaN).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {

@@ -59,10 +59,12 @@ fa_status fa_kv_append_paged_fp8(const void* k_new, const void* v_new, int64_t k
     const long long width = (long long)Hkv * D;
     if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0) return FA_ERR_INVALID_ARG;
     if ((long long)total_new * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (sms <= 0) return FA_ERR_CUDA;
     const Kv8AppendArgs a{make_pool(k_pages, v_pages, k_scales, v_scales, block_table, Hkv, num_pages, page_size,
                                     max_pages_per_seq),
                           k_new, v_new, k_stride, v_stride, cu_seqlens_new, kv_lens, B, total_new, D,
-                          dtype == FA_BF16};
+                          dtype == FA_BF16, sms};
     return launch_kv8_append(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -78,9 +80,11 @@ fa_status fa_kv_read_paged_fp8(const void* k_pages, const void* v_pages, const u
     if (total == 0) return FA_OK;
     if (!k || !v || misaligned(k, 16) || misaligned(v, 16)) return FA_ERR_INVALID_ARG;
     if ((long long)total * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (sms <= 0) return FA_ERR_CUDA;
     const Kv8ReadArgs a{make_pool(k_pages, v_pages, k_scales, v_scales, block_table, Hkv, num_pages, page_size,
                                   max_pages_per_seq),
-                        k, v, cu_seqlens, kv_starts, B, total, D, dtype == FA_BF16};
+                        k, v, cu_seqlens, kv_starts, B, total, D, dtype == FA_BF16, sms};
     return launch_kv8_read(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
