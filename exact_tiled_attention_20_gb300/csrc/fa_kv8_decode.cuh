@@ -31,6 +31,7 @@ struct Kv8DecParams {
     float* lse_part;  // [2 grid, group * Sq]
     int B, Sq, Hq, group, capacity, causal, whole;
     int grid;  // ranges, and CTAs of the split kernel
+    unsigned page_recip;  // floor(2^32 / page_size) + 1
     float scale_log2;
 };
 
@@ -356,11 +357,16 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         const int key = ls.k0 + lj * KT + (lane % NSUB) * 16;
         run = -1;
         if (key < ls.k1) {
-            const unsigned pi = (unsigned)key / (unsigned)p.pool.page_size;
+            // key / page_size: the reciprocal, rounded up, gives the quotient or one more
+            unsigned pi = __umulhi((unsigned)key, p.page_recip);
+            int slot = (int)((unsigned)key - pi * (unsigned)p.pool.page_size);
+            if (slot < 0) {
+                --pi;
+                slot += p.pool.page_size;
+            }
             const int page = p.pool.table[(size_t)ls.b * p.pool.max_pages + pi];
             if (page >= 0 && page < p.pool.num_pages)
-                run = (page * Hkv + ls.hk) * (p.pool.page_size / 16) +
-                      (int)((unsigned)key - pi * (unsigned)p.pool.page_size) / 16;
+                run = (page * Hkv + ls.hk) * (p.pool.page_size / 16) + slot / 16;
         }
     };
     // Starts the copies of the loader's tile into stage st; rows without a key become zeros.
@@ -458,6 +464,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             }
         }
         if constexpr (!C::QRegs) __syncthreads();
+        const int full = p.causal ? min(k1, len - p.Sq + 1) : k1;  // keys that every row sees
 
         float o[KS][NT][4], ms[NT][E], mo[NT][E], l[NT][E];
 #pragma unroll
@@ -539,6 +546,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             // mo by kPSlack.
             float lv[NSUB][2];
             bool grow = false;
+            const bool masked = k0 + j * KT + KT > full;
 #pragma unroll
             for (int s = 0; s < NSUB; ++s) {
 #pragma unroll
@@ -551,7 +559,8 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
 #pragma unroll
                         for (int e = 0; e < E; ++e) {
                             float& v = sc[s][i][nt][e];
-                            v = key < lim[nt][e] ? v * (kf * qf[nt][e]) : kNegInf;
+                            v *= kf * qf[nt][e];
+                            if (masked && key >= lim[nt][e]) v = kNegInf;
                             grow |= v + lv[s][i] > mo[nt][e] + kPSlack || v > ms[nt][e] + 64.f;
                         }
                 }
@@ -895,6 +904,7 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     p.group = a.Hq / a.pool.Hkv;
     p.capacity = a.pool.page_size * a.pool.max_pages;
     p.causal = a.causal ? 1 : 0;
+    p.page_recip = (unsigned)((1ull << 32) / (unsigned)a.pool.page_size) + 1u;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     // As many ranges as CTAs are resident at once, where the workspace's slots (one partial
     // result each of one pair) allow it: two a range.  If they allow fewer ranges than there are
