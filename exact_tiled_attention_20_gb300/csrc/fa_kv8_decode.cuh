@@ -10,9 +10,10 @@
 // starting and finishing a pair costs.  CTA c takes the range of units [c W, (c + 1) W):
 // every CTA gets the same work whatever the mix of lengths.  A pair whose keys lie in one
 // range is finished by its CTA.  One that is cut leaves a partial output and its log-sum-exp
-// in each range, which the merge kernel joins; a range meets at most two such pairs, one
-// that began before it and one that goes on behind it, so two slots a range hold them all.
-// Without room for that (`whole`), a CTA takes the pairs that begin in its range, uncut.
+// in each range, which the merge kernel joins.  A range meets at most one pair that began
+// before it and one that goes on behind it: the partial results fill a slot for each range
+// and one more for each range or for each pair, whichever are fewer, whatever the number of
+// pieces.  Without room for that (`whole`), a CTA takes the pairs that begin in its range, uncut.
 #pragma once
 
 #include <algorithm>
@@ -27,8 +28,8 @@ struct Kv8DecParams {
     void* o;
     float* lse;
     const int32_t* kv_lens;
-    float* o_part;    // [2 grid, group * Sq, D]: slot 2 r, 2 r + 1 of range r
-    float* lse_part;  // [2 grid, group * Sq]
+    float* o_part;    // [slots, group * Sq, D]
+    float* lse_part;  // [slots, group * Sq]
     int B, Sq, Hq, group, capacity, causal, whole;
     int grid;  // ranges, and CTAs of the split kernel
     unsigned page_recip;  // floor(2^32 / page_size) + 1
@@ -63,8 +64,10 @@ __device__ __forceinline__ int kv8_first_piece(int start, int w) { return (start
 __device__ __forceinline__ int kv8_pieces(int start, int units, int w) {
     return units > 0 ? (start + units - 1) / w - kv8_first_piece(start, w) + 1 : 0;
 }
-// The slot of a pair's piece in range r, `first` of its pieces or not.
-__device__ __forceinline__ int kv8_slot(int r, bool first) { return 2 * r + (first ? 1 : 0); }
+// The slot of a pair's piece in range r, the first of its pieces or not.
+__device__ __forceinline__ int kv8_slot(const Kv8DecParams& p, int r, bool first, int pair) {
+    return !first ? r : p.grid + (p.grid <= p.B * p.pool.Hkv ? r : pair);
+}
 
 template <bool kBF16>
 __device__ __forceinline__ uint16_t float_to16(float x) {
@@ -136,35 +139,58 @@ struct Kv8Seg {
     bool cut;
 };
 
-// The next segment of range `rng` from unit x on (x advances past it); false where none is left.
-__device__ __forceinline__ bool kv8_next_segment(const Kv8DecParams& p, const Kv8Plan& t, int rng, int W, int& x,
-                                                 int x_end, Kv8Seg& s) {
-    const int Hkv = p.pool.Hkv;
-    while (x < x_end) {
+// Walks the segments of range `rng`, units x .. x_end - 1.
+struct Kv8Walk {
+    int x, x_end;
+    int b, hk, start, units;  // the pair that holds unit x, or ends there
+
+    __device__ __forceinline__ void init(const Kv8DecParams& p, const Kv8Plan& t, int rng, int W) {
+        const int Hkv = p.pool.Hkv, total = Hkv * t.prefix[p.B];
+        x = (int)min((long long)rng * W, (long long)total);
+        x_end = (int)min((long long)x + W, (long long)total);
+        if (x >= x_end) return;
         int lo = 0, hi = p.B;  // largest b with Hkv * prefix[b] <= x: it has keys
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (Hkv * t.prefix[mid] <= x) lo = mid; else hi = mid;
         }
-        const int first = Hkv * t.prefix[lo], units = t.prefix[lo + 1] - t.prefix[lo];
-        s.b = lo;
-        s.hk = (x - first) / units;
-        const int start = first + s.hk * units;
-        if (p.whole && x > start) {  // the range before has it
-            x = start + units;
-            continue;
-        }
-        const int end = p.whole ? start + units : min(x_end, start + units);
-        s.len = (units - kKv8Lead) * kKv8Unit - t.pad[lo];
-        s.k0 = max(x - start - kKv8Lead, 0) * kKv8Unit;
-        s.k1 = min((end - start - kKv8Lead) * kKv8Unit, s.len);
-        s.slot = kv8_slot(rng, rng == kv8_first_piece(start, W));
-        s.cut = !p.whole && kv8_pieces(start, units, W) > 1;
-        x = end;
-        if (s.k1 > s.k0) return true;  // else the range ends within the lead
+        b = lo;
+        units = t.prefix[lo + 1] - t.prefix[lo];
+        hk = (x - Hkv * t.prefix[lo]) / units;
+        start = Hkv * t.prefix[lo] + hk * units;
     }
-    return false;
-}
+
+    // The next segment; false where none is left.
+    __device__ __forceinline__ bool next(const Kv8DecParams& p, const Kv8Plan& t, int rng, int W, Kv8Seg& s) {
+        while (x < x_end) {
+            if (x >= start + units) {
+                start += units;
+                if (++hk == p.pool.Hkv) {
+                    hk = 0;
+                    do {
+                        ++b;
+                        units = t.prefix[b + 1] - t.prefix[b];
+                    } while (units == 0);
+                }
+            }
+            if (p.whole && x > start) {  // the range before has it
+                x = start + units;
+                continue;
+            }
+            const int end = p.whole ? start + units : min(x_end, start + units);
+            s.b = b;
+            s.hk = hk;
+            s.len = (units - kKv8Lead) * kKv8Unit - t.pad[b];
+            s.k0 = max(x - start - kKv8Lead, 0) * kKv8Unit;
+            s.k1 = min((end - start - kKv8Lead) * kKv8Unit, s.len);
+            s.slot = kv8_slot(p, rng, rng == kv8_first_piece(start, W), b * p.pool.Hkv + hk);
+            s.cut = !p.whole && kv8_pieces(start, units, W) > 1;
+            x = end;
+            if (s.k1 > s.k0) return true;  // else the range ends within the lead
+        }
+        return false;
+    }
+};
 
 // ------------------------------------------------------------------ shared layout ----
 // Each warp streams its own tiles of KT keys through a ring of NST stages in shared memory:
@@ -190,8 +216,12 @@ struct Kv8Cfg {
     // 4 g and 4 t, one query row apart, then lie in 32 different banks.
     static constexpr int XD = D + 8;
     static constexpr int ExchBytes = 2 * HB * 4 * XD * 4;      // two buffers
-    static constexpr bool QRegs = D / 16 * NT <= 16;           // query fragments in registers, else shared
-    static constexpr int QBytes = QRegs ? 0 : D / 16 * NT * 32 * 8;
+    // Query fragments stay in registers or, where they are too many, in shared memory; they are
+    // made there, in the exchange's room if they do not stay.
+    static constexpr bool QRegs = D / 16 * NT <= 16;
+    static constexpr int QStage = D / 16 * NT * 32 * 8;
+    static constexpr int QBytes = QRegs ? 0 : QStage;
+    static_assert(!QRegs || QStage <= ExchBytes, "queries fit the exchange");
     static constexpr int FixedBytes = 128 + kKv8Warps * (RingBytes + ScaleBytes) + ExchBytes + QBytes;
     static constexpr int WA = D == 96 ? 64 : D;
     static constexpr int KS = D / 16;        // steps of 16 dims, and 16-dim blocks of O^T
@@ -284,7 +314,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS, XD = C::XD, NT = C::NT, E = C::E;
     extern __shared__ uint8_t smem_raw[];
     __shared__ float s_mo[kKv8Warps][16], s_ms[kKv8Warps][16], s_l[kKv8Warps][16];
-    __shared__ float s_f[16], s_finv[16], s_lse[16];
+    __shared__ float s_f[16], s_finv[16], s_lse[16], s_qf[16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -293,7 +323,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     const uint32_t scales = base + kKv8Warps * C::RingBytes + warp * C::ScaleBytes;
     uint8_t* rest = smem_raw + (base - raw) + kKv8Warps * (C::RingBytes + C::ScaleBytes);
     float* exch = reinterpret_cast<float*>(rest);
-    uint2* s_q = reinterpret_cast<uint2*>(rest + C::ExchBytes);
+    uint2* s_q = reinterpret_cast<uint2*>(C::QRegs ? rest : rest + C::ExchBytes);
     Kv8Plan plan;
     plan.prefix = reinterpret_cast<int*>(rest + C::ExchBytes + C::QBytes);
     plan.pad = reinterpret_cast<uint8_t*>(plan.prefix + p.B + 1);
@@ -326,30 +356,24 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         step[i] = C::run_step(c);
     }
     const int Hkv = p.pool.Hkv, cols = p.group * p.Sq;
-    const int total = Hkv * plan.prefix[p.B];
-    const int x0 = (int)min((long long)blockIdx.x * W, (long long)total);
-    const int x_end = (int)min((long long)x0 + W, (long long)total);
+    Kv8Walk lw, cw;  // the loader's and the products'
+    lw.init(p, plan, (int)blockIdx.x, W);
+    cw = lw;
 
     // The loader walks the warp's tiles (w, w + kKv8Warps, ... of each segment) up to NST - 1
     // ahead of the products, across the ends of segments.
     Kv8Seg ls;
-    int lx = x0, lj = 0, ltiles = 0, run = -1;
+    int lj = 0, ltiles = 0, run = -1;
     // Steps to the next tile and looks up the 16-key run of the pool that holds run lane % NSUB
     // of it: -1 where there is none (behind k1, or a page outside the pool).
     auto next_tile = [&]() {
         lj += kKv8Warps;
         while (lj >= ltiles) {
-            if (!kv8_next_segment(p, plan, (int)blockIdx.x, W, lx, x_end, ls)) {
+            if (!lw.next(p, plan, (int)blockIdx.x, W, ls)) {
                 ltiles = 0;
                 lj = 0;
                 grid_launch_dependents();  // only now: the merge's CTAs would take room from this grid's
                 return;
-            }
-            // the segment's queries, which are read when its products begin, on their way to L2
-            for (int i = lane; i < cols * (D / 32); i += 32) {
-                const int col = i / (D / 32);
-                const size_t row = ((size_t)ls.b * p.Sq + col / p.group) * p.Hq + ls.hk * p.group + col % p.group;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(q16 + row * D + i % (D / 32) * 32));
             }
             ltiles = (ls.k1 - ls.k0 + KT - 1) / KT;
             lj = warp;
@@ -409,9 +433,28 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         cp_async_commit();
     }
 
-    int st = 0, x = x0;
+    // Queries.  Warp w turns rows w, w + 4, ... of a segment into fragments, a lane four dims at a
+    // time; they are loaded while the segment before is joined.
+    constexpr int QU = (D / 4 + 31) / 32;
+    uint2 raw_q[HB][QU];
+    auto load_queries = [&](const Kv8Seg& s) {
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            const int c = i * 4 + warp, tok = c / p.group, h = s.hk * p.group + c - tok * p.group;
+            const uint16_t* src = q16 + (((size_t)s.b * p.Sq + tok) * p.Hq + h) * D;
+#pragma unroll
+            for (int k = 0; k < QU; ++k) {
+                const int d = (lane + 32 * k) * 4;
+                raw_q[i][k] = c < cols && d < D ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
+            }
+        }
+    };
+
+    int st = 0;
     Kv8Seg sg;
-    while (kv8_next_segment(p, plan, (int)blockIdx.x, W, x, x_end, sg)) {
+    bool more = cw.next(p, plan, (int)blockIdx.x, W, sg);
+    if (more) load_queries(sg);
+    while (more) {
         const int b = sg.b, hk = sg.hk, len = sg.len, k0 = sg.k0, k1 = sg.k1;
         const int tiles = (k1 - k0 + KT - 1) / KT;
 
@@ -419,51 +462,52 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         // multiplied by a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's
         // subnormals are then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values
         // that far below their row's largest.
-        uint2 qr[C::QRegs ? KS * NT : 1];
-        float qf[NT][E];
-        int lim[NT][E];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int c = (nt * 2 + (g & 1)) * 4 + (g >> 1);
-            const bool in = c < cols && (g & 1) < E;
-            const int tok = c / p.group, h = hk * p.group + c % p.group;
-            const uint16_t* src = q16 + (((size_t)b * p.Sq + tok) * p.Hq + h) * D;
-            uint2 w[KS];
-            float amax = 0.f;
+        for (int i = 0; i < HB; ++i) {
+            float x[QU][4], amax = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int d = ks * 16 < C::WA ? (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 : 64 + t * 8 + (ks - 4) * 4;
-                w[ks] = in ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
-                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(float_from16<kBF16>((uint16_t)w[ks].x)),
-                                               fabsf(float_from16<kBF16>((uint16_t)(w[ks].x >> 16)))),
-                                         fmaxf(fabsf(float_from16<kBF16>((uint16_t)w[ks].y)),
-                                               fabsf(float_from16<kBF16>((uint16_t)(w[ks].y >> 16))))));
+            for (int k = 0; k < QU; ++k) {
+                const uint32_t w[2] = {raw_q[i][k].x, raw_q[i][k].y};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[k][2 * e] = float_from16<kBF16>((uint16_t)w[e]);
+                    x[k][2 * e + 1] = float_from16<kBF16>((uint16_t)(w[e] >> 16));
+                    amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * e]), fabsf(x[k][2 * e + 1])));
+                }
             }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             // amax = f 2^x; the factor is 2^(13 - x), from the exponent field, kept normal
             int ex = (int)(__float_as_uint(amax) >> 23);
             ex = ex == 255 ? 127 + 13 : max(ex, 14);
             const float up = __uint_as_float((uint32_t)(254 + 13 - ex) << 23);
-            const float down = p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23);
+            if (lane == 0) s_qf[i * 4 + warp] = p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23);
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint2 f = {pack_f16x2(float_from16<kBF16>((uint16_t)w[ks].x) * up,
-                                            float_from16<kBF16>((uint16_t)(w[ks].x >> 16)) * up),
-                                 pack_f16x2(float_from16<kBF16>((uint16_t)w[ks].y) * up,
-                                            float_from16<kBF16>((uint16_t)(w[ks].y >> 16)) * up)};
-                if constexpr (C::QRegs)
-                    qr[ks * NT + nt] = f;
-                else if (warp == 0)
-                    s_q[(ks * NT + nt) * 32 + lane] = f;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                qf[nt][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
-                lim[nt][e] = p.causal ? min(k1, len - p.Sq + ((nt * 2 + e) * 4 + t) / p.group + 1) : k1;
+            for (int k = 0; k < QU; ++k) {
+                const int d = (lane + 32 * k) * 4;
+                const int ks = d < C::WA ? (d >> 6) * 4 + ((d >> 2) & 3) : 4 + ((d >> 2) & 1);
+                const int tt = d < C::WA ? (d >> 4) & 3 : ((d - 64) >> 3) & 3;
+                if (d < D)
+                    s_q[(ks * NT + (i >> 1)) * 32 + (2 * warp + (i & 1)) * 4 + tt] =
+                        make_uint2(pack_f16x2(x[k][0] * up, x[k][1] * up), pack_f16x2(x[k][2] * up, x[k][3] * up));
             }
         }
-        if constexpr (!C::QRegs) __syncthreads();
+        __syncthreads();
+        uint2 qr[C::QRegs ? KS * NT : 1];
+        if constexpr (C::QRegs) {
+#pragma unroll
+            for (int i = 0; i < KS * NT; ++i) qr[i] = E == 2 || (g & 1) == 0 ? s_q[i * 32 + lane] : make_uint2(0, 0);
+        }
+        float qf[NT][E];
+        int lim[NT][E];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = (nt * 2 + e) * 4 + t;
+                qf[nt][e] = s_qf[c];
+                lim[nt][e] = p.causal ? min(k1, len - p.Sq + c / p.group + 1) : k1;
+            }
         const int full = p.causal ? min(k1, len - p.Sq + 1) : k1;  // keys that every row sees
 
         float o[KS][NT][4], ms[NT][E], mo[NT][E], l[NT][E];
@@ -655,6 +699,10 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             __syncwarp();  // the stage may be overwritten
         }
 
+        const Kv8Seg done = sg;
+        more = cw.next(p, plan, (int)blockIdx.x, W, sg);
+        if (more) load_queries(sg);
+
         // Join the warps: per query row the maxima and sums over the lanes of one t, then the four
         // warps' through shared memory; the outputs, brought to one reference, are added up in two
         // buffers, warps 2 and 3 onto what 0 and 1 have left there.
@@ -700,7 +748,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                     }
                 }
         };
-        if (warp < 2) leave(false);
+        if (warp < 2 && warp < tiles) leave(false);
         if (tid >= 64 && tid < 64 + cols) {
             // O = (sum of the outputs) 2^(Mo - kPShift - Ms) / L.  The power is taken in two halves:
             // V scales go down to 2^-127.
@@ -719,8 +767,10 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             s_lse[col] = L == 0.f ? kNegInf : (Ms + lg2_approx(L)) * kLn2;
         }
         __syncthreads();
-        if (warp >= 2) leave(true);
-        __syncthreads();
+        if (tiles > 2) {  // else warps 2 and 3 had none
+            if (warp >= 2 && warp < tiles) leave(true);
+            __syncthreads();
+        }
         for (int i = tid; i < cols * (D / 2); i += kKv8Threads) {
             // Pair u of dims is block k, row g of the products; four threads of one g take
             // neighbouring pairs.
@@ -736,16 +786,18 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                 d = (k >> 3) * 128 + gg * 16 + (k & 7) * 2;
             }
             const float2 v0 = *reinterpret_cast<const float2*>(exch + col * XD + (k * 8 + gg) * 2);
-            const float2 v1 = *reinterpret_cast<const float2*>(exch + (HB * 4 + col) * XD + (k * 8 + gg) * 2);
+            const float2 v1 = tiles > 1
+                                  ? *reinterpret_cast<const float2*>(exch + (HB * 4 + col) * XD + (k * 8 + gg) * 2)
+                                  : make_float2(0.f, 0.f);
             const float f = s_f[col], finv = s_finv[col];
             const float a0 = (v0.x + v1.x) * finv * f, a1 = (v0.y + v1.y) * finv * f;
             const int tok = col / p.group, h = hk * p.group + col % p.group;
             const size_t row = ((size_t)b * p.Sq + tok) * p.Hq + h;
-            if (!sg.cut) {
+            if (!done.cut) {
                 *reinterpret_cast<uint32_t*>(o16 + row * D + d) = pack2<kBF16>(a0, a1);
                 if (d == 0 && p.lse) p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s_lse[col];
             } else {
-                const size_t part = (size_t)sg.slot * cols + col;
+                const size_t part = (size_t)done.slot * cols + col;
                 *reinterpret_cast<float2*>(p.o_part + part * D + d) = make_float2(a0, a1);
                 if (d == 0) p.lse_part[part] = s_lse[col];
             }
@@ -809,6 +861,7 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     const int W = kv8_width(p, sum), start = p.pool.Hkv * before + h / p.group * units;
     const int n = kv8_pieces(start, units, W), first = kv8_first_piece(start, W);
     const int cols = p.group * p.Sq, col = tok * p.group + h % p.group;
+    const int pair = b * p.pool.Hkv + h / p.group;
     grid_dependency_wait();
     grid_launch_dependents();
     // Rows with one piece or none have been written by the split kernel.  n is the same in all of
@@ -822,7 +875,7 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
 #pragma unroll
         for (int u = 0; u < NB; ++u) {  // pieces past n: the last one, with weight 0
             const int c = min(c0 + u * WPR, n - 1);
-            const size_t at = (size_t)kv8_slot(first + c, c == 0) * cols + col;
+            const size_t at = (size_t)kv8_slot(p, first + c, c == 0, pair) * cols + col;
             w[u] = p.lse_part[at];
 #pragma unroll
             for (int i = 0; i < V; ++i) v[u][i] = p.o_part[at * D + lane + i * 32];
@@ -906,14 +959,16 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     p.causal = a.causal ? 1 : 0;
     p.page_recip = (unsigned)((1ull << 32) / (unsigned)a.pool.page_size) + 1u;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    // As many ranges as CTAs are resident at once, where the workspace's slots (one partial
-    // result each of one pair) allow it: two a range.  If they allow fewer ranges than there are
-    // pairs to spread, no pair is cut.
+    // As many ranges as CTAs are resident at once, where the workspace's slots (a partial result
+    // of one pair each) allow it: ranges + min(ranges, pairs) of them.  Cutting costs a second
+    // kernel (3 us); it pays where it evens out the work of more pairs than CTAs, or cuts fewer
+    // pairs into two pieces each or more (8 pairs of 148..445 keys in 8 ranges took 11.5 us,
+    // whole 6.0).
     const int per_sm = p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::CTAS : Kv8Cfg<D, 4>::CTAS;
     const long long pairs = (long long)a.B * a.pool.Hkv, resident = (long long)per_sm * a.num_sms;
     const long long most = pairs * ((p.capacity + kKv8Unit - 1) / kKv8Unit);
-    const long long ranges = std::min({resident, most, a.slots / 2});
-    p.whole = a.slots == 0 || ranges < std::min(resident, pairs);
+    const long long ranges = std::min({resident, most, std::max(a.slots / 2, a.slots - pairs)});
+    p.whole = a.slots == 0 || ranges < std::min(resident, 2 * pairs);
     p.grid = (int)(p.whole ? std::min(resident, pairs) : ranges);
     fa_status st;
     if (p.group * p.Sq <= 4)
