@@ -85,6 +85,13 @@ __device__ __forceinline__ float float_from16(uint16_t x) {
     }
 }
 
+// Thread i prefetches 128-byte line first + i of `bytes` bytes, i < kTableLines.
+__device__ __forceinline__ void kv8_prefetch(const void* base, long long bytes, int first) {
+    const long long at = ((long long)first + threadIdx.x) * 128;
+    if (threadIdx.x < kTableLines && at < bytes)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(base) + at));
+}
+
 // The plan in shared memory: the units of one pair of each sequence summed over the
 // sequences before b, and what the last unit of b lacks to be full, so that
 // len = (units - kKv8Lead) * kKv8Unit - pad.
@@ -206,7 +213,7 @@ struct Kv8Cfg {
     static constexpr int NT = (HB + 1) / 2;     // 8-column blocks of P
     static constexpr int E = HB == 1 ? 1 : 2;   // columns of a lane in use
     static constexpr int KT = D == 256 ? 16 : 32;
-    static constexpr int NST = D == 64 ? 4 : D == 256 && NT == 1 ? 3 : 2;
+    static constexpr int NST = D == 64 || (D == 256 && NT == 1) ? 3 : 2;
     static constexpr int CTAS = D == 256 || NT == 2 ? 2 : 3;  // resident on an SM
     static constexpr int NSUB = KT / 16;  // runs of 16 keys
     static constexpr int TileBytes = KT * D;
@@ -328,14 +335,11 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     plan.prefix = reinterpret_cast<int*>(rest + C::ExchBytes + C::QBytes);
     plan.pad = reinterpret_cast<uint8_t*>(plan.prefix + p.B + 1);
 
+    // While the kernel before may still be running: the lengths and the block table, which the
+    // plan and the first copies wait for in turn, are sent for to L2 (a hint: it reads nothing).
+    kv8_prefetch(p.kv_lens, p.B * 4ll, (int)blockIdx.x * kTableLines);
+    kv8_prefetch(p.pool.table, (long long)p.B * p.pool.max_pages * 4, (int)blockIdx.x * kTableLines);
     grid_dependency_wait();
-    {
-        // The plan takes a trip to memory (kv_lens), and what it says to look up in the table would
-        // take another: the table's lines are sent for now, a few by each CTA.
-        const long long lines = ((long long)p.B * p.pool.max_pages + 31) / 32;
-        const long long line = (long long)blockIdx.x * kTableLines + tid;
-        if (tid < kTableLines && line < lines) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pool.table + line * 32));
-    }
     const int W = kv8_make_plan(p, plan);
     uint16_t* o16 = static_cast<uint16_t*>(p.o);
     const uint16_t* q16 = static_cast<const uint16_t*>(p.q);
@@ -831,6 +835,19 @@ inline bool prefer_shared(const void* f, const void* g, int* done) {
     return true;
 }
 
+template <int N>
+__device__ __forceinline__ void load_vec(float* v, const float* p) {
+    if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else if constexpr (N == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x, v[1] = x.y;
+    } else {
+        v[0] = *p;
+    }
+}
+
 // Joins the pieces of each row (b, token, head): lse = log sum_c exp(lse_c), and the outputs
 // weighted with exp(lse_c - lse).  WPR warps share a row, each taking every WPR-th piece; a
 // lane holds D / 32 dims.  It moves few bytes: its time is the launch and the dependent trips
@@ -840,7 +857,9 @@ inline bool prefer_shared(const void* f, const void* g, int* done) {
 template <int D, int WPR, bool kBF16>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     constexpr int V = D / 32, Rows = 8 / WPR, NB = V <= 4 ? 8 : 4;
-    __shared__ float s_acc[WPR > 1 ? 8 : 1][D], s_sum[8], s_max[8];
+    constexpr int Vec = V % 4 == 0 ? 4 : V % 2 == 0 ? 2 : 1;  // values of a lane side by side
+    __shared__ __align__(16) float s_acc[WPR > 1 ? 8 : 1][D];
+    __shared__ float s_sum[8], s_max[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * Rows + warp / WPR, part = warp % WPR;
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -862,8 +881,8 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     const int n = kv8_pieces(start, units, W), first = kv8_first_piece(start, W);
     const int cols = p.group * p.Sq, col = tok * p.group + h % p.group;
     const int pair = b * p.pool.Hkv + h / p.group;
-    grid_dependency_wait();
     grid_launch_dependents();
+    grid_dependency_wait();
     // Rows with one piece or none have been written by the split kernel.  n is the same in all of
     // a row's warps.
     if (row >= p.B * p.Sq * p.Hq || n < 2) return;
@@ -878,7 +897,7 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
             const size_t at = (size_t)kv8_slot(p, first + c, c == 0, pair) * cols + col;
             w[u] = p.lse_part[at];
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[u][i] = p.o_part[at * D + lane + i * 32];
+            for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
         }
 #pragma unroll
         for (int u = 0; u < NB; ++u) {
@@ -902,7 +921,7 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     }
     if constexpr (WPR > 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
+        for (int i = 0; i < V; ++i) s_acc[warp][i / Vec * Vec * 32 + lane * Vec + i % Vec] = acc[i];
         if (lane == 0) {
             s_sum[warp] = s;
             s_max[warp] = m;
@@ -920,13 +939,24 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
             const float f = ex2_approx((s_max[w] - ref) * (1.f / kLn2));
             s += f * s_sum[w];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(f, s_acc[w][lane + i * 32], acc[i]);
+            for (int i = 0; i < V; ++i)
+                acc[i] = fmaf(f, s_acc[w][i / Vec * Vec * 32 + lane * Vec + i % Vec], acc[i]);
         }
     }
     const float inv = 1.f / s;  // s == 0: no piece holds a visible key
-    uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane;
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i * 32] = float_to16<kBF16>(s == 0.f ? 0.f : acc[i] * inv);
+    for (int i = 0; i < V; ++i) acc[i] = s == 0.f ? 0.f : acc[i] * inv;
+    uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * Vec;
+#pragma unroll
+    for (int i = 0; i < V; i += Vec) {
+        if constexpr (Vec == 1)
+            out[i * 32] = float_to16<kBF16>(acc[i]);
+        else if constexpr (Vec == 2)
+            *reinterpret_cast<uint32_t*>(out + i * 32) = pack2<kBF16>(acc[i], acc[i + 1]);
+        else
+            *reinterpret_cast<uint2*>(out + i * 32) =
+                make_uint2(pack2<kBF16>(acc[i], acc[i + 1]), pack2<kBF16>(acc[i + 2], acc[i + 3]));
+    }
     if (p.lse && lane == 0)
         p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kLn2;
 }
