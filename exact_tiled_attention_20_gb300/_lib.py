@@ -422,41 +422,48 @@ def _refuse(*wanted):
 
 def _fp8_pool(k_pages, v_pages, k_scales, v_scales, block_table):
     """Checks the pool's tensors; returns (device index, num_pages, Hkv, page_size, D, B, max_pages)."""
-    for t in (k_pages, v_pages, k_scales, v_scales, block_table):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("the pool, its scales and block_table must be CUDA tensors")
-    device, shape, table = k_pages.get_device(), k_pages.shape, block_table.shape
-    if len(shape) != 4:
-        raise ValueError("k_pages must be [num_pages, Hkv, page_size, D]")
-    if len(table) != 2:
-        raise ValueError("block_table must be [B, max_pages_per_seq]")
-    rows = shape[:3]
-    if not (device >= 0 and v_pages.get_device() == device and k_scales.get_device() == device
-            and v_scales.get_device() == device and block_table.get_device() == device
-            and k_pages.dtype is _F8 and v_pages.dtype is _F8 and k_scales.dtype is _U8 and v_scales.dtype is _U8
-            and block_table.dtype is _I32 and v_pages.shape == shape and k_scales.shape == rows
-            and v_scales.shape == rows and k_pages.is_contiguous() and v_pages.is_contiguous()
-            and k_scales.is_contiguous() and v_scales.is_contiguous() and block_table.is_contiguous()):
-        _refuse(("k_pages", k_pages, _F8, device, shape), ("v_pages", v_pages, _F8, device, shape),
-                ("k_scales", k_scales, _U8, device, rows), ("v_scales", v_scales, _U8, device, rows),
-                ("block_table", block_table, _I32, device, table))
-    return (device, *shape, *table)
+    try:
+        device, shape = k_pages.get_device(), k_pages.shape
+        num_pages, Hkv, page, D = shape
+        B, max_pages = block_table.shape
+        rows = (num_pages, Hkv, page)
+        if (device >= 0 and v_pages.get_device() == device and k_scales.get_device() == device
+                and v_scales.get_device() == device and block_table.get_device() == device
+                and k_pages.dtype is _F8 and v_pages.dtype is _F8 and k_scales.dtype is _U8
+                and v_scales.dtype is _U8 and block_table.dtype is _I32 and v_pages.shape == shape
+                and k_scales.shape == rows and v_scales.shape == rows and k_pages.is_contiguous()
+                and v_pages.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous()
+                and block_table.is_contiguous()):
+            return device, num_pages, Hkv, page, D, B, max_pages
+    except (AttributeError, ValueError):  # no tensors, or of other dimensions
+        for t in (k_pages, v_pages, k_scales, v_scales, block_table):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("the pool, its scales and block_table must be CUDA tensors") from None
+        raise ValueError("k_pages must be [num_pages, Hkv, page_size, D] and block_table "
+                         "[B, max_pages_per_seq]") from None
+    _refuse(("k_pages", k_pages, _F8, device, shape), ("v_pages", v_pages, _F8, device, shape),
+            ("k_scales", k_scales, _U8, device, rows), ("v_scales", v_scales, _U8, device, rows),
+            ("block_table", block_table, _I32, device, None))
 
 
 def _is(t, dtype, device, shape):
     """Whether t is a contiguous tensor of this type and shape (None: any) on this device."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
-            and (shape is None or t.shape == shape) and t.is_contiguous())
+    try:
+        return (t.dtype is dtype and t.get_device() == device and (shape is None or t.shape == shape)
+                and t.is_contiguous())
+    except AttributeError:
+        return False
 
 
 def _stream_on(device, stream):
     """(handle of `stream` or of the device's current stream, the stream where it is not the
     current one)."""
+    current = _raw_stream(device)
     if stream is None:
-        return _raw_stream(device), None
+        return current, None
     if stream.device.index != device:
         raise ValueError(f"stream is on {stream.device}, not on cuda:{device}")
-    return stream.cuda_stream, (None if stream.cuda_stream == _raw_stream(device) else stream)
+    return stream.cuda_stream, (None if stream.cuda_stream == current else stream)
 
 
 def _made(t, other):
