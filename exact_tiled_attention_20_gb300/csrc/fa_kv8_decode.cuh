@@ -55,7 +55,7 @@ __device__ __forceinline__ int kv8_units(int len) {
 
 // W, from the units of one pair of each sequence summed.
 __device__ __forceinline__ int kv8_width(const Kv8DecParams& p, int sum_units) {
-    return max((int)(((long long)p.pool.Hkv * sum_units + p.grid - 1) / p.grid), 1);
+    return max((int)(((unsigned)(p.pool.Hkv * sum_units) + (unsigned)p.grid - 1u) / (unsigned)p.grid), 1);
 }
 
 // The ranges that hold keys of the pair of `units` units beginning at unit `start`: the first
