@@ -14,6 +14,9 @@
 // before it and one that goes on behind it: the partial results fill a slot for each range
 // and one more for each range or for each pair, whichever are fewer, whatever the number of
 // pieces.  Without room for that (`whole`), a CTA takes the pairs that begin in its range, uncut.
+// Where every sequence is short and there are many pairs (`solo`), each warp has a range of
+// its own and takes whole pairs: a pair of a few tiles gives four warps little to share, and
+// joining them costs as much as the tiles.
 #pragma once
 
 #include <algorithm>
@@ -31,6 +34,7 @@ struct Kv8DecParams {
     float* o_part;    // [slots, group * Sq, D]
     float* lse_part;  // [slots, group * Sq]
     int B, Sq, Hq, group, capacity, causal, whole;
+    int solo_keys;  // the longest sequence of a batch whose pairs warps take alone; 0: none
     int grid;  // ranges, and CTAs of the split kernel
     unsigned page_recip;  // floor(2^32 / page_size) + 1
     float scale_log2;
@@ -53,9 +57,14 @@ __device__ __forceinline__ int kv8_units(int len) {
     return len > 0 ? (len + kKv8Unit - 1) / kKv8Unit + kKv8Lead : 0;
 }
 
-// W, from the units of one pair of each sequence summed.
-__device__ __forceinline__ int kv8_width(const Kv8DecParams& p, int sum_units) {
-    return max((int)(((unsigned)(p.pool.Hkv * sum_units) + (unsigned)p.grid - 1u) / (unsigned)p.grid), 1);
+// Whether warps take pairs alone, from the units of one pair of the longest sequence.
+__device__ __forceinline__ bool kv8_solo(const Kv8DecParams& p, int max_units) {
+    return p.solo_keys > 0 && max_units <= p.solo_keys / kKv8Unit + kKv8Lead;
+}
+
+// W for so many ranges, from the units of one pair of each sequence summed.
+__device__ __forceinline__ int kv8_width(const Kv8DecParams& p, int sum_units, int ranges) {
+    return max((int)(((unsigned)(p.pool.Hkv * sum_units) + (unsigned)ranges - 1u) / (unsigned)ranges), 1);
 }
 
 // The ranges that hold keys of the pair of `units` units beginning at unit `start`: the first
@@ -101,12 +110,13 @@ struct Kv8Plan {
     static __host__ __device__ constexpr int bytes(int B) { return (B + 1) * 4 + ((B + 15) & ~15); }
 };
 
-// Fills the plan from kv_lens (all threads; ends with a barrier) and returns W.
+// Fills the plan from kv_lens (all threads; ends with a barrier); returns the units of one pair of
+// the longest sequence.
 __device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Plan& t) {
-    __shared__ int warp_sum[kKv8Warps];
+    __shared__ int warp_sum[kKv8Warps], warp_max[kKv8Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.B + kKv8Threads - 1) / kKv8Threads;
-    int sum = 0;
+    int sum = 0, most = 0;
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
         if (b < p.B) {
@@ -114,6 +124,7 @@ __device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Pla
             t.prefix[b] = units;
             t.pad[b] = (uint8_t)(len > 0 ? (units - kKv8Lead) * kKv8Unit - len : 0);
             sum += units;
+            most = max(most, units);
         }
     }
     int incl = sum;
@@ -121,11 +132,18 @@ __device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Pla
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) {
+        warp_sum[warp] = incl;
+        warp_max[warp] = most;
+    }
     __syncthreads();
     int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += warp_sum[w];
+    for (int w = 0; w < kKv8Warps; ++w) {
+        if (w < warp) run += warp_sum[w];
+        most = max(most, warp_max[w]);
+    }
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
         if (b < p.B) {
@@ -136,7 +154,7 @@ __device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Pla
     }
     if (threadIdx.x == kKv8Threads - 1) t.prefix[p.B] = run;
     __syncthreads();
-    return kv8_width(p, t.prefix[p.B]);
+    return most;
 }
 
 // The part of one pair that lies in one range.
@@ -150,8 +168,10 @@ struct Kv8Seg {
 struct Kv8Walk {
     int x, x_end;
     int b, hk, start, units;  // the pair that holds unit x, or ends there
+    bool whole;
 
-    __device__ __forceinline__ void init(const Kv8DecParams& p, const Kv8Plan& t, int rng, int W) {
+    __device__ __forceinline__ void init(const Kv8DecParams& p, const Kv8Plan& t, int rng, int W, bool whole_) {
+        whole = whole_;
         const int Hkv = p.pool.Hkv, total = Hkv * t.prefix[p.B];
         x = (int)min((long long)rng * W, (long long)total);
         x_end = (int)min((long long)x + W, (long long)total);
@@ -180,18 +200,18 @@ struct Kv8Walk {
                     } while (units == 0);
                 }
             }
-            if (p.whole && x > start) {  // the range before has it
+            if (whole && x > start) {  // the range before has it
                 x = start + units;
                 continue;
             }
-            const int end = p.whole ? start + units : min(x_end, start + units);
+            const int end = whole ? start + units : min(x_end, start + units);
             s.b = b;
             s.hk = hk;
             s.len = (units - kKv8Lead) * kKv8Unit - t.pad[b];
             s.k0 = max(x - start - kKv8Lead, 0) * kKv8Unit;
             s.k1 = min((end - start - kKv8Lead) * kKv8Unit, s.len);
             s.slot = kv8_slot(p, rng, rng == kv8_first_piece(start, W), b * p.pool.Hkv + hk);
-            s.cut = !p.whole && kv8_pieces(start, units, W) > 1;
+            s.cut = !whole && kv8_pieces(start, units, W) > 1;
             x = end;
             if (s.k1 > s.k0) return true;  // else the range ends within the lead
         }
@@ -226,9 +246,10 @@ struct Kv8Cfg {
     // Query fragments stay in registers or, where they are too many, in shared memory; they are
     // made there, in the exchange's room if they do not stay.
     static constexpr bool QRegs = D / 16 * NT <= 16;
-    static constexpr int QStage = D / 16 * NT * 32 * 8;
+    static constexpr int QLanes = 16 * E;  // lanes that hold a query fragment: with E = 1 those of even g
+    static constexpr int QStage = D / 16 * NT * QLanes * 8;
     static constexpr int QBytes = QRegs ? 0 : QStage;
-    static_assert(!QRegs || QStage <= ExchBytes, "queries fit the exchange");
+    static_assert(!QRegs || kKv8Warps * QStage <= ExchBytes, "each warp's queries fit the exchange");
     static constexpr int FixedBytes = 128 + kKv8Warps * (RingBytes + ScaleBytes) + ExchBytes + QBytes;
     static constexpr int WA = D == 96 ? 64 : D;
     static constexpr int KS = D / 16;        // steps of 16 dims, and 16-dim blocks of O^T
@@ -321,7 +342,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS, XD = C::XD, NT = C::NT, E = C::E;
     extern __shared__ uint8_t smem_raw[];
     __shared__ float s_mo[kKv8Warps][16], s_ms[kKv8Warps][16], s_l[kKv8Warps][16];
-    __shared__ float s_f[16], s_finv[16], s_lse[16], s_qf[16];
+    __shared__ float s_f[16], s_finv[16], s_lse[16], s_qfs[kKv8Warps][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -330,7 +351,6 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     const uint32_t scales = base + kKv8Warps * C::RingBytes + warp * C::ScaleBytes;
     uint8_t* rest = smem_raw + (base - raw) + kKv8Warps * (C::RingBytes + C::ScaleBytes);
     float* exch = reinterpret_cast<float*>(rest);
-    uint2* s_q = reinterpret_cast<uint2*>(C::QRegs ? rest : rest + C::ExchBytes);
     Kv8Plan plan;
     plan.prefix = reinterpret_cast<int*>(rest + C::ExchBytes + C::QBytes);
     plan.pad = reinterpret_cast<uint8_t*>(plan.prefix + p.B + 1);
@@ -340,7 +360,20 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     kv8_prefetch(p.kv_lens, p.B * 4ll, (int)blockIdx.x * kTableLines);
     kv8_prefetch(p.pool.table, (long long)p.B * p.pool.max_pages * 4, (int)blockIdx.x * kTableLines);
     grid_dependency_wait();
-    const int W = kv8_make_plan(p, plan);
+    // A group of gw warps works through a range; this is warp wi of it.
+    const int most = kv8_make_plan(p, plan);
+    const bool solo = C::QRegs && kv8_solo(p, most);
+    const int gw = solo ? 1 : kKv8Warps, wi = solo ? 0 : warp;
+    const int rng = solo ? (int)blockIdx.x * kKv8Warps + warp : (int)blockIdx.x;
+    const int W = kv8_width(p, plan.prefix[p.B], solo ? p.grid * kKv8Warps : p.grid);
+    auto group_sync = [&]() {
+        if (solo)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
+    uint2* s_q = reinterpret_cast<uint2*>(C::QRegs ? rest + (solo ? warp * C::QStage : 0) : rest + C::ExchBytes);
+    float* s_qf = s_qfs[solo ? warp : 0];
     uint16_t* o16 = static_cast<uint16_t*>(p.o);
     const uint16_t* q16 = static_cast<const uint16_t*>(p.q);
     const int rows = p.Sq * p.Hq;
@@ -361,26 +394,26 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     }
     const int Hkv = p.pool.Hkv, cols = p.group * p.Sq;
     Kv8Walk lw, cw;  // the loader's and the products'
-    lw.init(p, plan, (int)blockIdx.x, W);
+    lw.init(p, plan, rng, W, p.whole || solo);
     cw = lw;
 
-    // The loader walks the warp's tiles (w, w + kKv8Warps, ... of each segment) up to NST - 1
+    // The loader walks the warp's tiles (wi, wi + gw, ... of each segment) up to NST - 1
     // ahead of the products, across the ends of segments.
     Kv8Seg ls;
     int lj = 0, ltiles = 0, run = -1;
     // Steps to the next tile and looks up the 16-key run of the pool that holds run lane % NSUB
     // of it: -1 where there is none (behind k1, or a page outside the pool).
     auto next_tile = [&]() {
-        lj += kKv8Warps;
+        lj += gw;
         while (lj >= ltiles) {
-            if (!lw.next(p, plan, (int)blockIdx.x, W, ls)) {
+            if (!lw.next(p, plan, rng, W, ls)) {
                 ltiles = 0;
                 lj = 0;
                 grid_launch_dependents();  // only now: the merge's CTAs would take room from this grid's
                 return;
             }
             ltiles = (ls.k1 - ls.k0 + KT - 1) / KT;
-            lj = warp;
+            lj = wi;
         }
         const int key = ls.k0 + lj * KT + (lane % NSUB) * 16;
         run = -1;
@@ -437,14 +470,15 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         cp_async_commit();
     }
 
-    // Queries.  Warp w turns rows w, w + 4, ... of a segment into fragments, a lane four dims at a
-    // time; they are loaded while the segment before is joined.
+    // Queries.  Warp w turns rows w, w + 4, ... of a segment into fragments (a warp alone all of
+    // them, four rows at a time), a lane four dims at a time; they are loaded while the segment
+    // before is joined.
     constexpr int QU = (D / 4 + 31) / 32;
     uint2 raw_q[HB][QU];
-    auto load_queries = [&](const Kv8Seg& s) {
+    auto load_queries = [&](const Kv8Seg& s, int w, uint2 (&raw_q)[HB][QU]) {
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
-            const int c = i * 4 + warp, tok = c / p.group, h = s.hk * p.group + c - tok * p.group;
+            const int c = i * 4 + w, tok = c / p.group, h = s.hk * p.group + c - tok * p.group;
             const uint16_t* src = q16 + (((size_t)s.b * p.Sq + tok) * p.Hq + h) * D;
 #pragma unroll
             for (int k = 0; k < QU; ++k) {
@@ -453,29 +487,21 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             }
         }
     };
-
-    int st = 0;
-    Kv8Seg sg;
-    bool more = cw.next(p, plan, (int)blockIdx.x, W, sg);
-    if (more) load_queries(sg);
-    while (more) {
-        const int b = sg.b, hk = sg.hk, len = sg.len, k0 = sg.k0, k1 = sg.k1;
-        const int tiles = (k1 - k0 + KT - 1) / KT;
-
-        // Query fragments as f16, column 2 t + e of block nt being row (2 nt + e) * 4 + t.  A row is
-        // multiplied by a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's
-        // subnormals are then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values
-        // that far below their row's largest.
+    // Fragments as f16, column 2 t + e of block nt being row (2 nt + e) * 4 + t.  A row is multiplied by
+    // a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's subnormals are
+    // then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values that far below their
+    // row's largest.
+    auto make_fragments = [&](int w, const uint2 (&raw_q)[HB][QU]) {
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
             float x[QU][4], amax = 0.f;
 #pragma unroll
             for (int k = 0; k < QU; ++k) {
-                const uint32_t w[2] = {raw_q[i][k].x, raw_q[i][k].y};
+                const uint32_t r[2] = {raw_q[i][k].x, raw_q[i][k].y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[k][2 * e] = float_from16<kBF16>((uint16_t)w[e]);
-                    x[k][2 * e + 1] = float_from16<kBF16>((uint16_t)(w[e] >> 16));
+                    x[k][2 * e] = float_from16<kBF16>((uint16_t)r[e]);
+                    x[k][2 * e + 1] = float_from16<kBF16>((uint16_t)(r[e] >> 16));
                     amax = fmaxf(amax, fmaxf(fabsf(x[k][2 * e]), fabsf(x[k][2 * e + 1])));
                 }
             }
@@ -485,22 +511,48 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             int ex = (int)(__float_as_uint(amax) >> 23);
             ex = ex == 255 ? 127 + 13 : max(ex, 14);
             const float up = __uint_as_float((uint32_t)(254 + 13 - ex) << 23);
-            if (lane == 0) s_qf[i * 4 + warp] = p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23);
+            if (lane == 0) s_qf[i * 4 + w] = p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23);
 #pragma unroll
             for (int k = 0; k < QU; ++k) {
                 const int d = (lane + 32 * k) * 4;
                 const int ks = d < C::WA ? (d >> 6) * 4 + ((d >> 2) & 3) : 4 + ((d >> 2) & 1);
                 const int tt = d < C::WA ? (d >> 4) & 3 : ((d - 64) >> 3) & 3;
-                if (d < D)
-                    s_q[(ks * NT + (i >> 1)) * 32 + (2 * warp + (i & 1)) * 4 + tt] =
+                if (d < D)  // of lane 4 g + tt, g = 2 w + i % 2
+                    s_q[(ks * NT + (i >> 1)) * C::QLanes + (E * w + (i & 1)) * 4 + tt] =
                         make_uint2(pack_f16x2(x[k][0] * up, x[k][1] * up), pack_f16x2(x[k][2] * up, x[k][3] * up));
             }
         }
-        __syncthreads();
+    };
+    // This lane's fragment: step ks, block nt.
+    auto fragment = [&](int ks, int nt) -> uint2 {
+        if constexpr (E == 2)
+            return s_q[(ks * NT + nt) * C::QLanes + lane];
+        else
+            return (g & 1) == 0 ? s_q[(ks * NT + nt) * C::QLanes + (g >> 1) * 4 + t] : make_uint2(0, 0);
+    };
+
+    int st = 0;
+    Kv8Seg sg;
+    bool more = cw.next(p, plan, rng, W, sg);
+    if (more && !solo) load_queries(sg, warp, raw_q);
+    while (more) {
+        const int b = sg.b, hk = sg.hk, len = sg.len, k0 = sg.k0, k1 = sg.k1;
+        const int tiles = (k1 - k0 + KT - 1) / KT;
+
+        if (!solo) {
+            make_fragments(warp, raw_q);
+        } else {
+            uint2 all[kKv8Warps][HB][QU];
+#pragma unroll
+            for (int w = 0; w < kKv8Warps; ++w) load_queries(sg, w, all[w]);
+#pragma unroll
+            for (int w = 0; w < kKv8Warps; ++w) make_fragments(w, all[w]);
+        }
+        group_sync();
         uint2 qr[C::QRegs ? KS * NT : 1];
         if constexpr (C::QRegs) {
 #pragma unroll
-            for (int i = 0; i < KS * NT; ++i) qr[i] = E == 2 || (g & 1) == 0 ? s_q[i * 32 + lane] : make_uint2(0, 0);
+            for (int i = 0; i < KS * NT; ++i) qr[i] = fragment(i / NT, i % NT);
         }
         float qf[NT][E];
         int lim[NT][E];
@@ -528,7 +580,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             }
         }
 
-        for (int j = warp; j < tiles; j += kKv8Warps) {
+        for (int j = wi; j < tiles; j += gw) {
             cp_async_wait<NST - 2>();
             __syncwarp();
             if (lj < ltiles) {
@@ -561,7 +613,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                         if constexpr (C::QRegs)
                             q = qr[ks * NT + nt];
                         else
-                            q = s_q[(ks * NT + nt) * 32 + lane];
+                            q = fragment(ks, nt);
                         mma_16816(acc[ks & 1][nt], a0, a1, a2, a3, q.x, q.y);
                     }
                 };
@@ -704,12 +756,11 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         }
 
         const Kv8Seg done = sg;
-        more = cw.next(p, plan, (int)blockIdx.x, W, sg);
-        if (more) load_queries(sg);
+        more = cw.next(p, plan, rng, W, sg);
+        if (more && !solo) load_queries(sg, warp, raw_q);
 
-        // Join the warps: per query row the maxima and sums over the lanes of one t, then the four
-        // warps' through shared memory; the outputs, brought to one reference, are added up in two
-        // buffers, warps 2 and 3 onto what 0 and 1 have left there.
+        // Per query row the maxima and sums over the lanes of one t.
+        float m_all[NT][E], sum_all[NT][E];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -720,13 +771,52 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                 float sum = l[nt][e] * ex2_approx(ms[nt][e] - m);
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                if (g == 0) {
+                m_all[nt][e] = m;
+                sum_all[nt][e] = sum;
+            }
+        // O = (sum of the outputs) 2^(Mo - kPShift - Ms) / L.  The power is taken in two halves, f and
+        // f / L: V scales go down to 2^-127.  L = 0: no visible key, and O = 0.
+        auto half_power = [](float Mo, float Ms) { return ex2_approx((Mo - kPShift - Ms) * 0.5f); };
+        auto log_sum = [](float Ms, float L) {
+            return L == 0.f ? -__int_as_float(0x7f800000) : (Ms + lg2_approx(L)) * kLn2;
+        };
+        if (solo) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int col = (nt * 2 + e) * 4 + t;
+                    if (col >= cols) continue;
+                    const float L = sum_all[nt][e], f = half_power(mo[nt][e], m_all[nt][e]);
+                    const float finv = L == 0.f ? 0.f : f / L;
+                    const int tok = col / p.group, h = hk * p.group + col % p.group;
+                    const size_t row = ((size_t)b * p.Sq + tok) * p.Hq + h;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const int d = C::WA == 64 ? (k < 4 ? g * 8 + k * 2 : 64 + g * 4 + (k - 4) * 2)
+                                                  : (k >> 3) * 128 + g * 16 + (k & 7) * 2;
+                        *reinterpret_cast<uint32_t*>(o16 + row * D + d) =
+                            pack2<kBF16>(o[k][nt][e] * finv * f, o[k][nt][2 + e] * finv * f);
+                    }
+                    if (g == 0 && p.lse)
+                        p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = log_sum(m_all[nt][e], L);
+                }
+            __syncwarp();  // before the next pair's queries
+            continue;
+        }
+        // Join the four warps through shared memory; the outputs, brought to one reference, are added
+        // up in two buffers, warps 2 and 3 onto what 0 and 1 have left there.
+        if (g == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
                     const int col = (nt * 2 + e) * 4 + t;
                     s_mo[warp][col] = mo[nt][e];
-                    s_ms[warp][col] = m;
-                    s_l[warp][col] = sum;
+                    s_ms[warp][col] = m_all[nt][e];
+                    s_l[warp][col] = sum_all[nt][e];
                 }
-            }
+        }
         __syncthreads();
         auto leave = [&](bool add) {
 #pragma unroll
@@ -754,8 +844,6 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         };
         if (warp < 2 && warp < tiles) leave(false);
         if (tid >= 64 && tid < 64 + cols) {
-            // O = (sum of the outputs) 2^(Mo - kPShift - Ms) / L.  The power is taken in two halves:
-            // V scales go down to 2^-127.
             const int col = tid - 64;
             float Mo = s_mo[0][col], Ms = s_ms[0][col], L = 0.f;
 #pragma unroll
@@ -765,10 +853,10 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             }
 #pragma unroll
             for (int w = 0; w < kKv8Warps; ++w) L = fmaf(ex2_approx(s_ms[w][col] - Ms), s_l[w][col], L);
-            const float f = ex2_approx((Mo - kPShift - Ms) * 0.5f);
+            const float f = half_power(Mo, Ms);
             s_f[col] = f;
-            s_finv[col] = L == 0.f ? 0.f : f / L;  // no visible key: O = 0
-            s_lse[col] = L == 0.f ? kNegInf : (Ms + lg2_approx(L)) * kLn2;
+            s_finv[col] = L == 0.f ? 0.f : f / L;
+            s_lse[col] = log_sum(Ms, L);
         }
         __syncthreads();
         if (tiles > 2) {  // else warps 2 and 3 had none
@@ -864,21 +952,23 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     const int row = blockIdx.x * Rows + warp / WPR, part = warp % WPR;
     const float kNegInf = -__int_as_float(0x7f800000);
     const int b = row / (p.Sq * p.Hq), tok = row / p.Hq % p.Sq, h = row % p.Hq;
-    int before = 0, sum = 0, units = 0;
+    int before = 0, sum = 0, units = 0, most = 0;
     for (int i = lane; i < p.B; i += 32) {
         const int t = kv8_units(kv8_len(p, i));
         before += i < b ? t : 0;
         units += i == b ? t : 0;
         sum += t;
+        most = max(most, t);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         before += __shfl_xor_sync(0xffffffffu, before, o);
         units += __shfl_xor_sync(0xffffffffu, units, o);
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    const int W = kv8_width(p, sum), start = p.pool.Hkv * before + h / p.group * units;
-    const int n = kv8_pieces(start, units, W), first = kv8_first_piece(start, W);
+    const int W = kv8_width(p, sum, p.grid), start = p.pool.Hkv * before + h / p.group * units;
+    const int n = kv8_solo(p, most) ? 1 : kv8_pieces(start, units, W), first = kv8_first_piece(start, W);
     const int cols = p.group * p.Sq, col = tok * p.group + h % p.group;
     const int pair = b * p.pool.Hkv + h / p.group;
     grid_launch_dependents();
@@ -1000,6 +1090,14 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     const long long ranges = std::min({resident, most, std::max(a.slots / 2, a.slots - pairs)});
     p.whole = a.slots == 0 || ranges < std::min(resident, 2 * pairs);
     p.grid = (int)(p.whole ? std::min(resident, pairs) : ranges);
+    // A warp alone needs no join, but its tiles come one after another: better while they are few
+    // and the pairs many.  Measured, in microseconds with CTAs and with warps, D = 128 where not
+    // said: 2048 pairs of 64 keys 18.5, 13.0, of 10..320 32.2, 27.8, of 10..500 38.1, 39.6 (D = 64);
+    // 1600 of 10..120, D = 256, 24.1, 22.0, of 10..500 43.4, 57.1; 488 of 4, D = 64, 10.0, 7.8; 512
+    // of 1..512 15.3, 24.0.
+    p.solo_keys = 0;
+    if (p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::QRegs : Kv8Cfg<D, 4>::QRegs)
+        p.solo_keys = pairs >= 2ll * p.grid ? (D == 256 ? 128 : 320) : pairs > p.grid ? 128 : 0;
     fa_status st;
     if (p.group * p.Sq <= 4)
         st = a.bf16 ? launch_kv8_split<D, 1, true>(p, s) : launch_kv8_split<D, 1, false>(p, s);

@@ -419,6 +419,18 @@ def test_decode_many_sequences(fa):
     _decode_case(fa, 64, 2, 1, 1, 16, lens)
 
 
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("group,Sq,longest,ns", [(1, 1, 320, 0), (4, 1, 321, 0), (3, 2, 128, 0), (5, 3, 129, 0),
+                                                 (2, 1, 90, 1), (15, 1, 320, 0)])
+def test_decode_many_short_pairs(fa, D, group, Sq, longest, ns):
+    """960 pairs, all short: the kernel may give each warp pairs of its own. Empty sequences among
+    them, lengths at and one past the longest that form takes."""
+    rng = np.random.default_rng(D)
+    lens = (rng.integers(0, 60, 80) * (rng.random(80) < 0.8)).tolist()
+    lens[7], lens[-1] = longest, 33
+    _decode_case(fa, D, group * 12, 12, Sq, 16, lens, ns=ns, seed=group)
+
+
 def test_decode_contiguous_cache_is_one_page_each(fa):
     """page_size = the whole capacity and an identity table: the same bits as small pages."""
     pool, q, o, lse = _decode_case(fa, 96, 4, 2, 2, 16, [300, 222], ns=5)
