@@ -96,7 +96,9 @@ inline fa_status launch_overlapped(void (*kern)(P...), unsigned grid, unsigned b
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return FA_OK;
+    cudaGetLastError();  // reported here, not by the caller's next call
+    return FA_ERR_CUDA;
 }
 
 // Everything that earlier kernels of the stream wrote is visible after this.

@@ -101,8 +101,8 @@ fa_status fa_decode_splitkv_paged_fp8(const void* q, const void* k_pages, const 
     const fa_status chk =
         decode_check_args(q, k_pages, v_pages, kv_lens, o, lse, B, Sq, Hq, Hkv, D, capacity, scale, dtype);
     if (chk != FA_OK) return chk;
-    // The plan counts 64-key units, and one more for each (sequence, kv head) pair, in 32 bits.
-    if ((long long)B * Hkv > 0x7fffffffLL / (capacity / 64 + 2)) return FA_ERR_UNSUPPORTED;
+    // The plan counts 64-key units, and a few more for each (sequence, kv head) pair, in 32 bits.
+    if ((long long)B * Hkv > 0x7fffffffLL / (capacity / 64 + 8)) return FA_ERR_UNSUPPORTED;
     if ((long long)B * Sq * Hq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const int sms = device_sms();
     if (sms <= 0) return FA_ERR_CUDA;

@@ -49,7 +49,7 @@ constexpr int kTableLines = 8;  // lines of the block table that a CTA prefetche
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ int kv8_len(const Kv8DecParams& p, int b) {
-    return min(max(p.kv_lens[b], 0), p.capacity);
+    return min(max(__ldcg(p.kv_lens + b), 0), p.capacity);  // past L1: the merge reads it early
 }
 
 // Units of one pair of a sequence.

@@ -245,9 +245,10 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void *q, const void *k_cache,
  * page_size * max_pages_per_seq <= 2^31 - 4096; num_pages * Hkv * page_size / 16 < 2^31; the
  * pools and scales are 16-byte aligned.  Table
  * entries outside [0, num_pages) that a call meets are the caller's error: nothing is read
- * or written outside the pool (what happens instead is said at each call).  A contiguous
- * cache of Smax keys per sequence is the pool with page_size = Smax and block_table[b][0]
- * = b.  `dtype` is the type of the 16-bit side; rows may be written in one and read or
+ * or written outside the pool (what happens instead is said at each call).  Outputs and the
+ * workspace must not overlap the inputs.  A contiguous
+ * cache of Smax keys per sequence (a multiple of 16) is the pool with page_size = Smax and
+ * block_table[b][0] = b.  `dtype` is the type of the 16-bit side; rows may be written in one and read or
  * attended over in the other.
  *
  * fa_kv_append_paged_fp8 quantises new rows as it writes them.

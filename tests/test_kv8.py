@@ -553,6 +553,28 @@ def test_captured_step_replays_with_new_lengths(fa):
     _same(pool.host(), ref)
 
 
+def test_captured_split_decode_follows_the_lengths(fa):
+    """Sequences cut into many pieces, the lengths moved on inside the graph: each replay gives the
+    bits of an eager call with its lengths (the merge plans from the new ones too)."""
+    rng = np.random.default_rng(11)
+    pool = Pool(2 * 40, 2, 32, 128, 2, 40, seed=16)
+    pool.fill(rng, [1200, 1100])
+    q = torch.from_numpy(rng.standard_normal((2, 1, 8, 128))).to(torch.bfloat16).to(DEV)
+    kl = _int([1000, 60])
+    ws = torch.empty(fa.fa_decode_workspace_bytes(2, 8, 128, 16), dtype=torch.uint8, device=DEV)
+    o, lse = torch.empty_like(q), torch.empty(2, 8, 1, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        kl.add_(33)
+        fa.fa_decode_splitkv_paged_fp8(q, *pool.args, kl, num_splits=16, workspace=ws, out=o, lse=lse)
+    for i in range(1, 5):
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = fa.fa_decode_splitkv_paged_fp8(q, *pool.args, _int([1000 + 33 * i, 60 + 33 * i]), num_splits=16)
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
 def test_two_streams_at_once(fa):
     """Two decodes with a workspace each on two streams give what each gives alone."""
     pool, q, o, lse = _decode_case(fa, 128, 8, 2, 1, 16, [1800, 900], ns=16, seed=6)

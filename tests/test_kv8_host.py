@@ -56,7 +56,8 @@ def test_read_refuses(lib, change, code):
     (dict(q=None), INVALID), (dict(q=FAKE + 2), INVALID), (dict(o=None), INVALID), (dict(o=FAKE + 8), INVALID),
     (dict(lse=FAKE + 2), INVALID), (dict(lens=None), INVALID), (dict(Sq=0), INVALID), (dict(Hq=0), INVALID),
     (dict(Hq=12), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
-    (dict(Hq=136), UNSUPPORTED), (dict(Sq=9), UNSUPPORTED)])
+    (dict(Hq=136), UNSUPPORTED), (dict(Sq=9), UNSUPPORTED),
+    (dict(B=1024, Hq=1 << 10, Hkv=1 << 10, max_pages=1 << 13), UNSUPPORTED)])
 def test_decode_refuses(lib, change, code):
     assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **change}.values()) == code
 
