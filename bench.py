@@ -69,6 +69,9 @@ CASES = """\
   --case decode_workload [iters] [D]          the decode workload (its lengths at head dim D,
                                               default 128), default split count
   --case decode_paged_workload [iters]        the same in 256-key pages, random page order
+  --case decode_fp8_workload [iters] [D]      the same from an 8-bit cache in 256-key pages; likewise
+  --case append_fp8_workload [iters] [D]      the write of its rows into that cache, and
+  --case read_fp8_workload [iters] [D]        their read back as bf16
 """
 
 
@@ -1049,6 +1052,32 @@ def run_case(argv):
             kp, vp, table = (t.to(dev) for t in inputs.paged_layout(kh, vh, page=256))
             call = lambda: fa.fa_decode_splitkv_paged(q, kp, vp, table, lens, num_splits=ns,  # noqa: E731
                                                       workspace=ws, out=o)
+    elif kind in ("decode_fp8_workload", "append_fp8_workload", "read_fp8_workload"):
+        iters = int(rest[0]) if rest else 3
+        w, d, page = inputs.DECODE, int(rest[1]) if len(rest) > 1 else inputs.DECODE.D, 256
+        # the workload's lengths: the first draw of its recipe
+        lens_h = torch.randint(w.len_lo, w.len_hi + 1, (w.B,), generator=torch.Generator("cpu").manual_seed(w.seed))
+        lens = lens_h.to(torch.int32).to(dev)
+        cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens_h.cumsum(0)]).to(torch.int32).to(dev)
+        total, mp = int(lens_h.sum()), w.Smax // page
+        table = torch.randperm(w.B * mp, device=dev, generator=g).to(torch.int32).view(w.B, mp)
+        pages = [torch.zeros(w.B * mp, w.Hkv, page, d, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+                 for _ in range(2)]
+        scales = [torch.zeros(w.B * mp, w.Hkv, page, dtype=torch.uint8, device=dev) for _ in range(2)]
+        k, v = rnd(total, w.Hkv, d), rnd(total, w.Hkv, d)
+        pool = (*pages, *scales, table)
+        fa.fa_kv_append_paged_fp8(k, v, *pool, lens, cu_seqlens_new=cu)
+        if kind == "append_fp8_workload":
+            call = lambda: fa.fa_kv_append_paged_fp8(k, v, *pool, lens, cu_seqlens_new=cu)  # noqa: E731
+        elif kind == "read_fp8_workload":
+            call = lambda: fa.fa_kv_read_paged_fp8(*pool, cu, k_out=k, v_out=v)  # noqa: E731
+        else:
+            ns = fa.fa_decode_default_splits(w.B, w.Hkv, w.Smax)
+            ws = torch.empty(fa.fa_decode_workspace_bytes(w.B, w.Hq, d, ns), dtype=torch.uint8, device=dev)
+            q = rnd(w.B, 1, w.Hq, d)
+            o, lse = torch.empty_like(q), torch.empty(w.B, w.Hq, 1, device=dev)
+            call = lambda: fa.fa_decode_splitkv_paged_fp8(q, *pool, lens, num_splits=ns, workspace=ws,  # noqa: E731
+                                                          out=o, lse=lse)
     else:
         raise SystemExit(f"unknown case {kind!r}; kinds:\n" + CASES)
     call()

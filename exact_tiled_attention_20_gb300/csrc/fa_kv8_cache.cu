@@ -13,11 +13,10 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxB = 1024;
 
-// Where a packed row's token lies in the pool: (page, slot); page -1: nowhere in the pool,
-// -2: the row belongs to no sequence.
-struct TokenAt {
-    int page, slot;
-};
+// Where a packed row's token lies: the pool's row of its head 0 (head h is h * page_size rows on),
+// or one of these.
+constexpr long long kNoPlace = -1;     // outside the table's capacity or the pool
+constexpr long long kNoSequence = -2;  // the row belongs to no sequence
 
 // The sequence that owns packed row t: the first b with cu[b + 1] > t.
 __device__ __forceinline__ int sequence_of(const int* cu, int B, int t) {
@@ -29,12 +28,12 @@ __device__ __forceinline__ int sequence_of(const int* cu, int B, int t) {
     return lo;
 }
 
-__device__ __forceinline__ TokenAt token_at(const Kv8Pool& p, int b, long long key) {
-    if (key < 0 || key >= (long long)p.page_size * p.max_pages) return {-1, 0};
+__device__ __forceinline__ long long place_of(const Kv8Pool& p, int b, long long key) {
+    if (key < 0 || key >= (long long)p.page_size * p.max_pages) return kNoPlace;
     const int i = (int)key / p.page_size;
     const int page = p.table[(size_t)b * p.max_pages + i];
-    if (page < 0 || page >= p.num_pages) return {-1, 0};
-    return {page, (int)key - i * p.page_size};
+    if (page < 0 || page >= p.num_pages) return kNoPlace;
+    return (long long)page * p.Hkv * p.page_size + ((int)key - i * p.page_size);
 }
 
 // A 16-byte load of data that is read once.
@@ -89,10 +88,9 @@ __device__ __forceinline__ uint32_t lane_max(const uint4& w) {
     return max_abs2<kBF16>(max_abs2<kBF16>(w.x, w.y), max_abs2<kBF16>(w.z, w.w));
 }
 
-// A word's two values, times `inv`, as codes.
+// A word's two values in fp32.
 template <bool kBF16>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, float inv) {
-    float lo, hi;
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
     if constexpr (kBF16) {
         lo = __uint_as_float(w << 16);
         hi = __uint_as_float(w & 0xffff0000u);
@@ -101,27 +99,39 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w, float inv) {
             : "=f"(lo), "=f"(hi)
             : "r"(w));
     }
-    return e4m3x2_from_floats(lo * inv, hi * inv);
+}
+
+// The codes of two words' four values times `inv`.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t codes4(uint32_t x, uint32_t y, float inv) {
+    float a, b, c, d;
+    unpack2<kBF16>(x, a, b);
+    unpack2<kBF16>(y, c, d);
+    uint32_t r;
+    asm("{\n.reg .b16 p, q;\ncvt.rn.satfinite.e4m3x2.f32 p, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 q, %4, %3;\n"
+        "mov.b32 %0, {p, q};\n}"
+        : "=r"(r)
+        : "f"(a * inv), "f"(b * inv), "f"(c * inv), "f"(d * inv));
+    return r;
 }
 
 template <bool kBF16>
 __device__ __forceinline__ uint2 codes8(const uint4& w, float inv) {
-    return {__byte_perm(codes2<kBF16>(w.x, inv), codes2<kBF16>(w.y, inv), 0x5410),
-            __byte_perm(codes2<kBF16>(w.z, inv), codes2<kBF16>(w.w, inv), 0x5410)};
+    return {codes4<kBF16>(w.x, w.y, inv), codes4<kBF16>(w.z, w.w, inv)};
 }
 
 // The same with NaN in the place of what is not finite.
 template <bool kBF16>
 __device__ __noinline__ uint2 codes8_nan(uint4 w, float inv) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-    uint32_t c[4];
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t bad = nonfinite<kBF16>(r[i]);
-        c[i] = codes2<kBF16>(r[i] & ~bad, inv);
-        if (bad & 0xffffu) c[i] = (c[i] & 0xff00u) | 0x7fu;
-        if (bad >> 16) c[i] = (c[i] & 0xffu) | 0x7f00u;
+    uint32_t c[2];
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t b0 = nonfinite<kBF16>(r[2 * i]), b1 = nonfinite<kBF16>(r[2 * i + 1]);
+        c[i] = codes4<kBF16>(r[2 * i] & ~b0, r[2 * i + 1] & ~b1, inv);
+        const uint32_t bad = __byte_perm(b0, b1, 0x6420);  // a byte of each mask's halves
+        c[i] = (c[i] & ~bad) | (0x7f7f7f7fu & bad);
     }
-    return {c[0] | c[1] << 16, c[2] | c[3] << 16};
+    return {c[0], c[1]};
 }
 
 template <bool kBF16>
@@ -142,7 +152,8 @@ __device__ __forceinline__ void quantise(const uint4& wk, const uint4& wv, uint3
                                          uint2& cv) {
     constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
     uint32_t m = group_max<G, kBF16>(lane_max<kBF16>(wk), lane_max<kBF16>(wv));
-    const bool odd = __any_sync(0xffffffffu, (m & 0xffffu) >= kInf || (m >> 16) >= kInf);
+    // a half at or past kInf carries into its top bit
+    const bool odd = __any_sync(0xffffffffu, ((m + (0x8000u - kInf) * 0x10001u) & 0x80008000u) != 0);
     if (odd) m = group_max<G, kBF16>(lane_max<kBF16>(finite_only<kBF16>(wk)), lane_max<kBF16>(finite_only<kBF16>(wv)));
     sk = kv8_scale_byte<kBF16>(m & 0xffffu);
     sv = kv8_scale_byte<kBF16>(m >> 16);
@@ -155,7 +166,7 @@ template <int D, int U, bool kBF16>
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArgs a) {
     using C = AppendCfg<D, U>;
     __shared__ int cu[kMaxB + 1];
-    __shared__ TokenAt place[U == 1 ? 1 : C::Run + 1];
+    __shared__ long long place[U == 1 ? 1 : C::Run + 1];
     grid_dependency_wait();
     grid_launch_dependents();
     const int Hkv = a.pool.Hkv;
@@ -166,6 +177,10 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
     int tok[U], head[U];  // the row's token, counted from t0
     uint4 wk[U], wv[U];
     const int tok_step = C::Groups / Hkv, head_step = C::Groups - tok_step * Hkv;
+    const bool lanes = lane_g * 8 < D;
+    const int left = (int)min(rows - first - group, (long long)C::Run);  // rows of this group: u * Groups < left
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k_new) + lane_g * 8;
+    const uint16_t* vp = static_cast<const uint16_t*>(a.v_new) + lane_g * 8;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (u == 0) {
@@ -180,10 +195,9 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
             }
         }
         wk[u] = wv[u] = make_uint4(0, 0, 0, 0);
-        if (first + u * C::Groups + group < rows && lane_g * 8 < D) {
-            const size_t at = (size_t)head[u] * D + lane_g * 8;
-            wk[u] = load_once(static_cast<const uint16_t*>(a.k_new) + (t0 + tok[u]) * a.k_stride + at);
-            wv[u] = load_once(static_cast<const uint16_t*>(a.v_new) + (t0 + tok[u]) * a.v_stride + at);
+        if (u * C::Groups < left && lanes) {
+            wk[u] = load_once(kp + (t0 + tok[u]) * a.k_stride + (long long)head[u] * D);
+            wv[u] = load_once(vp + (t0 + tok[u]) * a.v_stride + (long long)head[u] * D);
         }
     }
     if (a.cu) {
@@ -191,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
         __syncthreads();
     }
     // The n new tokens are the last n of the sequence's kv_lens[b] keys.
-    auto find = [&](int t) -> TokenAt {
+    auto find = [&](int t) -> long long {
         int b, n, i;
         if (a.cu) {
             b = sequence_of(cu, a.B, t);
@@ -202,11 +216,11 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
             b = t / n;
             i = t - b * n;
         }
-        return i >= 0 ? token_at(a.pool, b, (long long)a.kv_lens[b] - n + i) : TokenAt{-2, 0};
+        return i >= 0 ? place_of(a.pool, b, (long long)a.kv_lens[b] - n + i) : kNoSequence;
     };
-    TokenAt mine = {-2, 0};
+    long long mine = kNoSequence;
     if constexpr (U == 1) {
-        if (first + group < rows) mine = find(t0 + tok[0]);
+        if (left > 0) mine = find(t0 + tok[0]);
     } else {
         const long long last = first + C::Run - 1 < rows ? first + C::Run - 1 : rows - 1;
         const int tokens = (int)(last / Hkv) - t0 + 1;
@@ -218,10 +232,10 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
         uint2 ck, cv;
         uint32_t sk, sv;
         quantise<C::G, kBF16>(wk[u], wv[u], sk, sv, ck, cv);
-        if (first + u * C::Groups + group >= rows || lane_g * 8 >= D) continue;
-        const TokenAt at = U == 1 ? mine : place[tok[u]];
-        if (at.page < 0) continue;
-        const size_t r = ((size_t)at.page * Hkv + head[u]) * a.pool.page_size + at.slot;
+        if (u * C::Groups >= left || !lanes) continue;
+        const long long at = U == 1 ? mine : place[tok[u]];
+        if (at < 0) continue;
+        const long long r = at + (long long)head[u] * a.pool.page_size;
         *reinterpret_cast<uint2*>(a.pool.k + r * D + lane_g * 8) = ck;
         *reinterpret_cast<uint2*>(a.pool.v + r * D + lane_g * 8) = cv;
         if (lane_g == 0) {
@@ -259,7 +273,7 @@ template <int D, int U, bool kBF16>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadArgs a) {
     using C = ReadCfg<D, U>;
     __shared__ int cu[kMaxB + 1];
-    __shared__ TokenAt place[U == 1 ? 1 : C::Run + 1];
+    __shared__ long long place[U == 1 ? 1 : C::Run + 1];
     grid_dependency_wait();
     grid_launch_dependents();
     const int Hkv = a.pool.Hkv;
@@ -267,10 +281,10 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadArgs a)
     const int t0 = (int)(first / Hkv);
     for (int i = threadIdx.x; i <= a.B; i += kThreads) cu[i] = a.cu[i];
     __syncthreads();
-    auto find = [&](int t) -> TokenAt {
+    auto find = [&](int t) -> long long {
         const int b = sequence_of(cu, a.B, t);
-        return b < a.B && t >= cu[b] ? token_at(a.pool, b, (long long)(a.starts ? a.starts[b] : 0) + (t - cu[b]))
-                                     : TokenAt{-2, 0};
+        return b < a.B && t >= cu[b] ? place_of(a.pool, b, (long long)(a.starts ? a.starts[b] : 0) + (t - cu[b]))
+                                     : kNoSequence;
     };
     if constexpr (U > 1) {
         const long long last = first + C::Run - 1 < rows ? first + C::Run - 1 : rows - 1;
@@ -280,20 +294,21 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadArgs a)
     }
     const int group = threadIdx.x / C::PerRow, c8 = threadIdx.x % C::PerRow * 8;
     if (group >= C::Groups) return;
-    TokenAt at[U];
+    bool owned[U];  // rows of no sequence are left as they were
     uint2 ck[U], cv[U];
     uint32_t sk[U], sv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const long long row = first + u * C::Groups + group;
-        at[u] = {-2, 0};
+        owned[u] = false;
         ck[u] = cv[u] = make_uint2(0, 0);
         sk[u] = sv[u] = 0;
         if (row >= rows) continue;
         const int t = (int)(row / Hkv), h = (int)(row - (long long)t * Hkv);
-        at[u] = U == 1 ? find(t) : place[t - t0];
-        if (at[u].page < 0) continue;
-        const size_t r = ((size_t)at[u].page * Hkv + h) * a.pool.page_size + at[u].slot;
+        const long long at = U == 1 ? find(t) : place[t - t0];
+        owned[u] = at != kNoSequence;
+        if (at < 0) continue;
+        const long long r = at + (long long)h * a.pool.page_size;
         ck[u] = *reinterpret_cast<const uint2*>(a.pool.k + r * D + c8);
         cv[u] = *reinterpret_cast<const uint2*>(a.pool.v + r * D + c8);
         sk[u] = a.pool.ks[r];
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadArgs a)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (at[u].page == -2) continue;  // a row of no sequence: left as it was
+        if (!owned[u]) continue;
         const size_t to = (size_t)(first + u * C::Groups + group) * D + c8;
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k) + to) = dequantise8<kBF16>(ck[u], kv8_scale(sk[u]));
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v) + to) = dequantise8<kBF16>(cv[u], kv8_scale(sv[u]));
