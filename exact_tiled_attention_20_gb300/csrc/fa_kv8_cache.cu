@@ -141,10 +141,10 @@ __device__ __forceinline__ uint4 finite_only(const uint4& w) {
 }
 
 // Quantises a K and a V row held by the G lanes of a group, 8 values of each a lane (all lanes of
-// the warp take part): the scale bytes and the lane's 8 codes of each.  The largest magnitudes
-// are found on 16-bit pairs and both rows' reduced together, since the ALU and not the memory
-// bound an earlier form (280 instructions a lane for the two rows: 107 us for 540672 of each, D =
-// 128, at 68 % of the ALU's rate).
+// the warp take part): the scale bytes and the lane's 8 codes of each.  The instructions of this
+// kernel bound it more than HBM does (with 140 for a lane's 8 values the ALU ran at 68 % of its
+// rate and the kernel at 57 % of a copy's; now 53 % and 88 %), so the largest magnitudes are
+// found on 16-bit pairs and both rows' reduced in one word.
 // A value that is not finite takes no part in the scale and becomes NaN (e4m3 has no
 // infinity): an overflow upstream stays visible.
 template <int G, bool kBF16>
@@ -325,8 +325,9 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8ReadArgs a)
 
 // Rows of a group: more of them for the loads in flight where the rows fill the SMs many times
 // over, one where they do not, since then a CTA's latency is what a call takes.  Measured, in
-// microseconds for 1, 2 and 4 rows: append of 540672 rows of 128 94, 72.1, 72.5, of 42936 rows of
-// 96 8.8, 7.5, 9.2; read of 540672 rows of 128 80.7, 66.3, 64.7 (61.3 at the rate of a copy).
+// microseconds for 1, 2 and 4 rows: append of 540672 rows of 128 92.5, 69.5, 69.4 (61.3 at the rate
+// of a copy), of 42936 rows of 96 8.7, 7.2, 8.1, of 64 rows of 128 2.2, 2.7, 3.3; read of 540672
+// rows of 128 81.3, 66.4, 64.6 (61.3).
 int rows_of_a_group(long long rows, int groups, int num_sms) {
     const long long waves = rows / ((long long)groups * num_sms);
     return waves >= 64 ? 4 : waves >= 8 ? 2 : 1;

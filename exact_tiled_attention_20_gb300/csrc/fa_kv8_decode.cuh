@@ -17,6 +17,25 @@
 // Where every sequence is short and there are many pairs (`solo`), each warp has a range of
 // its own and takes whole pairs: a pair of a few tiles gives four warps little to share, and
 // joining them costs as much as the tiles.
+//
+// What bounds it: each cached byte is read once and meets at most 16 query rows, so HBM does;
+// the products are 16 % of the tensor pipe's time even as mma.sync, which takes its operands
+// from registers.  That is why these are not tcgen05 products: codes have to become fp16 on
+// the way (the probabilities and queries do not fit e4m3), and registers, where the
+// conversion leaves them, are where mma.sync wants them, while tcgen05 would have them
+// written back to shared memory first.  (K Q^T as e4m3 products, the queries in two or three
+// e4m3 pieces, was right and needs no conversion of K, but slower: 62.7 -> 83.5 us for 8
+// sequences of 700..16384 keys at D = 256 with 16 rows, 90 -> 107 us for the fp16 batch below.)
+// So a warp works alone on a tile: it copies its own keys (cp.async, 98 KB in flight on an SM),
+// and nothing but the end of a pair makes it wait for another warp.
+//
+// Measured (split and merge, back to back, inputs larger than L2): lengths 1024..32768 x 8
+// sequences, 8 kv heads of 4 query heads, D = 128, 279 MB: 47.7 us, 5.85 TB/s, 86 % of a copy's
+// rate; 64 sequences of 1..8192,
+// 541 MB: 88.7 us, 6.1 TB/s, 90 %; the first at D = 64, 96, 256 with 157, 235, 624 MB: 31.4, 45.5,
+// 99 us, 74, 76, 93 %.  About 8 us of a call do not stream: 1.0 for the plan, 0.5 for the first
+// table entries, 1.4 for the last join and about 1 of uneven ends, 2 for the merge kernel, 1 to
+// pass from one kernel to the next and 1 to fill and drain the memory's queues.
 #pragma once
 
 #include <algorithm>
@@ -227,6 +246,11 @@ struct Kv8Walk {
 // meet no bank twice.
 //
 // HB: query rows in blocks of four (1, 2 or 4 blocks; a row is a (token, head) of one kv head).
+//
+// KT x NST x CTAS were measured (us): D = 128, two batches, 32 x 2 x 3 48.7 and 89.6, 16 x 4 x 3
+// 51.0 and 91.6, 16 x 3 x 4 50.9 and 91.4, 32 x 3 x 2 49.2 and 98.3: three CTAs cover each other's
+// joins.  D = 64: 32 x 3 20.6, 32 x 4 21.0, 64 x 2 20.9.  D = 96: 32 x 2 20.7, 16 x 5 21.8.  At D = 256 and
+// with 16 query rows the registers allow two CTAs; three at D = 96 spill and take 41.9 for 37.3.
 template <int D_, int HB_>
 struct Kv8Cfg {
     static constexpr int D = D_, HB = HB_;
