@@ -304,8 +304,9 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  *             values are the caller's error and are clamped on the device
  *   causal    as fa_decode_splitkv_multi: token s sees keys j <= kv_lens[b] - Sq + s
  * (Hq / Hkv) * Sq <= 16.  A token that sees no key gets O = 0 and LSE = -inf.  Cached codes
- * enter the products exactly; the probabilities are rounded to fp16 (11 bits) for P.V; O is
- * rounded once.  What lies in the pool behind a sequence's last key is not used, NaN codes
+ * enter the products exactly; the probabilities, with V's scales in them, are rounded to fp16 for
+ * P.V (11 bits for weights down to 2^-25 of the row's largest, fewer below; one under 2^-36 of it may
+ * vanish); O is rounded once.  What lies in the pool behind a sequence's last key is not used, NaN codes
  * there included.  Keys on a page outside the pool count as zero rows.
  *   num_splits  sizes the workspace, which holds B * Hkv * num_splits partial results (<= 0:
  *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0)).  The keys of

@@ -91,20 +91,32 @@ def cached(codes, scales, table, b, first, n):
     return out
 
 
+def cached_scales(scales, table, b, n):
+    """The scales of keys 0 .. n - 1 of sequence b, [n, Hkv]; of a key without a page the least."""
+    num_pages, Hkv, page = scales.shape
+    out = np.full((n, Hkv), 2.0 ** -127)
+    for i in range(n):
+        at = _where(table, b, i, num_pages, page)
+        if at is not None:
+            out[i] = 2.0 ** (scales[at[0], :, at[1]].astype(np.float64) - 127)
+    return out
+
+
 def decode(q, pool, table, kv_lens, scale, causal=True):
-    """q [B, Sq, Hq, D] -> (o [B, Sq, Hq, D], lse [B, Hq, Sq], o_abs, s_abs): o_abs is
-    sum_j p_j |v_j| and s_abs the largest scale * sum_d |q_d k_jd| of the row, which the
-    error bounds of a computation in fewer bits go by."""
+    """q [B, Sq, Hq, D] -> (o [B, Sq, Hq, D], lse [B, Hq, Sq], o_abs, s_abs, o_top), the last three
+    what the error bounds of a computation in fewer bits go by: o_abs = sum_j p_j |v_j|; s_abs the
+    largest scale * sum_d |q_d k_jd| of the row; o_top = max_j (p_j vscale_j) * sum_j |vcode_j|."""
     q = np.asarray(q, np.float64)
     B, Sq, Hq, D = q.shape
     k, v, ks, vs = pool
     capacity = table.shape[1] * k.shape[2]
     g = Hq // k.shape[1]
-    o, o_abs = np.zeros(q.shape), np.zeros(q.shape)
+    o, o_abs, o_top = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     lse, s_abs = np.full((B, Hq, Sq), -np.inf), np.zeros((B, Hq, Sq))
     for b in range(B):
         n = min(max(int(kv_lens[b]), 0), capacity)
         kb, vb = cached(k, ks, table, b, 0, n), cached(v, vs, table, b, 0, n)
+        sb = cached_scales(vs, table, b, n)
         for i in range(Sq):
             m = min(n, n - Sq + i + 1) if causal else n
             if m <= 0:
@@ -115,7 +127,9 @@ def decode(q, pool, table, kv_lens, scale, causal=True):
                 p = np.exp(s - top)
                 l = p.sum()
                 o[b, i, h] = p @ vb[:m, h // g] / l
-                o_abs[b, i, h] = p @ np.abs(vb[:m, h // g]) / l
+                va, sv = np.abs(vb[:m, h // g]), sb[:m, h // g]
+                o_abs[b, i, h] = p @ va / l
+                o_top[b, i, h] = (p * sv).max() / l * (va / sv[:, None]).sum(0)
                 lse[b, h, i] = top + np.log(l)
                 s_abs[b, h, i] = (np.abs(kb[:m, h // g]) @ np.abs(q[b, i, h])).max() * scale
-    return o, lse, o_abs, s_abs
+    return o, lse, o_abs, s_abs, o_top

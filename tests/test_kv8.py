@@ -5,7 +5,7 @@ codes, scales and read values are compared bit for bit.
 
 The decode's bound, per output value, from its roundings (a rounding is off by at most half
 a step: 2^-9 ... here taken as eps / 2 of the type):
-    |dO| <= u_o |O| + c A,   A = sum_j p_j |v_j|
+    |dO| <= u_o |O| + c A + 2^-36 T,   A = sum_j p_j |v_j|,   T = max_j (p_j vscale_j) sum_j |vcode_j|
     u_o  one rounding of the output: 2^-8 (bf16), 2^-11 (fp16); of a subnormal, half of its step
     c    2^-11 (P rounded to fp16) + 2 e_s + 2^-21 + N 2^-23
     e_s  error of a score, in its exponent: (D + 8) 2^-22 max_j scale sum_d |q_d k_jd| (a sum of
@@ -13,6 +13,9 @@ a step: 2^-9 ... here taken as eps / 2 of the type):
          factors), twice because it enters the numerator and the denominator; 2^-21 is
          exp2's and the division's; N = n / 4 + 64 sums over the n keys (at least four
          partial sums run side by side in any split)
+    T    P_j is fp16(2^11 w_j / r), w_j = p_j vscale_j, with r at least 2^-4 of the largest w and at
+         most it: below 2^-14 its steps are 2^-24, an error of at most 2^-25 r / 2^11 <= 2^-36 max w
+         for each key, whose code it multiplies
 and |dLSE| <= e_s + (2^-21 + N 2^-23) + 2^-22 |LSE|.
 """
 import math
@@ -274,13 +277,13 @@ def test_read_zeros_where_there_is_no_page(fa):
 
 # ------------------------------------------------------------------------ decode ----
 def _check(o, lse, ref, n, D, dtype):
-    o_ref, lse_ref, o_abs, s_abs = ref
+    o_ref, lse_ref, o_abs, s_abs, o_top = ref
     o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
     e_s = (D + 8) * 2.0 ** -22 * s_abs                                     # [B, Hq, Sq]
     sums = 2.0 ** -21 + (n / 4 + 64) * 2.0 ** -23
     c = np.transpose(2.0 ** -11 + 2 * e_s + sums, (0, 2, 1))[..., None]
     step = float(torch.finfo(DT[dtype]).smallest_normal) * float(torch.finfo(DT[dtype]).eps)
-    bound = U_O[dtype] * np.abs(o_ref) + c * o_abs + step / 2
+    bound = U_O[dtype] * np.abs(o_ref) + c * o_abs + 2.0 ** -36 * o_top + step / 2
     assert np.isfinite(o).all()
     off = np.abs(o - o_ref)
     assert (off <= bound).all(), f"|dO| {off.max():.3e}, {np.max(off / bound):.2f} of its bound"

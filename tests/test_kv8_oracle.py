@@ -55,21 +55,21 @@ def test_decode_is_attention_over_the_values():
     table[2, 0] = -1
     lens = np.array([48, 40, 17], np.int32)
     q = rng.standard_normal((B, 1, Hq, D))
-    o, lse, o_abs, _ = kv8.decode(q, (codes[0], codes[1], scales[0], scales[1]), table, lens, 0.1)
+    o, lse, o_abs, _, o_top = kv8.decode(q, (codes[0], codes[1], scales[0], scales[1]), table, lens, 0.1)
     safe = np.where((table < 0) | (table >= pages), pages, table)
     vals = [np.concatenate([kv8.values(c, s).transpose(0, 2, 1, 3), np.zeros((1, page, Hkv, D))])
             for c, s in zip(codes, scales)]
     o_ref, lse_ref = oracle.decode_paged(q, vals[0], vals[1], safe, lens, scale=0.1)
     np.testing.assert_allclose(o[:, 0], o_ref, rtol=1e-12, atol=1e-12)
     np.testing.assert_allclose(lse[:, :, 0], lse_ref, rtol=1e-12)
-    assert (o_abs >= np.abs(o) - 1e-12).all()
+    assert (o_abs >= np.abs(o) - 1e-12).all() and (o_top >= o_abs - 1e-12).all()
 
 
 def test_decode_masks_from_the_bottom_right():
     """Sq = 4 tokens over 2 keys: the first two see none; the last sees both."""
     pool = (np.full((1, 1, 16, 64), 0x38, np.uint8),) * 2 + (np.full((1, 1, 16), 127, np.uint8),) * 2
     q = np.ones((1, 4, 1, 64))
-    o, lse, _, _ = kv8.decode(q, pool, np.zeros((1, 1), np.int32), [2], 0.5)
+    o, lse, _, _, _ = kv8.decode(q, pool, np.zeros((1, 1), np.int32), [2], 0.5)
     assert (o[0, :2] == 0).all() and np.isneginf(lse[0, 0, :2]).all()
     assert lse[0, 0, 2] == 32.0 and abs(lse[0, 0, 3] - (32 + math.log(2))) < 1e-12
     assert (kv8.decode(q, pool, np.zeros((1, 1), np.int32), [2], 0.5, causal=False)[0] == 1).all()
