@@ -31,9 +31,8 @@
 //
 // Measured (split and merge, back to back, inputs larger than L2): lengths 1024..32768 x 8
 // sequences, 8 kv heads of 4 query heads, D = 128, 279 MB: 47.7 us, 5.85 TB/s, 86 % of a copy's
-// rate; 64 sequences of 1..8192,
-// 541 MB: 88.7 us, 6.1 TB/s, 90 %; the first at D = 64, 96, 256 with 157, 235, 624 MB: 31.4, 45.5,
-// 99 us, 74, 76, 93 %.  About 8 us of a call do not stream: 1.0 for the plan, 0.5 for the first
+// rate; 64 sequences of 1..8192, 541 MB: 88.7 us, 6.1 TB/s, 90 %; 8 of U[1024, 32768] at D = 64, 96,
+// 128, 256 with 158, 235, 313, 623 MB: 31.4, 45.5, 52.9, 99 us, 74, 76, 87, 93 %.  About 8 us of a call do not stream: 1.0 for the plan, 0.5 for the first
 // table entries, 1.4 for the last join and about 1 of uneven ends, 2 for the merge kernel, 1 to
 // pass from one kernel to the next and 1 to fill and drain the memory's queues.
 #pragma once
@@ -400,14 +399,6 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     float* s_qf = s_qfs[solo ? warp : 0];
     uint16_t* o16 = static_cast<uint16_t*>(p.o);
     const uint16_t* q16 = static_cast<const uint16_t*>(p.q);
-    const int rows = p.Sq * p.Hq;
-    for (int b = blockIdx.x; b < p.B; b += p.grid) {  // sequences without keys
-        if (plan.prefix[b + 1] > plan.prefix[b]) continue;
-        for (int i = tid; i < rows * D; i += kKv8Threads) o16[(size_t)b * rows * D + i] = 0;
-        if (p.lse)
-            for (int i = tid; i < rows; i += kKv8Threads) p.lse[(size_t)b * rows + i] = kNegInf;
-    }
-
     // This lane's 16-byte units of a run of 16 rows: unit i * 32 + lane of the run's 16 D bytes.
     uint32_t dst[C::Copies], step[C::Copies];
 #pragma unroll
@@ -492,6 +483,14 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             next_tile();
         }
         cp_async_commit();
+    }
+
+    const int rows = p.Sq * p.Hq;
+    for (int b = blockIdx.x; b < p.B; b += p.grid) {  // sequences without keys
+        if (plan.prefix[b + 1] > plan.prefix[b]) continue;
+        for (int i = tid; i < rows * D; i += kKv8Threads) o16[(size_t)b * rows * D + i] = 0;
+        if (p.lse)
+            for (int i = tid; i < rows; i += kKv8Threads) p.lse[(size_t)b * rows + i] = kNegInf;
     }
 
     // Queries.  Warp w turns rows w, w + 4, ... of a segment into fragments (a warp alone all of
@@ -1105,9 +1104,9 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     p.scale_log2 = a.scale * 1.4426950408889634f;
     // As many ranges as CTAs are resident at once, where the workspace's slots (a partial result
     // of one pair each) allow it: ranges + min(ranges, pairs) of them.  Cutting costs a second
-    // kernel (3 us); it pays where it evens out the work of more pairs than CTAs, or cuts fewer
-    // pairs into two pieces each or more (8 pairs of 148..445 keys in 8 ranges took 11.5 us,
-    // whole 6.0).
+    // kernel (2 us); it pays where it evens out the work of more pairs than CTAs, or cuts fewer
+    // pairs into two pieces each or more (8 pairs of 148..445 keys, D = 64, 10 rows, took 11.5 us in 8
+    // ranges and 9.6 whole).
     const int per_sm = p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::CTAS : Kv8Cfg<D, 4>::CTAS;
     const long long pairs = (long long)a.B * a.pool.Hkv, resident = (long long)per_sm * a.num_sms;
     const long long most = pairs * ((p.capacity + kKv8Unit - 1) / kKv8Unit);

@@ -563,15 +563,17 @@ def test_captured_split_decode_follows_the_lengths(fa):
     pool = Pool(2 * 40, 2, 32, 128, 2, 40, seed=16)
     pool.fill(rng, [1200, 1100])
     q = torch.from_numpy(rng.standard_normal((2, 1, 8, 128))).to(torch.bfloat16).to(DEV)
-    kl = _int([1000, 60])
+    q0, kl = q.clone(), _int([1000, 60])
     ws = torch.empty(fa.fa_decode_workspace_bytes(2, 8, 128, 16), dtype=torch.uint8, device=DEV)
     o, lse = torch.empty_like(q), torch.empty(2, 8, 1, device=DEV)
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
         kl.add_(33)
+        q.copy_(q0)                              # a copy and not a kernel before the decode
         fa.fa_decode_splitkv_paged_fp8(q, *pool.args, kl, num_splits=16, workspace=ws, out=o, lse=lse)
     for i in range(1, 5):
+        q.zero_()
         graph.replay()
         torch.cuda.synchronize()
         a, b = fa.fa_decode_splitkv_paged_fp8(q, *pool.args, _int([1000 + 33 * i, 60 + 33 * i]), num_splits=16)
