@@ -74,11 +74,6 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 }  // namespace
 
-int device_sms() {
-    DeviceInfo di;
-    return device_info(&di) ? di.num_sms : 0;
-}
-
 bool encode_tmap_4d(CUtensorMap* map, const void* base, bool bf16, uint64_t dim0, uint64_t dim1,
                     uint64_t dim2, uint64_t dim3, uint32_t box_rows) {
     return encode_tmap_4d_box(map, base, bf16, dim0, dim1, dim2, dim3, 1, box_rows);

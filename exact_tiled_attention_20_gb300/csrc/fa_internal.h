@@ -79,9 +79,6 @@ fa_status decode_check_args(const void* q, const void* k_cache, const void* v_ca
                             const int32_t* kv_lens, const void* o, const float* lse, int B, int Sq,
                             int Hq, int Hkv, int D, int Smax, float scale, fa_dtype dtype);
 
-// SMs of the current device; 0 where it cannot be queried.
-int device_sms();
-
 // Sets the dynamic shared-memory limit of `func` once per device.
 bool ensure_smem_attr(const void* func, int bytes, int* done_flags);
 

@@ -4,6 +4,18 @@
 namespace fa {
 namespace {
 
+// SMs of the current device, asked for once per device; 0 where it cannot be queried.
+int device_sms() {
+    static int known[64] = {0};
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    sms = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
+    if (sms > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    __atomic_store_n(&known[dev], sms, __ATOMIC_RELAXED);
+    return sms;
+}
+
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
 // Checks of the pool that all three entry points share.
