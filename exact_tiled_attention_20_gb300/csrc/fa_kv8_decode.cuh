@@ -67,7 +67,8 @@ constexpr int kTableLines = 8;  // lines of the block table that a CTA prefetche
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ int kv8_len(const Kv8DecParams& p, int b) {
-    return min(max(__ldcg(p.kv_lens + b), 0), p.capacity);  // past L1: the merge reads it early
+    // Past L1: the merge reads it before the kernels before it are known to be done.
+    return min(max(__ldcg(p.kv_lens + b), 0), p.capacity);
 }
 
 // Units of one pair of a sequence.
@@ -130,8 +131,7 @@ struct Kv8Plan {
 
 // Fills the plan from kv_lens (all threads; ends with a barrier); returns the units of one pair of
 // the longest sequence.
-__device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Plan& t) {
-    __shared__ int warp_sum[kKv8Warps], warp_max[kKv8Warps];
+__device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Plan& t, int* warp_sum, int* warp_max) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.B + kKv8Threads - 1) / kKv8Threads;
     int sum = 0, most = 0;
@@ -237,6 +237,13 @@ struct Kv8Walk {
     }
 };
 
+// What the warps of a CTA tell one another about each query row, and of the plan.
+struct Kv8Small {
+    float mo[kKv8Warps][16], ms[kKv8Warps][16], l[kKv8Warps][16];
+    float f[16], finv[16], lse[16], qf[16];
+    int warp_sum[kKv8Warps], warp_max[kKv8Warps];
+};
+
 // ------------------------------------------------------------------ shared layout ----
 // Each warp streams its own tiles of KT keys through a ring of NST stages in shared memory:
 // K codes and V codes, and the scales of both beside the ring.  A row is split into a part of
@@ -250,13 +257,16 @@ struct Kv8Walk {
 // 51.0 and 91.6, 16 x 3 x 4 50.9 and 91.4, 32 x 3 x 2 49.2 and 98.3: three CTAs cover each other's
 // joins.  D = 64: 32 x 3 20.6, 32 x 4 21.0, 64 x 2 20.9.  D = 96: 32 x 2 20.7, 16 x 5 21.8.  At D = 256 and
 // with 16 query rows the registers allow two CTAs; three at D = 96 spill and take 41.9 for 37.3.
+// A CTA more or less on an SM is worth more than a stage or a buffer: 5 to 8 rows at D = 256 (8 of
+// 700..16384 keys) take 67.8 us with three stages in one CTA and 59.9 with two in two; at D = 128 (256 of
+// 100..1000 keys, 8 kv heads) 95 with two buffers of the exchange and 70.5 with one.
 template <int D_, int HB_>
 struct Kv8Cfg {
     static constexpr int D = D_, HB = HB_;
     static constexpr int NT = (HB + 1) / 2;     // 8-column blocks of P
     static constexpr int E = HB == 1 ? 1 : 2;   // columns of a lane in use
     static constexpr int KT = D == 256 ? 16 : 32;
-    static constexpr int NST = D == 64 || (D == 256 && NT == 1) ? 3 : 2;
+    static constexpr int NST = D == 64 || (D == 256 && HB == 1) ? 3 : 2;
     static constexpr int CTAS = D == 256 || NT == 2 ? 2 : 3;  // resident on an SM
     static constexpr int NSUB = KT / 16;  // runs of 16 keys
     static constexpr int TileBytes = KT * D;
@@ -265,15 +275,22 @@ struct Kv8Cfg {
     // Row of the exchange in floats: pair (block k, row g) of dims at 2 (8 k + g); a half-warp's
     // 4 g and 4 t, one query row apart, then lie in 32 different banks.
     static constexpr int XD = D + 8;
-    static constexpr int ExchBytes = 2 * HB * 4 * XD * 4;      // two buffers
+    static constexpr int Bufs = D == 128 && HB == 2 ? 1 : 2;   // one where a third CTA fits with it
+    static constexpr int ExchBytes = Bufs * HB * 4 * XD * 4;
     // Query fragments stay in registers or, where they are too many, in shared memory; they are
     // made there, in the exchange's room if they do not stay.
     static constexpr bool QRegs = D / 16 * NT <= 16;
     static constexpr int QLanes = 16 * E;  // lanes that hold a query fragment: with E = 1 those of even g
     static constexpr int QStage = D / 16 * NT * QLanes * 8;
     static constexpr int QBytes = QRegs ? 0 : QStage;
-    static_assert(!QRegs || kKv8Warps * QStage <= ExchBytes, "each warp's queries fit the exchange");
+    static_assert(!QRegs || QStage <= ExchBytes, "queries fit the exchange");
     static constexpr int FixedBytes = 128 + kKv8Warps * (RingBytes + ScaleBytes) + ExchBytes + QBytes;
+    // CTAs that are resident on an SM with the plan of B sequences: 228 KB, less 1 KB for each.
+    static int resident(int B) {
+        const int each = (FixedBytes + Kv8Plan::bytes(B) + (int)sizeof(Kv8Small) + 127) / 128 * 128;
+        const int fit = 228 * 1024 / (each + 1024);
+        return fit < CTAS ? fit : CTAS;
+    }
     static constexpr int WA = D == 96 ? 64 : D;
     static constexpr int KS = D / 16;        // steps of 16 dims, and 16-dim blocks of O^T
     static constexpr int Copies = D / 32;    // 16-byte copies of a lane per run and tensor
@@ -364,8 +381,9 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     using C = Kv8Cfg<D, HB>;
     constexpr int KT = C::KT, NSUB = C::NSUB, NST = C::NST, KS = C::KS, XD = C::XD, NT = C::NT, E = C::E;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ float s_mo[kKv8Warps][16], s_ms[kKv8Warps][16], s_l[kKv8Warps][16];
-    __shared__ float s_f[16], s_finv[16], s_lse[16], s_qfs[kKv8Warps][16];
+    __shared__ Kv8Small sm;
+    auto &s_mo = sm.mo, &s_ms = sm.ms, &s_l = sm.l;
+    auto &s_f = sm.f, &s_finv = sm.finv, &s_lse = sm.lse, &s_qf = sm.qf;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -384,19 +402,12 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     kv8_prefetch(p.pool.table, (long long)p.B * p.pool.max_pages * 4, (int)blockIdx.x * kTableLines);
     grid_dependency_wait();
     // A group of gw warps works through a range; this is warp wi of it.
-    const int most = kv8_make_plan(p, plan);
+    const int most = kv8_make_plan(p, plan, sm.warp_sum, sm.warp_max);
     const bool solo = C::QRegs && kv8_solo(p, most);
     const int gw = solo ? 1 : kKv8Warps, wi = solo ? 0 : warp;
     const int rng = solo ? (int)blockIdx.x * kKv8Warps + warp : (int)blockIdx.x;
     const int W = kv8_width(p, plan.prefix[p.B], solo ? p.grid * kKv8Warps : p.grid);
-    auto group_sync = [&]() {
-        if (solo)
-            __syncwarp();
-        else
-            __syncthreads();
-    };
-    uint2* s_q = reinterpret_cast<uint2*>(C::QRegs ? rest + (solo ? warp * C::QStage : 0) : rest + C::ExchBytes);
-    float* s_qf = s_qfs[solo ? warp : 0];
+    uint2* s_q = reinterpret_cast<uint2*>(C::QRegs ? rest : rest + C::ExchBytes);
     uint16_t* o16 = static_cast<uint16_t*>(p.o);
     const uint16_t* q16 = static_cast<const uint16_t*>(p.q);
     // This lane's 16-byte units of a run of 16 rows: unit i * 32 + lane of the run's 16 D bytes.
@@ -493,15 +504,28 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             for (int i = tid; i < rows; i += kKv8Threads) p.lse[(size_t)b * rows + i] = kNegInf;
     }
 
-    // Queries.  Warp w turns rows w, w + 4, ... of a segment into fragments (a warp alone all of
-    // them, four rows at a time), a lane four dims at a time; they are loaded while the segment
-    // before is joined.
+    // Queries as f16 fragments, column 2 t + e of block nt being row (2 nt + e) * 4 + t.  A row is
+    // multiplied by a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's
+    // subnormals are then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values that
+    // far below their row's largest.
+    struct Factor {
+        float up, down;  // the power of two, and softmax scale * log2 e over it
+    };
+    auto factor = [&](float amax) -> Factor {
+        // amax = f 2^x; the factor is 2^(13 - x), from the exponent field, kept normal
+        int ex = (int)(__float_as_uint(amax) >> 23);
+        ex = ex == 255 ? 127 + 13 : max(ex, 14);
+        return {__uint_as_float((uint32_t)(254 + 13 - ex) << 23),
+                p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23)};
+    };
+    // Four warps: warp w makes rows w, w + 4, ... of a segment, a lane four dims at a time, in shared
+    // memory; they are loaded while the segment before is joined.
     constexpr int QU = (D / 4 + 31) / 32;
     uint2 raw_q[HB][QU];
-    auto load_queries = [&](const Kv8Seg& s, int w, uint2 (&raw_q)[HB][QU]) {
+    auto load_queries = [&](const Kv8Seg& s) {
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
-            const int c = i * 4 + w, tok = c / p.group, h = s.hk * p.group + c - tok * p.group;
+            const int c = i * 4 + warp, tok = c / p.group, h = s.hk * p.group + c - tok * p.group;
             const uint16_t* src = q16 + (((size_t)s.b * p.Sq + tok) * p.Hq + h) * D;
 #pragma unroll
             for (int k = 0; k < QU; ++k) {
@@ -510,11 +534,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             }
         }
     };
-    // Fragments as f16, column 2 t + e of block nt being row (2 nt + e) * 4 + t.  A row is multiplied by
-    // a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's subnormals are
-    // then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values that far below their
-    // row's largest.
-    auto make_fragments = [&](int w, const uint2 (&raw_q)[HB][QU]) {
+    auto make_fragments = [&]() {
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
             float x[QU][4], amax = 0.f;
@@ -530,18 +550,16 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // amax = f 2^x; the factor is 2^(13 - x), from the exponent field, kept normal
-            int ex = (int)(__float_as_uint(amax) >> 23);
-            ex = ex == 255 ? 127 + 13 : max(ex, 14);
-            const float up = __uint_as_float((uint32_t)(254 + 13 - ex) << 23);
-            if (lane == 0) s_qf[i * 4 + w] = p.scale_log2 * __uint_as_float((uint32_t)(ex - 13) << 23);
+            const Factor fac = factor(amax);
+            const float up = fac.up;
+            if (lane == 0) s_qf[i * 4 + warp] = fac.down;
 #pragma unroll
             for (int k = 0; k < QU; ++k) {
                 const int d = (lane + 32 * k) * 4;
                 const int ks = d < C::WA ? (d >> 6) * 4 + ((d >> 2) & 3) : 4 + ((d >> 2) & 1);
                 const int tt = d < C::WA ? (d >> 4) & 3 : ((d - 64) >> 3) & 3;
-                if (d < D)  // of lane 4 g + tt, g = 2 w + i % 2
-                    s_q[(ks * NT + (i >> 1)) * C::QLanes + (E * w + (i & 1)) * 4 + tt] =
+                if (d < D)  // of lane 4 g + tt, g = 2 warp + i % 2
+                    s_q[(ks * NT + (i >> 1)) * C::QLanes + (E * warp + (i & 1)) * 4 + tt] =
                         make_uint2(pack_f16x2(x[k][0] * up, x[k][1] * up), pack_f16x2(x[k][2] * up, x[k][3] * up));
             }
         }
@@ -557,36 +575,63 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     int st = 0;
     Kv8Seg sg;
     bool more = cw.next(p, plan, rng, W, sg);
-    if (more && !solo) load_queries(sg, warp, raw_q);
+    if (more && !solo) load_queries(sg);
     while (more) {
         const int b = sg.b, hk = sg.hk, len = sg.len, k0 = sg.k0, k1 = sg.k1;
         const int tiles = (k1 - k0 + KT - 1) / KT;
 
-        if (!solo) {
-            make_fragments(warp, raw_q);
-        } else {
-            uint2 all[kKv8Warps][HB][QU];
-#pragma unroll
-            for (int w = 0; w < kKv8Warps; ++w) load_queries(sg, w, all[w]);
-#pragma unroll
-            for (int w = 0; w < kKv8Warps; ++w) make_fragments(w, all[w]);
-        }
-        group_sync();
         uint2 qr[C::QRegs ? KS * NT : 1];
-        if constexpr (C::QRegs) {
-#pragma unroll
-            for (int i = 0; i < KS * NT; ++i) qr[i] = fragment(i / NT, i % NT);
-        }
         float qf[NT][E];
+        if (!solo) {
+            make_fragments();
+            __syncthreads();
+            if constexpr (C::QRegs) {
+#pragma unroll
+                for (int i = 0; i < KS * NT; ++i) qr[i] = fragment(i / NT, i % NT);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < E; ++e) qf[nt][e] = s_qf[(nt * 2 + e) * 4 + t];
+        } else if constexpr (C::QRegs) {
+            // A warp alone: each lane loads what its fragments are made of.
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int c = (nt * 2 + (g & 1)) * 4 + (g >> 1), tok = c / p.group;
+                const bool in = c < cols && (g & 1) < E;
+                const uint16_t* src = q16 + (((size_t)b * p.Sq + tok) * p.Hq + hk * p.group + c - tok * p.group) * D;
+                uint2 w[KS];
+                float amax = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const int d = ks * 16 < C::WA ? (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 : 64 + t * 8 + (ks - 4) * 4;
+                    w[ks] = in ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
+                }
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(float_from16<kBF16>((uint16_t)w[ks].x)),
+                                                   fabsf(float_from16<kBF16>((uint16_t)(w[ks].x >> 16)))),
+                                             fmaxf(fabsf(float_from16<kBF16>((uint16_t)w[ks].y)),
+                                                   fabsf(float_from16<kBF16>((uint16_t)(w[ks].y >> 16))))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const Factor fac = factor(amax);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    qr[ks * NT + nt] = make_uint2(pack_f16x2(float_from16<kBF16>((uint16_t)w[ks].x) * fac.up,
+                                                             float_from16<kBF16>((uint16_t)(w[ks].x >> 16)) * fac.up),
+                                                  pack_f16x2(float_from16<kBF16>((uint16_t)w[ks].y) * fac.up,
+                                                             float_from16<kBF16>((uint16_t)(w[ks].y >> 16)) * fac.up));
+#pragma unroll
+                for (int e = 0; e < E; ++e) qf[nt][e] = __shfl_sync(0xffffffffu, fac.down, (2 * t + e) * 4);
+            }
+        }
         int lim[NT][E];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = (nt * 2 + e) * 4 + t;
-                qf[nt][e] = s_qf[c];
-                lim[nt][e] = p.causal ? min(k1, len - p.Sq + c / p.group + 1) : k1;
-            }
+            for (int e = 0; e < E; ++e)
+                lim[nt][e] = p.causal ? min(k1, len - p.Sq + ((nt * 2 + e) * 4 + t) / p.group + 1) : k1;
         const int full = p.causal ? min(k1, len - p.Sq + 1) : k1;  // keys that every row sees
 
         float o[KS][NT][4], ms[NT][E], mo[NT][E], l[NT][E];
@@ -780,7 +825,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
 
         const Kv8Seg done = sg;
         more = cw.next(p, plan, rng, W, sg);
-        if (more && !solo) load_queries(sg, warp, raw_q);
+        if (more && !solo) load_queries(sg);
 
         // Per query row the maxima and sums over the lanes of one t.
         float m_all[NT][E], sum_all[NT][E];
@@ -828,7 +873,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             continue;
         }
         // Join the four warps through shared memory; the outputs, brought to one reference, are added
-        // up in two buffers, warps 2 and 3 onto what 0 and 1 have left there.
+        // up in a buffer or two, by one or two warps at a time.
         if (g == 0) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -852,7 +897,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
 #pragma unroll
                     for (int w = 1; w < kKv8Warps; ++w) m = fmaxf(m, s_mo[w][col]);
                     const float f = ex2_approx(mo[nt][e] - m);
-                    float* row = exch + ((warp & 1) * HB * 4 + col) * XD;
+                    float* row = exch + (warp % C::Bufs * HB * 4 + col) * XD;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         float2* at = reinterpret_cast<float2*>(row) + k * 8 + g;
@@ -865,7 +910,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                     }
                 }
         };
-        if (warp < 2 && warp < tiles) leave(false);
+        if (warp < C::Bufs && warp < tiles) leave(false);
         if (tid >= 64 && tid < 64 + cols) {
             const int col = tid - 64;
             float Mo = s_mo[0][col], Ms = s_ms[0][col], L = 0.f;
@@ -882,10 +927,12 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             s_lse[col] = log_sum(Ms, L);
         }
         __syncthreads();
-        if (tiles > 2) {  // else warps 2 and 3 had none
-            if (warp >= 2 && warp < tiles) leave(true);
-            __syncthreads();
-        }
+#pragma unroll
+        for (int w = C::Bufs; w < kKv8Warps; w += C::Bufs)
+            if (tiles > w) {  // else warp w and those behind it had none
+                if (warp >= w && warp < w + C::Bufs && warp < tiles) leave(true);
+                __syncthreads();
+            }
         for (int i = tid; i < cols * (D / 2); i += kKv8Threads) {
             // Pair u of dims is block k, row g of the products; four threads of one g take
             // neighbouring pairs.
@@ -901,7 +948,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                 d = (k >> 3) * 128 + gg * 16 + (k & 7) * 2;
             }
             const float2 v0 = *reinterpret_cast<const float2*>(exch + col * XD + (k * 8 + gg) * 2);
-            const float2 v1 = tiles > 1
+            const float2 v1 = C::Bufs > 1 && tiles > 1
                                   ? *reinterpret_cast<const float2*>(exch + (HB * 4 + col) * XD + (k * 8 + gg) * 2)
                                   : make_float2(0.f, 0.f);
             const float f = s_f[col], finv = s_finv[col];
@@ -926,7 +973,7 @@ fa_status launch_kv8_split(const Kv8DecParams& p, cudaStream_t s) {
     using C = Kv8Cfg<D, HB>;
     static int attr[64] = {0};
     constexpr int most = C::FixedBytes + Kv8Plan::bytes(kKv8MaxB);
-    static_assert(most <= 227 * 1024 - 1024, "shared memory of a CTA");
+    static_assert(most <= 227 * 1024 - 1536, "shared memory of a CTA");
     if (!ensure_smem_attr((const void*)kv8_split_kernel<D, HB, kBF16>, most, attr)) return FA_ERR_CUDA;
     return launch_overlapped(kv8_split_kernel<D, HB, kBF16>, p.grid, kKv8Threads,
                              C::FixedBytes + Kv8Plan::bytes(p.B), s, p);
@@ -971,13 +1018,16 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecParams p) {
     constexpr int Vec = V % 4 == 0 ? 4 : V % 2 == 0 ? 2 : 1;  // values of a lane side by side
     __shared__ __align__(16) float s_acc[WPR > 1 ? 8 : 1][D];
     __shared__ float s_sum[8], s_max[8];
+    __shared__ int s_units[kKv8MaxB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * Rows + warp / WPR, part = warp % WPR;
     const float kNegInf = -__int_as_float(0x7f800000);
     const int b = row / (p.Sq * p.Hq), tok = row / p.Hq % p.Sq, h = row % p.Hq;
+    for (int i = threadIdx.x; i < p.B; i += 256) s_units[i] = kv8_units(kv8_len(p, i));
+    __syncthreads();
     int before = 0, sum = 0, units = 0, most = 0;
     for (int i = lane; i < p.B; i += 32) {
-        const int t = kv8_units(kv8_len(p, i));
+        const int t = s_units[i];
         before += i < b ? t : 0;
         units += i == b ? t : 0;
         sum += t;
@@ -1107,7 +1157,9 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     // kernel (2 us); it pays where it evens out the work of more pairs than CTAs, or cuts fewer
     // pairs into two pieces each or more (8 pairs of 148..445 keys, D = 64, 10 rows, took 11.5 us in 8
     // ranges and 9.6 whole).
-    const int per_sm = p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::CTAS : Kv8Cfg<D, 4>::CTAS;
+    const int per_sm = p.group * p.Sq <= 4   ? Kv8Cfg<D, 1>::resident(a.B)
+                       : p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::resident(a.B)
+                                             : Kv8Cfg<D, 4>::resident(a.B);
     const long long pairs = (long long)a.B * a.pool.Hkv, resident = (long long)per_sm * a.num_sms;
     const long long most = pairs * ((p.capacity + kKv8Unit - 1) / kKv8Unit);
     const long long ranges = std::min({resident, most, std::max(a.slots / 2, a.slots - pairs)});
