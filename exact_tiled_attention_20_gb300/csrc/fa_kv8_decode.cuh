@@ -311,6 +311,14 @@ struct Kv8Cfg {
     static __device__ __forceinline__ uint32_t run_step(int c) {
         return D == 96 && c >= 4 ? 512 : 16 * WA;
     }
+    // The first of the two dims whose sums a lane of row g holds in block k of O^T; it has them in
+    // o[k][.][e] and o[k][.][2 + e].
+    static __device__ __forceinline__ int dim(int k, int g) {
+        if constexpr (WA == 64)
+            return k < 4 ? g * 8 + k * 2 : 64 + g * 4 + (k - 4) * 2;
+        else
+            return (k >> 3) * 128 + g * 16 + (k & 7) * 2;
+    }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -347,6 +355,11 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     lo = e4m3x2_to_f16x2((uint16_t)(w & 0xffffu));
     hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+}
+
+// Whether one of a word's codes is NaN: all seven bits below its sign.
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+    return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
 }
 
 // D(16 x 8) += A(16 x 16) B(16 x 8), f16 in, fp32 out.  Lane 4 g + t holds A rows g, g + 8 at
@@ -765,6 +778,40 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                     for (int s = 0; s < NSUB; ++s)
                         l[nt][e] += ex2_approx(sc[s][0][nt][e] - ms[nt][e]) + ex2_approx(sc[s][1][nt][e] - ms[nt][e]);
 
+            // Keys that the mask hides from some rows have P = 0 there, which a NaN code of V would not
+            // respect.  So a NaN among them is brought to the rows that see it, and becomes a zero.
+            const int hidden = max(full - k0 - j * KT, 0), last = min(k1 - k0 - j * KT, KT);
+            if (hidden < last) {
+                bool bad = false;
+                for (int i = hidden * (D / 16) + lane; i < last * (D / 16); i += 32) {
+                    uint32_t w[4];
+                    lds128(sv + C::unit(i / (D / 16), i % (D / 16)), w);
+                    bad |= has_nan(w[0]) || has_nan(w[1]) || has_nan(w[2]) || has_nan(w[3]);
+                }
+                if (__any_sync(0xffffffffu, bad)) {
+                    for (int r = hidden; r < last; ++r)
+#pragma unroll
+                        for (int k = 0; k < KS; ++k)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int d = C::dim(k, g) + i;
+                                if ((lds8(sv + C::unit(r, d / 16) + d % 16) & 0x7f) != 0x7f) continue;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int e = 0; e < E; ++e)
+                                        if (k0 + j * KT + r < lim[nt][e])
+                                            o[k][nt][2 * i + e] = __int_as_float(0x7fffffff);
+                            }
+                    __syncwarp();
+                    for (int i = hidden * D + lane; i < last * D; i += 32) {
+                        const uint32_t at = sv + C::unit(i / D, i % D / 16) + i % 16;
+                        if ((lds8(at) & 0x7f) == 0x7f) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+                    }
+                    __syncwarp();
+                }
+            }
+
             // O^T += V^T P^T: 16 dims x 8 query rows over 16 keys.  A lane's units of keys 2 t,
             // 2 t + 1 (and + 8) are interleaved into pairs of keys.
 #pragma unroll
@@ -861,8 +908,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
                     const size_t row = ((size_t)b * p.Sq + tok) * p.Hq + h;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
-                        const int d = C::WA == 64 ? (k < 4 ? g * 8 + k * 2 : 64 + g * 4 + (k - 4) * 2)
-                                                  : (k >> 3) * 128 + g * 16 + (k & 7) * 2;
+                        const int d = C::dim(k, g);
                         *reinterpret_cast<uint32_t*>(o16 + row * D + d) =
                             pack2<kBF16>(o[k][nt][e] * finv * f, o[k][nt][2 + e] * finv * f);
                     }
@@ -937,16 +983,15 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             // Pair u of dims is block k, row g of the products; four threads of one g take
             // neighbouring pairs.
             const int col = i / (D / 2), u = i % (D / 2);
-            int k, gg, d;
+            int k, gg;
             if constexpr (C::WA == 64) {
                 k = u < 32 ? u & 3 : 4 + (u & 1);
                 gg = u < 32 ? u >> 2 : (u - 32) >> 1;
-                d = u < 32 ? gg * 8 + k * 2 : 64 + gg * 4 + (k - 4) * 2;
             } else {
                 k = (u & 3) + (u >> 5) * 4;
                 gg = (u >> 2) & 7;
-                d = (k >> 3) * 128 + gg * 16 + (k & 7) * 2;
             }
+            const int d = C::dim(k, gg);
             const float2 v0 = *reinterpret_cast<const float2*>(exch + col * XD + (k * 8 + gg) * 2);
             const float2 v1 = C::Bufs > 1 && tiles > 1
                                   ? *reinterpret_cast<const float2*>(exch + (HB * 4 + col) * XD + (k * 8 + gg) * 2)

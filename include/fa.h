@@ -306,8 +306,9 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  * (Hq / Hkv) * Sq <= 16.  A token that sees no key gets O = 0 and LSE = -inf.  Cached codes
  * enter the products exactly; the probabilities, with V's scales in them, are rounded to fp16 for
  * P.V (11 bits for weights down to 2^-25 of the row's largest, fewer below; one under 2^-36 of it may
- * vanish); O is rounded once.  What lies in the pool behind a sequence's last key is not used, NaN codes
- * there included.  Keys on a page outside the pool count as zero rows.
+ * vanish); O is rounded once.  What lies in the pool behind a sequence's last key is not used, nor is a key
+ * that `causal` hides from a token used for it, NaN codes there included.  Keys on a page outside the
+ * pool count as zero rows.
  *   num_splits  sizes the workspace, which holds B * Hkv * num_splits partial results (<= 0:
  *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0)).  The keys of
  *             all (sequence, kv head) pairs are laid end to end and cut into equal ranges, one

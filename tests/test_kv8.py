@@ -404,6 +404,37 @@ def test_decode_nan_key_reaches_its_rows_only(fa, D):
     assert o3[0, 0, 2:, 17].isnan().all() and o3[0].isnan().sum() == 2 and lse3.isfinite().all()
 
 
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("group,Sq,length,seqs", [(1, 2, 200, 1), (2, 4, 64, 1), (4, 4, 33, 1), (1, 16, 2050, 2),
+                                                  (1, 16, 7, 1), (2, 3, 70, 240)])
+def test_decode_nan_of_a_hidden_key(fa, D, group, Sq, length, seqs):
+    """NaN codes among the last Sq keys, in K or in V, change nothing for the tokens that the mask
+    hides them from (with one in K the seen rows' scores no longer move the references: other
+    roundings within the bound).  240 sequences: warps take pairs alone."""
+    Hkv, lens = 2, [length] * seqs
+    pool, q, o, lse = _decode_case(fa, D, group * Hkv, Hkv, Sq, 16, lens, seed=9)
+    ref = kv8.decode(q.double().numpy()[:1], pool.np, pool.table_np[:1], lens[:1], 1 / math.sqrt(D), True)
+    for back in range(1, min(Sq, length)):        # the key `back` before the last: tokens from Sq - 1 - back on see it
+        key, first = length - 1 - back, Sq - 1 - back
+        page, slot = pool.table_np[0, key // 16], key % 16
+        dim = (back * 37) % D
+        for which in (0, 1):
+            was = pool.np[which][page, 1, slot, dim]
+            pool.np[which][page, 1, slot, dim] = 0x7F + 0x80 * (back % 2)
+            pool.upload()
+            o2, lse2 = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int(lens))
+            pool.np[which][page, 1, slot, dim] = was
+            assert torch.equal(o2[1:], o[1:]) and torch.equal(o2[0, :, :group], o[0, :, :group])
+            seen = o2[0, first:, group:]
+            if which == 0:
+                assert seen.isnan().all() and lse2[0, group:, first:].isnan().all()
+                o2[0, first:, group:], lse2[0, group:, first:] = o[0, first:, group:], lse[0, group:, first:]
+                _check(o2[:1], lse2[:1], ref, length, D, "bf16")
+            else:
+                assert seen[..., dim].isnan().all() and seen.isnan().sum() == seen[..., dim].numel()
+                assert torch.equal(o2[0, :first], o[0, :first]) and torch.equal(lse2, lse)
+
+
 def test_decode_clamps_lengths_and_takes_all_empty(fa):
     pool, q, o, lse = _decode_case(fa, 128, 4, 2, 1, 16, [64, 64], seed=4)
     # max_pages is one more than needed: fill it too, then ask for more keys than there are
