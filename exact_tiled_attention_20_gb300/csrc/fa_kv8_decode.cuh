@@ -1211,13 +1211,17 @@ fa_status launch_kv8_decode_d(const Kv8DecodeArgs& a, cudaStream_t s) {
     p.whole = a.slots == 0 || ranges < std::min(resident, 2 * pairs);
     p.grid = (int)(p.whole ? std::min(resident, pairs) : ranges);
     // A warp alone needs no join, but its tiles come one after another: better while they are few
-    // and the pairs many.  Measured, in microseconds with CTAs and with warps, D = 128 where not
-    // said: 2048 pairs of 64 keys 18.5, 13.0, of 10..320 32.2, 27.8, of 10..500 38.1, 39.6 (D = 64);
-    // 1600 of 10..120, D = 256, 24.1, 22.0, of 10..500 43.4, 57.1; 488 of 4, D = 64, 10.0, 7.8; 512
-    // of 1..512 15.3, 24.0.
+    // and the pairs many.  Measured, in microseconds with CTAs and with warps, one query row and
+    // D = 64 where not said.  At least a pair for each warp: 2048 pairs of 10..500 keys 26.9, 25.4, with
+    // 8 rows 40.2, 34.5, of 10..1000 with 8 rows 53.1, 50.1, of 100..1000 with 8 rows, D = 128, 68.9, 73.1.
+    // Fewer: 1024 of 10..500 18.4, 20.9; of 64, D = 128 (2048), 18.4, 13.0.  Fewer than two for each CTA:
+    // 488 of 4 6.8, 4.9; 512 of 1..128 7.3, 7.3, of 1..250 8.7, 9.8.  D = 256: 1600 of 10..120 25.0, 22.2,
+    // of 10..300 34.7, 40.6.
     p.solo_keys = 0;
-    if (p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::QRegs : Kv8Cfg<D, 4>::QRegs)
-        p.solo_keys = pairs >= 2ll * p.grid ? (D == 256 ? 128 : 320) : pairs > p.grid ? 128 : 0;
+    if (p.group * p.Sq <= 8 ? Kv8Cfg<D, 2>::QRegs : Kv8Cfg<D, 4>::QRegs) {
+        if (pairs > p.grid) p.solo_keys = 128;
+        if (D != 256 && pairs >= 2ll * p.grid) p.solo_keys = pairs >= (long long)kKv8Warps * p.grid ? 512 : 320;
+    }
     fa_status st;
     if (p.group * p.Sq <= 4)
         st = a.bf16 ? launch_kv8_split<D, 1, true>(p, s) : launch_kv8_split<D, 1, false>(p, s);

@@ -12,7 +12,9 @@ def host(B, Hkv, capacity, slots, resident, D=128, in_registers=True):
     grid = min(resident, pairs) if whole else ranges
     solo = 0
     if in_registers:
-        solo = (128 if D == 256 else 320) if pairs >= 2 * grid else 128 if pairs > grid else 0
+        solo = 128 if pairs > grid else 0
+        if D != 256 and pairs >= 2 * grid:
+            solo = 512 if pairs >= 4 * grid else 320
     return grid, whole, solo
 
 

@@ -465,6 +465,16 @@ def test_decode_many_short_pairs(fa, D, group, Sq, longest, ns):
     _decode_case(fa, D, group * 12, 12, Sq, 16, lens, ns=ns, seed=group)
 
 
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("group,Sq,longest", [(1, 1, 512), (2, 4, 512), (4, 1, 513), (5, 3, 500)])
+def test_decode_a_pair_for_each_warp(fa, D, group, Sq, longest):
+    """1920 pairs, four for each CTA: lengths at and one past the longest that warps take alone."""
+    rng = np.random.default_rng(D)
+    lens = (rng.integers(0, 30, 160) * (rng.random(160) < 0.8)).tolist()
+    lens[3], lens[90], lens[-1] = longest, 257, 33
+    _decode_case(fa, D, group * 12, 12, Sq, 16, lens, seed=group)
+
+
 def test_decode_contiguous_cache_is_one_page_each(fa):
     """page_size = the whole capacity and an identity table: the same bits as small pages."""
     pool, q, o, lse = _decode_case(fa, 96, 4, 2, 2, 16, [300, 222], ns=5)

@@ -35,7 +35,7 @@ def _check(lens, Hkv, capacity, ns, resident, D):
 def test_every_key_once_and_every_piece_found(seed):
     rng = random.Random(seed)
     B, Hkv = rng.choice([1, 2, 3, 9, 40]), rng.choice([1, 2, 3, 8])
-    top = rng.choice([1, 40, 130, 320, 2000, 9000])
+    top = rng.choice([1, 40, 130, 320, 500, 2000, 9000])
     lens = [rng.choice([0, 1, top, rng.randint(0, top)]) for _ in range(B)]
     lens[rng.randrange(B)] = top
     capacity = max(16, -(-top // 16) * 16 * rng.choice([1, 1, 3]))
