@@ -63,7 +63,6 @@ constexpr int kKv8Lead = 4;   // units charged to each pair beside its keys
 constexpr int kKv8Threads = 128;
 constexpr int kKv8Warps = kKv8Threads / 32;
 constexpr int kKv8MaxB = 1024;
-constexpr int kTableLines = 8;  // lines of the block table that a CTA prefetches
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ int kv8_len(const Kv8DecParams& p, int b) {
@@ -113,11 +112,9 @@ __device__ __forceinline__ float float_from16(uint16_t x) {
     }
 }
 
-// Thread i prefetches 128-byte line first + i of `bytes` bytes, i < kTableLines.
-__device__ __forceinline__ void kv8_prefetch(const void* base, long long bytes, int first) {
-    const long long at = ((long long)first + threadIdx.x) * 128;
-    if (threadIdx.x < kTableLines && at < bytes)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(base) + at));
+// Sends for `bytes` bytes to L2 (a hint); both multiples of 16.
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // The plan in shared memory: the units of one pair of each sequence summed over the
@@ -173,6 +170,16 @@ __device__ __forceinline__ int kv8_make_plan(const Kv8DecParams& p, const Kv8Pla
     if (threadIdx.x == kKv8Threads - 1) t.prefix[p.B] = run;
     __syncthreads();
     return most;
+}
+
+// Whether a length is no longer what the plan was made of (all threads; a barrier).
+__device__ __forceinline__ bool kv8_plan_is_stale(const Kv8DecParams& p, const Kv8Plan& t) {
+    bool stale = false;
+    for (int b = threadIdx.x; b < p.B; b += kKv8Threads) {
+        const int units = t.prefix[b + 1] - t.prefix[b];
+        stale |= kv8_len(p, b) != (units > 0 ? (units - kKv8Lead) * kKv8Unit - t.pad[b] : 0);
+    }
+    return __syncthreads_or(stale);
 }
 
 // The part of one pair that lies in one range.
@@ -409,17 +416,60 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     plan.prefix = reinterpret_cast<int*>(rest + C::ExchBytes + C::QBytes);
     plan.pad = reinterpret_cast<uint8_t*>(plan.prefix + p.B + 1);
 
-    // While the kernel before may still be running: the lengths and the block table, which the
-    // plan and the first copies wait for in turn, are sent for to L2 (a hint: it reads nothing).
-    kv8_prefetch(p.kv_lens, p.B * 4ll, (int)blockIdx.x * kTableLines);
-    kv8_prefetch(p.pool.table, (long long)p.B * p.pool.max_pages * 4, (int)blockIdx.x * kTableLines);
-    grid_dependency_wait();
+    const int Hkv = p.pool.Hkv, cols = p.group * p.Sq;
     // A group of gw warps works through a range; this is warp wi of it.
-    const int most = kv8_make_plan(p, plan, sm.warp_sum, sm.warp_max);
-    const bool solo = C::QRegs && kv8_solo(p, most);
-    const int gw = solo ? 1 : kKv8Warps, wi = solo ? 0 : warp;
-    const int rng = solo ? (int)blockIdx.x * kKv8Warps + warp : (int)blockIdx.x;
-    const int W = kv8_width(p, plan.prefix[p.B], solo ? p.grid * kKv8Warps : p.grid);
+    bool solo;
+    int gw, wi, rng, W;
+    Kv8Walk lw, cw;  // the loader's and the products'
+    auto make_plan = [&]() {
+        const int most = kv8_make_plan(p, plan, sm.warp_sum, sm.warp_max);
+        solo = C::QRegs && kv8_solo(p, most);
+        gw = solo ? 1 : kKv8Warps;
+        wi = solo ? 0 : warp;
+        rng = solo ? (int)blockIdx.x * kKv8Warps + warp : (int)blockIdx.x;
+        W = kv8_width(p, plan.prefix[p.B], solo ? p.grid * kKv8Warps : p.grid);
+        lw.init(p, plan, rng, W, p.whole || solo);
+    };
+    // The 16-key run of the pool that holds keys key .. key + 15 of a segment: -1 where there is none
+    // (behind k1, or a page outside the pool).
+    auto run_of = [&](const Kv8Seg& s, int key, bool early) -> int {
+        if (key >= s.k1) return -1;
+        // key / page_size: the reciprocal, rounded up, gives the quotient or one more
+        unsigned pi = __umulhi((unsigned)key, p.page_recip);
+        int slot = (int)((unsigned)key - pi * (unsigned)p.pool.page_size);
+        if (slot < 0) {
+            --pi;
+            slot += p.pool.page_size;
+        }
+        const int* at = p.pool.table + (size_t)s.b * p.pool.max_pages + pi;
+        const int page = early ? __ldcg(at) : *at;
+        if (page < 0 || page >= p.pool.num_pages) return -1;
+        return (page * Hkv + s.hk) * (p.pool.page_size / 16) + slot / 16;
+    };
+    // While the kernel before may still be running and the memory idles: the plan, and the warps'
+    // first tiles are sent for to L2.  The lengths and the table may change until that kernel is
+    // done, so this is a guess: nothing but L2 lines depends on it, and the plan is made again if a
+    // length is another afterwards.  Behind a kernel that lets this one start early (this library's;
+    // others' are done by then) it saves 0.4 us by the plan and 0.9 by the tiles: one sequence of
+    // 32768 17.9 -> 16.6 us, the lengths 1024..32768 47.9 -> 46.4.  More tiles: 16.6 with 2, 17.5 with 4;
+    // for warps alone 12.8 us without and 13.5 with (2048 pairs of 64 keys).
+    make_plan();
+    {
+        Kv8Walk guess = lw;
+        Kv8Seg s;
+        if (!solo && guess.next(p, plan, rng, W, s) && lane < NSUB) {
+            const int run = run_of(s, s.k0 + wi * KT + lane * 16, true);
+            if (run >= 0) {
+                prefetch_l2(p.pool.k + (size_t)run * (16 * D), 16 * D);
+                prefetch_l2(p.pool.v + (size_t)run * (16 * D), 16 * D);
+                prefetch_l2(p.pool.ks + (size_t)run * 16, 16);
+                prefetch_l2(p.pool.vs + (size_t)run * 16, 16);
+            }
+        }
+    }
+    grid_dependency_wait();
+    if (kv8_plan_is_stale(p, plan)) make_plan();
+    cw = lw;
     uint2* s_q = reinterpret_cast<uint2*>(C::QRegs ? rest : rest + C::ExchBytes);
     uint16_t* o16 = static_cast<uint16_t*>(p.o);
     const uint16_t* q16 = static_cast<const uint16_t*>(p.q);
@@ -431,17 +481,12 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
         dst[i] = ring + C::unit(row, c);
         step[i] = C::run_step(c);
     }
-    const int Hkv = p.pool.Hkv, cols = p.group * p.Sq;
-    Kv8Walk lw, cw;  // the loader's and the products'
-    lw.init(p, plan, rng, W, p.whole || solo);
-    cw = lw;
 
     // The loader walks the warp's tiles (wi, wi + gw, ... of each segment) up to NST - 1
     // ahead of the products, across the ends of segments.
     Kv8Seg ls;
     int lj = 0, ltiles = 0, run = -1;
-    // Steps to the next tile and looks up the 16-key run of the pool that holds run lane % NSUB
-    // of it: -1 where there is none (behind k1, or a page outside the pool).
+    // Steps to the next tile and looks up run lane % NSUB of it.
     auto next_tile = [&]() {
         lj += gw;
         while (lj >= ltiles) {
@@ -454,20 +499,7 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
             ltiles = (ls.k1 - ls.k0 + KT - 1) / KT;
             lj = wi;
         }
-        const int key = ls.k0 + lj * KT + (lane % NSUB) * 16;
-        run = -1;
-        if (key < ls.k1) {
-            // key / page_size: the reciprocal, rounded up, gives the quotient or one more
-            unsigned pi = __umulhi((unsigned)key, p.page_recip);
-            int slot = (int)((unsigned)key - pi * (unsigned)p.pool.page_size);
-            if (slot < 0) {
-                --pi;
-                slot += p.pool.page_size;
-            }
-            const int page = p.pool.table[(size_t)ls.b * p.pool.max_pages + pi];
-            if (page >= 0 && page < p.pool.num_pages)
-                run = (page * Hkv + ls.hk) * (p.pool.page_size / 16) + slot / 16;
-        }
+        run = run_of(ls, ls.k0 + lj * KT + lane % NSUB * 16, false);
     };
     // Starts the copies of the loader's tile into stage st; rows without a key become zeros.
     auto issue = [&](int st) {

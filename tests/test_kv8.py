@@ -621,6 +621,42 @@ def test_captured_split_decode_follows_the_lengths(fa):
         assert torch.equal(a, o) and torch.equal(b, lse)
 
 
+def test_lengths_written_by_the_kernel_before(fa):
+    """The decode starts, and guesses its plan, while the kernel before it may still be running; here
+    that kernel (a read whose bf16 rows are the int32 lengths: 1.25 * 2^-125 is 288) writes
+    other lengths.  Each decode has the bits of one whose lengths have long been there."""
+    rng = np.random.default_rng(21)
+    B, n = 32, 60000
+    pool = Pool(B * 26, 2, 16, 64, B, 26, seed=22)
+    pool.fill(rng, [400] * B)
+    q = torch.from_numpy(rng.standard_normal((B, 1, 8, 64))).to(torch.bfloat16).to(DEV)
+    sets, wants = [], []
+    for i in range(3):
+        # lengths 0, 256, 272, 288, 320, 352 and 384 (codes at scale 2^-127)
+        codes = rng.choice([0.0, 4.0, 4.5, 5.0, 6.0, 7.0, 8.0], B)
+        bits = torch.from_numpy(codes * 2.0 ** -127).to(torch.bfloat16).view(torch.int16)
+        lens = bits.to(torch.int32).tolist()
+        assert max(lens) <= 400 and sum(x > 0 for x in lens) > 10
+        row = np.zeros(64)
+        row[::2] = codes                          # low halves of the 32-bit lengths
+        k = np.zeros((n // 16, 1, 16, 64), np.uint8)
+        k[-1, 0, -1] = torch.from_numpy(row).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        k = torch.from_numpy(k).to(DEV).view(torch.float8_e4m3fn)
+        zero = torch.zeros(k.shape[:3], dtype=torch.uint8, device=DEV)
+        sets.append((k, k, zero, zero, torch.arange(n // 16, dtype=torch.int32, device=DEV).view(1, -1)))
+        wants.append(fa.fa_decode_splitkv_paged_fp8(q, *pool.args, _int(lens), num_splits=8))
+    out = [torch.empty(n, 1, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    kl = out[0][n - 1, 0].view(torch.int32)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(B, 8, 64, 8), dtype=torch.uint8, device=DEV)
+    got = [[torch.empty_like(q), torch.empty(B, 8, 1, device=DEV)] for _ in range(12)]
+    cu = _int([0, n])
+    for i, (o, lse) in enumerate(got):
+        fa.fa_kv_read_paged_fp8(*sets[i % 3], cu, k_out=out[0], v_out=out[1])
+        fa.fa_decode_splitkv_paged_fp8(q, *pool.args, kl, num_splits=8, workspace=ws, out=o, lse=lse)
+    for i, (o, lse) in enumerate(got):
+        assert torch.equal(o, wants[i % 3][0]) and torch.equal(lse, wants[i % 3][1])
+
+
 def test_two_streams_at_once(fa):
     """Two decodes with a workspace each on two streams give what each gives alone."""
     pool, q, o, lse = _decode_case(fa, 128, 8, 2, 1, 16, [1800, 900], ns=16, seed=6)
