@@ -115,7 +115,7 @@ fa_status fa_decode_splitkv_paged_fp8(const void* q, const void* k_pages, const 
     if (chk != FA_OK) return chk;
     // The plan counts 64-key units, and a few more for each (sequence, kv head) pair, in 32 bits.
     if ((long long)B * Hkv > 0x7fffffffLL / (capacity / 64 + 8)) return FA_ERR_UNSUPPORTED;
-    if ((long long)B * Sq * Hq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    if ((long long)B * Sq * Hq > 0x7fffffffLL - 8) return FA_ERR_UNSUPPORTED;  // the merge counts past the last row
     const int sms = device_sms();
     if (sms <= 0) return FA_ERR_CUDA;
     const bool whole = num_splits == 1;

@@ -30,11 +30,13 @@
 // and nothing but the end of a pair makes it wait for another warp.
 //
 // Measured (split and merge, back to back, inputs larger than L2): lengths 1024..32768 x 8
-// sequences, 8 kv heads of 4 query heads, D = 128, 279 MB: 47.7 us, 5.85 TB/s, 86 % of a copy's
-// rate; 64 sequences of 1..8192, 541 MB: 88.7 us, 6.1 TB/s, 90 %; 8 of U[1024, 32768] at D = 64, 96,
-// 128, 256 with 158, 235, 313, 623 MB: 31.4, 45.5, 52.9, 99 us, 74, 76, 87, 93 %.  About 8 us of a call do not stream: 1.0 for the plan, 0.5 for the first
-// table entries, 1.4 for the last join and about 1 of uneven ends, 2 for the merge kernel, 1 to
-// pass from one kernel to the next and 1 to fill and drain the memory's queues.
+// sequences, 8 kv heads of 4 query heads, D = 128, 279 MB: 46.4 us, 6.0 TB/s, 89 % of a copy's
+// rate; 64 sequences of 1..8192, 542 MB: 88.4 us, 6.1 TB/s, 90 %; 8 of U[1024, 32768] at D = 64, 96,
+// 128, 256 with 158, 235, 313, 623 MB: 30.4, 44.5, 51.8, 99 us, 76, 78, 89, 92 %.  About 6.6 us of a
+// call do not stream (one sequence of 32768: 16.6 us, 10.0 at a copy's rate).  A trace from before
+// the plan came ahead of the wait (then 17.9) placed 7.9: 1.0 for the plan, 0.5 for the first table
+// entries, 1.4 for the last join and about 1 of uneven ends, 2 for the merge kernel, 1 to pass
+// from one kernel to the next and 1 to fill and drain the memory's queues.
 #pragma once
 
 #include <algorithm>
