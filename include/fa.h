@@ -237,7 +237,8 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void *q, const void *k_cache,
  * with one power-of-two scale:
  *   k_pages, v_pages    [num_pages, Hkv, page_size, D]  e4m3 codes
  *   k_scales, v_scales  [num_pages, Hkv, page_size]     bytes s; the scale is 2^(s - 127)
- * and stands for code * 2^(s - 127).  The head comes before the slot, other than in the
+ * and stands for code * 2^(s - 127), 0 <= s <= 254 (the append writes 247 at most; what a key with
+ * s = 255 that a call uses gives is not specified).  The head comes before the slot, other than in the
  * 16-bit pools, so that what one head reads of a page is one run of memory.
  *   block_table         device int32 [B, max_pages_per_seq]: key r of sequence b is slot
  *                       r % page_size of page block_table[b][r / page_size]
