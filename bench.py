@@ -1076,8 +1076,7 @@ def run_case(argv):
             ws = torch.empty(fa.fa_decode_workspace_bytes(w.B, w.Hq, d, ns), dtype=torch.uint8, device=dev)
             q = rnd(w.B, 1, w.Hq, d)
             o, lse = torch.empty_like(q), torch.empty(w.B, w.Hq, 1, device=dev)
-            call = lambda: fa.fa_decode_splitkv_paged_fp8(q, *pool, lens, num_splits=ns, workspace=ws,  # noqa: E731
-                                                          out=o, lse=lse)
+            call = lambda: fa.fa_decode_splitkv_paged_fp8(q, *pool, lens, workspace=ws, out=o, lse=lse)  # noqa: E731
     else:
         raise SystemExit(f"unknown case {kind!r}; kinds:\n" + CASES)
     call()

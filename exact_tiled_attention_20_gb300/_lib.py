@@ -609,10 +609,13 @@ def fa_decode_splitkv_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_t
     handle, other = _stream_on(device, stream)
     ns = int(num_splits)
     if workspace is None:
-        if ns <= 0:
+        room = ns
+        if room <= 0:
+            # Sizes the workspace and is not passed on: the default may be 1, and a caller's 1
+            # forbids cutting.
             with torch.cuda.device(device):
-                ns = lib.fa_decode_default_splits(B, Hkv, page * max_pages, 0)
-        workspace = _made(torch.empty(max(16, lib.fa_decode_workspace_bytes(B * Sq, Hq, D, ns)),
+                room = lib.fa_decode_default_splits(B, Hkv, page * max_pages, 0)
+        workspace = _made(torch.empty(max(16, lib.fa_decode_workspace_bytes(B * Sq, Hq, D, room)),
                                       dtype=_U8, device=q.device), other)
     elif not _is(workspace, _U8, device, None):
         _refuse(("workspace", workspace, _U8, device, None))

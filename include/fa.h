@@ -311,11 +311,15 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  * that `causal` hides from a token used for it, NaN codes there included.  Keys on a page outside the
  * pool count as zero rows.
  *   num_splits  sizes the workspace, which holds B * Hkv * num_splits partial results (<= 0:
- *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0)).  The keys of
- *             all (sequence, kv head) pairs are laid end to end and cut into equal ranges, one
- *             per CTA that can be resident, but at most half as many as that, since a range
- *             leaves up to two partial results; where this gives fewer ranges than pairs to
- *             spread, and where num_splits is 1, pairs are not cut and a CTA takes whole ones.
+ *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0) of a pair).  The
+ *             keys of all (sequence, kv head) pairs are laid end to end and cut into equal ranges,
+ *             one per CTA that can be resident, but no more than the partial results have room
+ *             for, of which r ranges leave at most r + min(r, B * Hkv); where this gives fewer
+ *             ranges than pairs to spread, pairs are not cut and a CTA takes whole ones.
+ *             1 is taken at its word: no pair is cut, however the lengths differ.  So a caller
+ *             who sizes the workspace by fa_decode_default_splits, which answers 1 from eight
+ *             pairs an SM up, passes 0 and not that answer: 1280 pairs of 1000 keys but for
+ *             eight of 32768 have ranges of 4160 keys with 0, and of 33768 with 1.
  *   workspace at least fa_decode_workspace_bytes(B * Sq, Hq, D, num_splits) bytes (after the
  *             default is applied); no initialisation; not used, and may be NULL, where
  *             num_splits is 1.  Calls that may overlap on the GPU need one each.

@@ -475,6 +475,34 @@ def test_decode_a_pair_for_each_warp(fa, D, group, Sq, longest):
     _decode_case(fa, D, group * 12, 12, Sq, 16, lens, seed=group)
 
 
+def test_decode_without_a_workspace_cuts_as_with_one(fa):
+    """More than eight pairs an SM, where the default is one partial result a pair, and a long
+    sequence among short ones: the call that makes its workspace has the bits of one that is given
+    it, so the long pairs are cut in both, and other bits than one that may not cut."""
+    rng = np.random.default_rng(31)
+    B, Hkv, D, page, mp = 160, 8, 64, 64, 96
+    lens = rng.integers(1, 40, B)
+    lens[77] = 6000
+    pool = Pool(B * 1 + mp, Hkv, page, D, 1, 1, seed=31)
+    pool.table_np = np.full((B, mp), -1, np.int32)
+    pages = rng.permutation(B + mp)
+    pool.table_np[:, 0] = pages[:B]
+    pool.table_np[77] = pages[B:]
+    pool.fill(rng, lens)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert B * Hkv >= 8 * sms and fa.fa_decode_default_splits(B, Hkv, mp * page) == 1
+    q = torch.from_numpy(rng.standard_normal((B, 1, Hkv, D))).to(torch.bfloat16).to(DEV)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(B, Hkv, D, 1), dtype=torch.uint8, device=DEV)
+    given = fa.fa_decode_splitkv_paged_fp8(q, *pool.args, _int(lens), workspace=ws)
+    made = fa.fa_decode_splitkv_paged_fp8(q, *pool.args, _int(lens))
+    uncut = fa.fa_decode_splitkv_paged_fp8(q, *pool.args, _int(lens), num_splits=1)
+    assert torch.equal(made[0], given[0]) and torch.equal(made[1], given[1])
+    assert not torch.equal(uncut[1][77], given[1][77])
+    ref = kv8.decode(q.double().cpu().numpy(), pool.np, pool.table_np, lens, 1 / math.sqrt(D))
+    for o, lse in (made, uncut):
+        _check(o, lse, ref, 6000, D, "bf16")
+
+
 def test_decode_contiguous_cache_is_one_page_each(fa):
     """page_size = the whole capacity and an identity table: the same bits as small pages."""
     pool, q, o, lse = _decode_case(fa, 96, 4, 2, 2, 16, [300, 222], ns=5)

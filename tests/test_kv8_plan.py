@@ -49,3 +49,20 @@ def test_every_key_once_and_every_piece_found(seed):
 def test_an_empty_batch_has_no_work():
     grid, whole, solo = kv8_plan.host(4, 2, 256, 8, 456)
     assert kv8_plan.segments([0] * 4, 2, grid, whole, solo) == ([], {})
+
+
+def test_one_partial_result_a_pair_cuts_a_long_sequence_among_many():
+    """The default's room for 160 sequences of 8 kv heads: no range holds more than its units."""
+    lens = [1000] * 159 + [32768]
+    grid, whole, solo = kv8_plan.host(160, 8, 32768, 160 * 8, 456)
+    segs, _ = kv8_plan.segments(lens, 8, grid, whole, solo)
+    held = {}
+    for r, _, _, k0, k1, _ in segs:
+        held[r] = held.get(r, 0) + k1 - k0
+    width = -(-8 * sum(kv8_plan.units(n) for n in lens) // grid)
+    assert max(held.values()) <= width * kv8_plan.UNIT < 32768 / 7
+    grid, whole, solo = kv8_plan.host(160, 8, 32768, 0, 456)    # what a caller's 1 asks for
+    held = {}
+    for r, _, _, k0, k1, _ in kv8_plan.segments(lens, 8, grid, whole, solo)[0]:
+        held[r] = held.get(r, 0) + k1 - k0
+    assert max(held.values()) >= 32768
