@@ -466,11 +466,18 @@ def _stream_on(device, stream):
     return stream.cuda_stream, (None if stream.cuda_stream == current else stream)
 
 
-def _made(t, other):
-    """A tensor made for a call: its memory is not reused before `other`, the call's stream
-    where it is not the current one, is done with it."""
-    if other is not None:
-        t.record_stream(other)
+def _made(shape, dtype, device, other, returned=True):
+    """A tensor made for a call on `other`, or on the current stream where that is None.  Its memory is
+    of the call's stream: what was freed there, and is still in use there, is in use by work that
+    comes before the call; memory of the current stream's could still be in use by work that
+    nothing orders before it.  A `returned` tensor is read on the current stream, and its memory is
+    not reused before the work queued there when it is freed is done."""
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -574,9 +581,9 @@ def fa_kv_read_paged_fp8(k_pages, v_pages, k_scales, v_scales, block_table, cu_s
     handle, other = _stream_on(device, stream)
     shape = (int(total), Hkv, D)
     if k_out is None:
-        k_out = _made(torch.empty(shape, dtype=dtype, device=k_pages.device), other)
+        k_out = _made(shape, dtype, k_pages.device, other)
     if v_out is None:
-        v_out = _made(torch.empty(shape, dtype=dtype, device=k_pages.device), other)
+        v_out = _made(shape, dtype, k_pages.device, other)
     if not (_is(k_out, dtype, device, shape) and _is(v_out, dtype, device, shape)):
         _refuse(("k_out", k_out, dtype, device, shape), ("v_out", v_out, dtype, device, shape))
     _call_on(device, lib.fa_kv_read_paged_fp8, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
@@ -615,16 +622,16 @@ def fa_decode_splitkv_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_t
             # forbids cutting.
             with torch.cuda.device(device):
                 room = lib.fa_decode_default_splits(B, Hkv, page * max_pages, 0)
-        workspace = _made(torch.empty(max(16, lib.fa_decode_workspace_bytes(B * Sq, Hq, D, room)),
-                                      dtype=_U8, device=q.device), other)
+        workspace = _made(max(16, lib.fa_decode_workspace_bytes(B * Sq, Hq, D, room)), _U8, q.device, other,
+                          returned=False)
     elif not _is(workspace, _U8, device, None):
         _refuse(("workspace", workspace, _U8, device, None))
     if out is None:
-        out = _made(torch.empty_like(q), other)
+        out = _made(shape, dtype, q.device, other)
     elif not _is(out, dtype, device, shape):
         _refuse(("out", out, dtype, device, shape))
     if lse is None:
-        lse = _made(torch.empty((B, Hq, Sq), dtype=_F32, device=q.device), other)
+        lse = _made((B, Hq, Sq), _F32, q.device, other)
     elif not _is(lse, _F32, device, (B, Hq, Sq)):
         _refuse(("lse", lse, _F32, device, (B, Hq, Sq)))
     _call_on(device, lib.fa_decode_splitkv_paged_fp8, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),

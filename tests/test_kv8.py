@@ -702,6 +702,48 @@ def test_two_streams_at_once(fa):
         assert torch.equal(oo, (o, alone[0])[i % 2]) and torch.equal(ll, (lse, alone[1])[i % 2])
 
 
+def test_another_stream_leaves_the_current_ones_memory_alone(fa):
+    """Blocks of the sizes that a call makes, freed on the current stream while work queued there has
+    yet to read or to write them: a call on another stream, which nothing orders behind that work,
+    takes none of them.  And its outputs, freed while the current stream has yet to read them, are
+    not handed to its next call."""
+    pool, q, o_ref, lse_ref = _decode_case(fa, 128, 8, 2, 1, 16, [1800, 900], ns=16, seed=7)
+    qd, kl, cu = q.to(DEV), _int([1800, 900]), _int([0, 1800, 2700])
+    minus = -qd
+    k_ref, v_ref = fa.fa_kv_read_paged_fp8(*pool.args, cu, total=2700)
+    need = fa.fa_decode_workspace_bytes(2, 8, 128, 16)
+    sizes = [q.numel() * 2, lse_ref.numel() * 4, need] + [k_ref.numel() * 2] * 2
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for late in ("read", "written"):
+        kept = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        blocks = [torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)            # 0.1 s
+        for a, b in zip(kept, blocks):
+            if late == "read":
+                a.copy_(b)
+            else:
+                b.fill_(0x77)
+        del b, blocks
+        got = [*fa.fa_decode_splitkv_paged_fp8(qd, *pool.args, kl, num_splits=16, stream=other),
+               *fa.fa_kv_read_paged_fp8(*pool.args, cu, total=2700, stream=other)]
+        torch.cuda.synchronize()
+        assert late != "read" or all((a == 0x5A).all() for a in kept)
+        for a, b in zip(got, (o_ref, lse_ref, k_ref, v_ref)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    del got, a
+    for _ in range(3):
+        o, lse = fa.fa_decode_splitkv_paged_fp8(qd, *pool.args, kl, num_splits=16, stream=other)
+        torch.cuda.current_stream().wait_stream(other)
+        torch.cuda._sleep(50_000_000)
+        copies = o.clone(), lse.clone()
+        del o, lse
+        fa.fa_decode_splitkv_paged_fp8(minus, *pool.args, kl, num_splits=16, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(copies[0], o_ref) and torch.equal(copies[1], lse_ref)
+
+
 def test_offsets_past_32_bits(fa):
     """A pool of more than 2^32 bytes of codes: the last pages are written, read and decoded."""
     Hkv, page, D, B = 8, 64, 128, 2
