@@ -322,7 +322,8 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  *             eight of 32768 have ranges of 4160 keys with 0, and of 33768 with 1.
  *   workspace at least fa_decode_workspace_bytes(B * Sq, Hq, D, num_splits) bytes (after the
  *             default is applied); no initialisation; not used, and may be NULL, where
- *             num_splits is 1.  Calls that may overlap on the GPU need one each.
+ *             num_splits is 1.  Calls that may overlap on the GPU need one each.  A num_splits
+ *             for which these bytes pass 2^63 is FA_ERR_UNSUPPORTED.
  * The result does not depend on num_splits beyond rounding; the same inputs give the same
  * bits.
  */

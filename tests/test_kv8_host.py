@@ -62,6 +62,15 @@ def test_decode_refuses(lib, change, code):
     assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **change}.values()) == code
 
 
+def test_decode_refuses_partial_results_past_64_bits(lib):
+    """2^23 rows and a count for which the bytes of the partial results pass 2^64 and come out small."""
+    splits = -(-2 ** 39 // 257)
+    assert 2 ** 23 * splits * 257 * 4 > 2 ** 64
+    assert lib.fa_decode_workspace_bytes(1024, 1 << 13, 256, splits) < 1 << 40
+    change = dict(B=1024, Hq=1 << 13, Hkv=1 << 13, D=256, splits=splits, ws_bytes=1 << 40)
+    assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **change}.values()) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("change", [dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=16)])
 def test_decode_refuses_a_bad_workspace(lib, change):
     if not torch.cuda.is_available():
