@@ -1,4 +1,6 @@
 // fa_kv8_api.cu -- C entry points of the 8-bit paged KV cache: argument checks and dispatch.
+#include <cmath>
+
 #include "fa_kv8.cuh"
 
 namespace fa {
@@ -109,10 +111,11 @@ fa_status fa_decode_splitkv_paged_fp8(const void* q, const void* k_pages, const 
     const fa_status pool_chk = check_pool(k_pages, v_pages, k_scales, v_scales, block_table, B, Hkv, D, num_pages,
                                           page_size, max_pages_per_seq, dtype);
     if (pool_chk != FA_OK) return pool_chk;
+    if (!q || !kv_lens || !o) return FA_ERR_INVALID_ARG;
+    if (misaligned(q, 16) || misaligned(o, 16) || misaligned(kv_lens, 4) || misaligned(lse, 4)) return FA_ERR_INVALID_ARG;
+    if (Sq <= 0 || Hq <= 0 || Hq % Hkv != 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+    if ((long long)(Hq / Hkv) * Sq > 16) return FA_ERR_UNSUPPORTED;
     const int capacity = page_size * max_pages_per_seq;
-    const fa_status chk =
-        decode_check_args(q, k_pages, v_pages, kv_lens, o, lse, B, Sq, Hq, Hkv, D, capacity, scale, dtype);
-    if (chk != FA_OK) return chk;
     // The plan counts 64-key units, and a few more for each (sequence, kv head) pair, in 32 bits.
     if ((long long)B * Hkv > 0x7fffffffLL / (capacity / 64 + 8)) return FA_ERR_UNSUPPORTED;
     if ((long long)B * Sq * Hq > 0x7fffffffLL - 8) return FA_ERR_UNSUPPORTED;  // the merge counts past the last row

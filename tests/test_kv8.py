@@ -516,6 +516,27 @@ def test_decode_contiguous_cache_is_one_page_each(fa):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_decode_with_a_wide_table(fa):
+    """A table for 2^30 + 2^20 keys a sequence, over 2^31 in the batch: the bits of one for 2^20."""
+    B, Hq, Hkv, D, page = 2, 4, 1, 64, 1 << 20
+    g = torch.Generator(DEV).manual_seed(17)
+    pages = [torch.zeros(B, Hkv, page, D, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.zeros(B, Hkv, page, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    x = torch.randn(2, 700, Hkv, D, generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.randn(B, 1, Hq, D, generator=g, device=DEV).to(torch.bfloat16)
+    kl, cu = _int([400, 300]), _int([0, 400, 700])
+    outs = []
+    for mp in (1, 1025):
+        table = torch.full((B, mp), -1, dtype=torch.int32, device=DEV)
+        table[:, 0] = torch.tensor([1, 0], dtype=torch.int32)
+        pool = (*pages, *scales, table)
+        fa.fa_kv_append_paged_fp8(x[0], x[1], *pool, kl, cu_seqlens_new=cu)
+        outs.append((*fa.fa_decode_splitkv_paged_fp8(q, *pool, kl, num_splits=5),
+                     *fa.fa_kv_read_paged_fp8(*pool, cu, total=700)))
+    for a, b in zip(*outs):
+        assert a.isfinite().all() and torch.equal(a, b)
+
+
 def test_decode_guard_bands_and_no_lse(fa):
     """Writes stay inside O, LSE and the workspace; LSE may be absent at the C entry."""
     B, Hq, Hkv, D, Sq, ns, pad = 3, 8, 2, 96, 2, 7, 4096

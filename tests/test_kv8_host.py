@@ -87,6 +87,20 @@ def test_valid_calls_without_a_device_fail_loudly(lib):
     assert lib.fa_decode_splitkv_paged_fp8(*DECODE.values()) == CUDA
 
 
+def test_decode_takes_the_tables_that_append_and_read_take(lib):
+    """Table capacities whose product with B passes 2^31 (the kernels count per pair, in 64-key units): up
+    to the header's B * Hkv * (capacity / 64 + 8) < 2^31, not to 2^31 keys over the batch."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: these arguments would be launched")
+    wide = dict(B=2, Hkv=8, max_pages=(1 << 26) + 1)                        # 2^30 + 16 keys each
+    assert lib.fa_kv_append_paged_fp8(*{**APPEND, **wide}.values()) == CUDA
+    assert lib.fa_kv_read_paged_fp8(*{**READ, **wide}.values()) == CUDA
+    assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **wide}.values()) == CUDA
+    edge = dict(Hq=128, Hkv=128, max_pages=1 << 16, ws_bytes=1 << 50)         # 2^20 keys: 128 * (2^14 + 8) a sequence
+    assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **edge, "B": 1023}.values()) == CUDA
+    assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **edge, "B": 1024}.values()) == UNSUPPORTED
+
+
 def _cpu_pool(pages=3, Hkv=2, page=16, D=64, B=2):
     return (torch.zeros(pages, Hkv, page, D).to(torch.float8_e4m3fn), torch.zeros(pages, Hkv, page, D).to(torch.float8_e4m3fn),
             torch.zeros(pages, Hkv, page, dtype=torch.uint8), torch.zeros(pages, Hkv, page, dtype=torch.uint8),
