@@ -383,8 +383,17 @@ def fa_decode_splitkv_multi(q, k_cache, v_cache, kv_lens, causal: bool = True,
 # kernels take a few microseconds, so a call asks for all it checks in one expression; only
 # where that fails does _refuse find out what to say.
 _F8, _U8, _I32, _F32 = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream  # handle of a device's current stream
 _fp8_lib = None
+
+
+def _public_raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The handle of a device's current stream, and the current device: what torch's own generated code
+# asks for them (0.1 us, where the public calls take 1), or those calls where a build lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _load_fp8():
@@ -483,7 +492,7 @@ def _made(shape, dtype, device, other, returned=True):
 
 def _call_on(device, fn, *args):
     """Calls a C entry point with the device of this index current."""
-    if torch._C._cuda_getDevice() == device:
+    if _current_device() == device:
         st = fn(*args)
     else:
         with torch.cuda.device(device):

@@ -765,6 +765,22 @@ def test_another_stream_leaves_the_current_ones_memory_alone(fa):
         assert torch.equal(copies[0], o_ref) and torch.equal(copies[1], lse_ref)
 
 
+def test_streams_are_found_by_torchs_public_calls_too(fa, monkeypatch):
+    from exact_tiled_attention_20_gb300 import _lib
+
+    pool, q, o, lse = _decode_case(fa, 64, 4, 2, 1, 16, [300, 17], seed=8)
+    qd, kl, side = q.to(DEV), _int([300, 17]), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert _lib._raw_stream(0) == _lib._public_raw_stream(0) == side.cuda_stream
+    monkeypatch.setattr(_lib, "_raw_stream", _lib._public_raw_stream)
+    monkeypatch.setattr(_lib, "_current_device", torch.cuda.current_device)
+    torch.cuda.synchronize()
+    for stream in (None, side):
+        a, b = fa.fa_decode_splitkv_paged_fp8(qd, *pool.args, kl, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
 def test_offsets_past_32_bits(fa):
     """A pool of more than 2^32 bytes of codes: the last pages are written, read and decoded."""
     Hkv, page, D, B = 8, 64, 128, 2

@@ -118,3 +118,24 @@ def test_binding_rejects_cpu_tensors(lib):
         fa.fa_kv_read_paged_fp8(*pool, torch.zeros(3, dtype=torch.int32), total=4)
     with pytest.raises(TypeError):
         fa.fa_decode_splitkv_paged_fp8(x, *pool, lens)
+
+
+def test_import_needs_no_cuda_build_of_torch():
+    """The package imports, and answers what needs no tensors, where torch lacks the names of its CUDA build."""
+    import os
+    import subprocess
+    import sys
+
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import exact_tiled_attention_20_gb300 as fa\n"
+            "from exact_tiled_attention_20_gb300 import _lib\n"
+            "assert fa.fa_decode_workspace_bytes(1, 1, 64, 1) > 0 and _lib._load_fp8() is not None\n"
+            "try:\n"
+            "    fa.fa_kv_read_paged_fp8(*[torch.zeros(1)] * 5, torch.zeros(2), total=1)\n"
+            "except (TypeError, ValueError):\n"
+            "    print('refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["refused"], r.stderr[-2000:]
