@@ -575,6 +575,12 @@ def test_decode_is_deterministic_and_independent_of_the_split(fa, D):
         assert ((a[1] - lse).abs() <= 1e-4).all()
 
 
+@pytest.mark.parametrize("D", HEAD_DIMS)
+@pytest.mark.parametrize("ns", [1, 2, 5, 64])
+def test_decode_holds_its_bound_for_every_split(fa, D, ns):
+    _decode_case(fa, D, 8, 2, 1, 16, [1500, 200, 801], ns=ns, seed=5)
+
+
 # -------------------------------------------------------------- used as a program ----
 def test_prompt_then_steps(fa):
     """A chunked prefill and decode steps as a serving loop runs them: each chunk is appended,
