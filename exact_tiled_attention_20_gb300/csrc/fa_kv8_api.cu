@@ -119,6 +119,8 @@ fa_status fa_decode_splitkv_paged_fp8(const void* q, const void* k_pages, const 
     // The plan counts 64-key units, and a few more for each (sequence, kv head) pair, in 32 bits.
     if ((long long)B * Hkv > 0x7fffffffLL / (capacity / 64 + 8)) return FA_ERR_UNSUPPORTED;
     if ((long long)B * Sq * Hq > 0x7fffffffLL - 8) return FA_ERR_UNSUPPORTED;  // the merge counts past the last row
+    // The values of a sequence without keys are written by one CTA, which counts a little past them.
+    if ((long long)Sq * Hq * D > 0x7fffffffLL - 255) return FA_ERR_UNSUPPORTED;
     // The bytes of the partial results (of each row D values and a log-sum-exp), in 64 bits.
     if (num_splits > 1 &&
         (long long)B * Sq * Hq * num_splits > (0x7fffffffffffffffLL - 512) / ((D + 1) * (int)sizeof(float)))

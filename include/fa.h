@@ -304,8 +304,8 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  *   kv_lens   device int32 [B], 0 <= kv_lens[b] <= page_size * max_pages_per_seq; other
  *             values are the caller's error and are clamped on the device
  *   causal    as fa_decode_splitkv_multi: token s sees keys j <= kv_lens[b] - Sq + s
- * (Hq / Hkv) * Sq <= 16; B * Hkv * (page_size * max_pages_per_seq / 64 + 8) < 2^31 and
- * B * Sq * Hq <= 2^31 - 9.  A token that sees no key gets O = 0 and LSE = -inf.  Cached codes
+ * (Hq / Hkv) * Sq <= 16; B * Hkv * (page_size * max_pages_per_seq / 64 + 8) < 2^31,
+ * B * Sq * Hq <= 2^31 - 9 and Sq * Hq * D <= 2^31 - 256.  A token that sees no key gets O = 0 and LSE = -inf.  Cached codes
  * enter the products exactly; the probabilities, with V's scales in them, are rounded to fp16 for
  * P.V (11 bits for weights down to 2^-25 of the row's largest, fewer below; one under 2^-36 of it may
  * vanish); O is rounded once.  What lies in the pool behind a sequence's last key is not used, nor is a key

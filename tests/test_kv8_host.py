@@ -101,6 +101,12 @@ def test_decode_takes_the_tables_that_append_and_read_take(lib):
     assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **edge, "B": 1024}.values()) == UNSUPPORTED
 
 
+def test_decode_refuses_more_values_of_a_sequence_than_32_bits_count(lib):
+    """8388608 rows of 256 values: an empty sequence's would be counted in 32 bits."""
+    change = dict(B=1, Hq=1 << 23, Hkv=1 << 19, D=256, max_pages=1, splits=1)
+    assert lib.fa_decode_splitkv_paged_fp8(*{**DECODE, **change}.values()) == UNSUPPORTED
+
+
 def _cpu_pool(pages=3, Hkv=2, page=16, D=64, B=2):
     return (torch.zeros(pages, Hkv, page, D).to(torch.float8_e4m3fn), torch.zeros(pages, Hkv, page, D).to(torch.float8_e4m3fn),
             torch.zeros(pages, Hkv, page, dtype=torch.uint8), torch.zeros(pages, Hkv, page, dtype=torch.uint8),
