@@ -82,7 +82,12 @@ fa_status launch_kv8_decode_d128(const Kv8DecodeArgs& a, cudaStream_t s);
 fa_status launch_kv8_decode_d256(const Kv8DecodeArgs& a, cudaStream_t s);
 
 // Launches `kern` so that its start may overlap the end of the kernel before it on the
-// stream; the kernel itself waits (grid_dependency_wait) before it touches global memory.
+// stream; the kernel itself waits (grid_dependency_wait), in every thread, before it writes global
+// memory or uses what that kernel may write.  What may be read earlier: by the split kernel lengths
+// and table entries, for a guess that it checks after the wait and that decides nothing but which
+// lines of the pool go to L2 (indices are held inside the table and the pool whatever they are);
+// by the merge kernel the lengths, since every CTA of the split kernel before it lets it start
+// only after its own wait, when all that came before is done.
 template <typename... P, typename... A>
 inline fa_status launch_overlapped(void (*kern)(P...), unsigned grid, unsigned block, size_t smem,
                                    cudaStream_t s, A... args) {

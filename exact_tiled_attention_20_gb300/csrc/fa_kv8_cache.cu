@@ -265,7 +265,7 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
 template <int D, int U>
 struct ReadCfg {
     static constexpr int PerRow = D / 8;                       // threads of one row, 8 values each
-    static constexpr int Groups = kThreads / PerRow;           // 21 rows at D = 96, 4 threads idle
+    static constexpr int Groups = kThreads / PerRow;           // 10 rows at D = 96, 8 threads idle
     static constexpr int Run = Groups * U;
 };
 

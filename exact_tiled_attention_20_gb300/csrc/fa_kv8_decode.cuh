@@ -453,7 +453,10 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     // done, so this is a guess: nothing but L2 lines depends on it, and the plan is made again if a
     // length is another afterwards.  Behind a kernel that lets this one start early (this library's;
     // others' are done by then) it saves 0.4 us by the plan and 0.9 by the tiles: one sequence of
-    // 32768 17.9 -> 16.6 us, the lengths 1024..32768 47.9 -> 46.4.  More tiles: 16.6 with 2, 17.5 with 4;
+    // 32768 17.9 -> 16.6 us, the lengths 1024..32768 47.9 -> 46.4, each behind a decode.  Behind an
+    // append of one token a sequence, the pair takes 0.9 us more than append and decode do among
+    // their own kind; behind a kernel that does not let this one start early, 1.8 (16.5 + 1.2 -> 19.5
+    // us and 46.3 + 1.2 -> 49.9 for an elementwise kernel).  More tiles: 16.6 with 2, 17.5 with 4;
     // for warps alone 12.8 us without and 13.5 with (2048 pairs of 64 keys).
     make_plan();
     {
@@ -552,9 +555,9 @@ __global__ void __launch_bounds__(kKv8Threads, Kv8Cfg<D, HB>::CTAS) kv8_split_ke
     }
 
     // Queries as f16 fragments, column 2 t + e of block nt being row (2 nt + e) * 4 + t.  A row is
-    // multiplied by a power of two that brings its largest magnitude to [2^13, 2^14).  fp16's
-    // subnormals are then 2^-38 of it, so bf16 and fp16 queries enter exactly but for values that
-    // far below their row's largest.
+    // multiplied by a power of two that brings its largest magnitude to [2^13, 2^14).  fp16 has all
+    // its 11 bits from 2^-14 on and steps of 2^-24 below, so bf16 and fp16 queries enter exactly
+    // but for values under 2^-27 of their row's largest, which are off by 2^-38 of it at most.
     struct Factor {
         float up, down;  // the power of two, and softmax scale * log2 e over it
     };

@@ -305,12 +305,16 @@ FA_API fa_status fa_kv_read_paged_fp8(const void *k_pages, const void *v_pages,
  *             values are the caller's error and are clamped on the device
  *   causal    as fa_decode_splitkv_multi: token s sees keys j <= kv_lens[b] - Sq + s
  * (Hq / Hkv) * Sq <= 16; B * Hkv * (page_size * max_pages_per_seq / 64 + 8) < 2^31,
- * B * Sq * Hq <= 2^31 - 9 and Sq * Hq * D <= 2^31 - 256.  A token that sees no key gets O = 0 and LSE = -inf.  Cached codes
- * enter the products exactly; the probabilities, with V's scales in them, are rounded to fp16 for
- * P.V (11 bits for weights down to 2^-25 of the row's largest, fewer below; one under 2^-36 of it may
- * vanish); O is rounded once.  What lies in the pool behind a sequence's last key is not used, nor is a key
- * that `causal` hides from a token used for it, NaN codes there included.  Keys on a page outside the
- * pool count as zero rows.
+ * B * Sq * Hq <= 2^31 - 9 and Sq * Hq * D <= 2^31 - 256.  A token that sees no key gets O = 0
+ * and LSE = -inf.  Cached codes enter the products exactly, queries but for values under 2^-27 of
+ * their row's largest, which are off by 2^-38 of it at most.  The factor that makes a sum of
+ * products a score, scale * 2^(ks - 127) times a power of two of the query row, is a 32-bit float:
+ * where a row's largest |q| times a key's scale passes 2^140 or so it overflows, and a score that
+ * would be 0 is NaN.  The probabilities, with V's scales in them, are rounded to fp16 for P.V (11
+ * bits for weights down to 2^-25 of the row's largest, fewer below; one under 2^-36 of it may
+ * vanish); O is rounded once.  What lies in the pool behind a sequence's last key is not used, nor
+ * is a key that `causal` hides from a token used for it, NaN codes there included.  Keys on a page
+ * outside the pool count as zero rows.
  *   num_splits  sizes the workspace, which holds B * Hkv * num_splits partial results (<= 0:
  *             fa_decode_default_splits(B, Hkv, page_size * max_pages_per_seq, 0) of a pair).  The
  *             keys of all (sequence, kv head) pairs are laid end to end and cut into equal ranges,
