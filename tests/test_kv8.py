@@ -563,6 +563,23 @@ def test_decode_guard_bands_and_no_lse(fa):
     assert st == 0 and torch.equal(o, o_ref)
 
 
+def test_decode_uncut_needs_no_workspace(fa):
+    """num_splits = 1 at the C entry without a workspace: the binding's bits, in every form that a CTA or
+    a warp alone takes pairs in."""
+    from exact_tiled_attention_20_gb300 import _lib
+
+    for D, Hkv, lens in ((128, 2, [700, 0, 129]), (64, 12, [20, 0, 300, 64] * 40), (256, 3, [90])):
+        pool, q, o, lse = _decode_case(fa, D, 4 * Hkv, Hkv, 1, 16, lens, ns=1)
+        got = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+        qd, kl = q.to(DEV), _int(lens)
+        num_pages, _, page, _ = pool.k.shape
+        st = _lib._load_fp8().fa_decode_splitkv_paged_fp8(
+            qd.data_ptr(), pool.k.data_ptr(), pool.v.data_ptr(), pool.ks.data_ptr(), pool.vs.data_ptr(),
+            pool.table.data_ptr(), kl.data_ptr(), got[0].data_ptr(), got[1].data_ptr(), len(lens), 1, 4 * Hkv, Hkv, D,
+            num_pages, page, pool.table.shape[1], 1 / math.sqrt(D), 1, 1, None, 0, 0, torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(got[0], o) and torch.equal(got[1], lse)
+
+
 @pytest.mark.parametrize("D", HEAD_DIMS)
 def test_decode_is_deterministic_and_independent_of_the_split(fa, D):
     pool, q, o, lse = _decode_case(fa, D, 8, 2, 1, 16, [1500, 200, 801], ns=1, seed=5)
@@ -614,6 +631,27 @@ def test_prompt_then_steps(fa):
             assert (np.abs(od.double().cpu().numpy()[:, 0] - o.double().cpu().numpy()) <= bound[:, 0]).all()
             assert ((ld[:, :, 0].T - lse).abs() <= 1e-3).all()
     _same(pool.host(), ref)
+
+
+def test_step_of_a_padded_batch(fa):
+    """Entries of a batch that hold no sequence (length 0, a table of -1): their rows are dropped by the
+    append, their outputs are zeros, and the other sequences are as in a batch without them."""
+    rng = np.random.default_rng(12)
+    Hq, Hkv, D, page, mp = 8, 2, 96, 16, 6
+    pool = Pool(4 * mp, Hkv, page, D, 4, mp, seed=17)
+    pool.table_np[1], pool.table_np[3] = -1, -1
+    lens = [60, 0, 33, 0]
+    pool.fill(rng, lens)
+    lens = [61, 0, 34, 0]
+    k, v, q = (torch.from_numpy(rng.standard_normal((4, 1, h, D))).to(torch.bfloat16) for h in (Hkv, Hkv, Hq))
+    real = [0, 2]
+    want = [a.copy() for a in pool.np]
+    kv8.append(want, k[real, 0].double().numpy(), v[real, 0].double().numpy(), pool.table_np[real], [61, 34], _cu([1, 1]))
+    fa.fa_kv_append_paged_fp8(k.to(DEV), v.to(DEV), *pool.args, _int(lens))
+    _same(pool.host(), want)
+    o, lse = fa.fa_decode_splitkv_paged_fp8(q.to(DEV), *pool.args, _int(lens))
+    assert (o[[1, 3]] == 0).all() and (lse[[1, 3]] == -math.inf).all()
+    _check(o, lse, kv8.decode(q.double().numpy(), want, pool.table_np, lens, 1 / math.sqrt(D)), 61, D, "bf16")
 
 
 def test_captured_step_replays_with_new_lengths(fa):
