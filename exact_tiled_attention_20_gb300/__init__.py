@@ -13,21 +13,29 @@ generators (``inputs``).  The binding's names mirror the C entry points:
 * ``fa_decode_splitkv_noalloc`` -- decode with library-owned scratch (no workspace);
 * ``fa_kv_append_paged_fp8``, ``fa_decode_splitkv_paged_fp8``, ``fa_kv_read_paged_fp8`` -- an
   8-bit paged KV cache: rows quantised as they are written, attended over, read back;
+* ``fa_kv_append_paged_rope`` -- new rows written into the 16-bit paged cache, keys and queries
+  rotated by their positions on the way;
+* ``fa_decode_splitkv_paged_tree``, ``fa_decode_splitkv_paged_window`` -- several query tokens
+  over that cache, under the mask of a draft tree or of a sliding window with sinks;
 * ``fa_decode_workspace_bytes``, ``fa_decode_default_splits``, ``fa_status_string``,
   ``fa_last_device_status``, ``fa_selftest_bounded_wait`` (the bounded-wait self-test).
 
 Importing the package does not load the library; the first call does, and raises if
 ``libfa.so`` has not been built.
 """
-from ._lib import (FA_BF16, FA_FP16, FaError, fa_decode_default_splits, fa_decode_splitkv,
+from ._lib import (FA_BF16, FA_FP16, FaError, fa_decode_default_splits, fa_decode_paged_workspace_bytes,
+                   fa_decode_splitkv,
                    fa_decode_splitkv_multi, fa_decode_splitkv_noalloc, fa_decode_splitkv_paged,
-                   fa_decode_splitkv_paged_fp8, fa_decode_workspace_bytes, fa_fwd, fa_fwd_varlen,
-                   fa_kv_append_paged_fp8, fa_kv_read_paged_fp8, fa_last_device_status, fa_selftest_bounded_wait,
+                   fa_decode_splitkv_paged_fp8, fa_decode_splitkv_paged_tree, fa_decode_splitkv_paged_window,
+                   fa_decode_workspace_bytes, fa_fwd, fa_fwd_varlen,
+                   fa_kv_append_paged_fp8, fa_kv_append_paged_rope, fa_kv_read_paged_fp8, fa_last_device_status, fa_selftest_bounded_wait,
                    fa_status_string, library_path, load)
 
 __all__ = [
     "FA_BF16", "FA_FP16", "FaError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_splitkv_paged",
     "fa_decode_splitkv_paged_fp8", "fa_kv_append_paged_fp8", "fa_kv_read_paged_fp8",
+    "fa_kv_append_paged_rope", "fa_decode_splitkv_paged_tree", "fa_decode_splitkv_paged_window",
+    "fa_decode_paged_workspace_bytes",
     "fa_decode_splitkv_noalloc", "fa_decode_splitkv_multi", "fa_decode_workspace_bytes", "fa_decode_default_splits",
     "fa_status_string", "fa_last_device_status", "fa_selftest_bounded_wait", "library_path", "load",
 ]

@@ -649,3 +649,184 @@ def fa_decode_splitkv_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_t
              1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, ns,
              workspace.data_ptr(), workspace.numel(), _DTYPE[dtype], handle)
     return out, lse
+
+
+# ---- 16-bit paged cache: the rotated append, and the decodes under a tree's or a window's mask.
+_paged16_lib = None
+
+
+def _load_paged16():
+    global _paged16_lib
+    if _paged16_lib is None:
+        lib = load()
+        P, I, F, SZ, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+        lib.fa_kv_append_paged_rope.argtypes = [P, P, P, L, L, L, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I,
+                                                I, I, I, I, P]
+        lib.fa_kv_append_paged_rope.restype = I
+        lib.fa_decode_paged_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        lib.fa_decode_paged_workspace_bytes.restype = SZ
+        lib.fa_decode_splitkv_paged_tree.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, SZ, I, P]
+        lib.fa_decode_splitkv_paged_tree.restype = I
+        lib.fa_decode_splitkv_paged_window.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, I, P, SZ, I,
+                                                       P]
+        lib.fa_decode_splitkv_paged_window.restype = I
+        _paged16_lib = lib
+    return _paged16_lib
+
+
+def _pool16(k_pages, v_pages, block_table, kv_lens):
+    """Checks the 16-bit pool's tensors; returns (dtype, device index, num_pages, page_size, Hkv, D, B, max_pages)."""
+    try:
+        device, dtype, shape = k_pages.get_device(), k_pages.dtype, k_pages.shape
+        num_pages, page, Hkv, D = shape
+        B, max_pages = block_table.shape
+        if (device >= 0 and dtype in _DTYPE and v_pages.dtype is dtype and block_table.dtype is _I32
+                and kv_lens.dtype is _I32 and v_pages.get_device() == device and block_table.get_device() == device
+                and kv_lens.get_device() == device and v_pages.shape == shape and kv_lens.shape == (B,)
+                and k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous()
+                and kv_lens.is_contiguous()):
+            return dtype, device, num_pages, page, Hkv, D, B, max_pages
+    except (AttributeError, ValueError):  # no tensors, or of other dimensions
+        for t in (k_pages, v_pages, block_table, kv_lens):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("the pool, block_table and kv_lens must be CUDA tensors") from None
+        raise ValueError("k_pages must be [num_pages, page_size, Hkv, D] and block_table "
+                         "[B, max_pages_per_seq]") from None
+    if dtype not in _DTYPE:
+        raise TypeError("k_pages and v_pages must be bf16 or fp16")
+    _refuse(("k_pages", k_pages, dtype, device, shape), ("v_pages", v_pages, dtype, device, shape),
+            ("block_table", block_table, _I32, device, None), ("kv_lens", kv_lens, _I32, device, (B,)))
+
+
+def fa_kv_append_paged_rope(k_new, v_new, k_pages, v_pages, block_table, kv_lens, cos=None, sin=None, q=None,
+                            q_out=None, positions=None, cu_seqlens_new=None, interleaved: bool = False, stream=None):
+    """Writes new K/V rows into the 16-bit paged cache, keys and queries rotated by their
+    positions on the way, through fa_kv_append_paged_rope.
+
+    k_new/v_new (and q, where given): [B, n, H, D] (n new tokens for each sequence), or packed
+    [total, H, D] with cu_seqlens_new int32 [B+1]; the tokens may be strided (slices of a fused
+    projection), the heads of a token dense.  k_pages/v_pages [num_pages, page_size, Hkv, D],
+    block_table int32 [B, max_pages_per_seq]; kv_lens int32 [B] counts the new tokens: they become
+    the last keys of their sequences.  cos/sin fp32 [max_pos, rot_dim / 2] (None: no rotation);
+    positions int32, one for each new token (None: a token's key).  Writes the pool in place;
+    returns the rotated queries (q_out, made here where it is None; it may be a contiguous q
+    itself), or None without q."""
+    lib = _paged16_lib or _load_paged16()
+    dtype, device, num_pages, page, Hkv, D, B, max_pages = _pool16(k_pages, v_pages, block_table, kv_lens)
+    total, k_stride = _new_rows("k_new", k_new, dtype, device, Hkv, D)
+    v_stride = _new_rows("v_new", v_new, dtype, device, Hkv, D)[1]
+    shape = k_new.shape
+    if v_new.shape != shape:
+        raise ValueError("k_new and v_new must have one shape")
+    cu = None
+    if cu_seqlens_new is not None:
+        if not _is(cu_seqlens_new, _I32, device, (B + 1,)):
+            _refuse(("cu_seqlens_new", cu_seqlens_new, _I32, device, (B + 1,)))
+        if len(shape) != 3:
+            raise ValueError("with cu_seqlens_new, the new rows are packed [total, H, D]")
+        cu = cu_seqlens_new.data_ptr()
+    elif len(shape) != 4 or shape[0] != B:
+        raise ValueError("without cu_seqlens_new, the new rows are [B, n, H, D]")
+    rot = max_pos = 0
+    if cos is not None or sin is not None:
+        if not isinstance(cos, torch.Tensor) or not isinstance(sin, torch.Tensor) or cos.dim() != 2:
+            raise TypeError("cos and sin must both be CUDA tensors [max_pos, rot_dim / 2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if not (_is(cos, _F32, device, None) and _is(sin, _F32, device, cos.shape)):
+            _refuse(("cos", cos, _F32, device, None), ("sin", sin, _F32, device, cos.shape))
+        if rot == 0:
+            raise ValueError("cos and sin must have rot_dim / 2 >= 8 columns")
+    if positions is not None and not _is(positions, _I32, device, shape[:-2]):
+        if not _is(positions, _I32, device, (total,)):
+            _refuse(("positions", positions, _I32, device, (total,)))
+    handle, other = _stream_on(device, stream)
+    Hq = q_stride = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != len(shape):
+            raise ValueError("q must have as many dimensions as k_new")
+        Hq = q.shape[-2]
+        if q.shape[:-2] != shape[:-2]:
+            raise ValueError("q must have the tokens of k_new")
+        q_stride = _new_rows("q", q, dtype, device, Hq, D)[1]
+        if q_out is None:
+            q_out = _made(q.shape, dtype, q.device, other)
+        elif not _is(q_out, dtype, device, q.shape):
+            _refuse(("q_out", q_out, dtype, device, q.shape))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _call_on(device, lib.fa_kv_append_paged_rope, q.data_ptr() if Hq else None, k_new.data_ptr(), v_new.data_ptr(),
+             q_stride, k_stride, v_stride, q_out.data_ptr() if Hq else None, cu, block_table.data_ptr(),
+             kv_lens.data_ptr(), None if positions is None else positions.data_ptr(), cos.data_ptr() if rot else None,
+             sin.data_ptr() if rot else None, k_pages.data_ptr(), v_pages.data_ptr(), B, total, Hq, Hkv, D, rot,
+             1 if interleaved else 0, max_pos, num_pages, page, max_pages, _DTYPE[dtype], handle)
+    return q_out
+
+
+def fa_decode_paged_workspace_bytes(B: int, Sq: int, Hq: int, Hkv: int, D: int, num_sms: int = 0) -> int:
+    return int((_paged16_lib or _load_paged16()).fa_decode_paged_workspace_bytes(B, Sq, Hq, Hkv, D, num_sms))
+
+
+def _decode_paged16(entry, q, k_pages, v_pages, block_table, kv_lens, tree_mask, window, scale, workspace, out, lse,
+                    stream):
+    lib = _paged16_lib or _load_paged16()
+    dtype, device, num_pages, page, Hkv, D, B, max_pages = _pool16(k_pages, v_pages, block_table, kv_lens)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+        raise ValueError(f"q must be a CUDA tensor [{B}, Sq, Hq, {D}]")
+    shape = q.shape
+    Sq, Hq = shape[1], shape[2]
+    if not _is(q, dtype, device, shape):
+        _refuse(("q", q, dtype, device, shape))
+    mask = ()
+    if tree_mask is not None:
+        words = (B, Sq, (Sq + 31) // 32)
+        if not _is(tree_mask, _I32, device, words):
+            _refuse(("tree_mask", tree_mask, _I32, device, words))
+        mask = (tree_mask.data_ptr(),)
+    handle, other = _stream_on(device, stream)
+    if workspace is None:
+        with torch.cuda.device(device):
+            need = lib.fa_decode_paged_workspace_bytes(B, Sq, Hq, Hkv, D, 0)
+        workspace = _made(max(16, need), _U8, q.device, other, returned=False)
+    elif not _is(workspace, _U8, device, None):
+        _refuse(("workspace", workspace, _U8, device, None))
+    if out is None:
+        out = _made(shape, dtype, q.device, other)
+    elif not _is(out, dtype, device, shape):
+        _refuse(("out", out, dtype, device, shape))
+    if lse is None:
+        lse = _made((B, Hq, Sq), _F32, q.device, other)
+    elif not _is(lse, _F32, device, (B, Hq, Sq)):
+        _refuse(("lse", lse, _F32, device, (B, Hq, Sq)))
+    _call_on(device, getattr(lib, entry), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+             block_table.data_ptr(), kv_lens.data_ptr(), *mask, out.data_ptr(), lse.data_ptr(), B, Sq, Hq, Hkv, D,
+             num_pages, page, max_pages, 1.0 / math.sqrt(D) if scale is None else float(scale), *window,
+             workspace.data_ptr(), workspace.numel(), _DTYPE[dtype], handle)
+    return out, lse
+
+
+def fa_decode_splitkv_paged_tree(q, k_pages, v_pages, block_table, kv_lens, tree_mask, scale: float | None = None,
+                                 workspace=None, out=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens over the 16-bit paged cache through
+    fa_decode_splitkv_paged_tree.
+
+    q [B, Sq, Hq, D]: the drafts are the last Sq of each sequence's kv_lens keys, appended
+    before.  tree_mask int32 [B, Sq, ceil(Sq / 32)]: draft t is seen by token i where bit t % 32 of
+    word t // 32 of mask [b, i] is set; every key before the drafts is seen by all.  workspace: a
+    CUDA uint8 tensor of at least fa_decode_paged_workspace_bytes(B, Sq, Hq, Hkv, D) bytes, or None
+    to allocate one.  Returns (o like q, lse fp32 [B, Hq, Sq])."""
+    if tree_mask is None:
+        raise TypeError("tree_mask must be a CUDA tensor")
+    return _decode_paged16("fa_decode_splitkv_paged_tree", q, k_pages, v_pages, block_table, kv_lens, tree_mask, (),
+                           scale, workspace, out, lse, stream)
+
+
+def fa_decode_splitkv_paged_window(q, k_pages, v_pages, block_table, kv_lens, window_left: int = -1, sinks: int = 0,
+                                   scale: float | None = None, workspace=None, out=None, lse=None, stream=None):
+    """Decode with a sliding window and sinks over the 16-bit paged cache through
+    fa_decode_splitkv_paged_window.
+
+    q [B, Sq, Hq, D], the last Sq of each sequence's kv_lens keys: token i, at key p = kv_lens[b] -
+    Sq + i, sees the keys j <= p with j >= p - window_left (-1: all) or j < sinks.  workspace as for
+    fa_decode_splitkv_paged_tree.  Returns (o like q, lse fp32 [B, Hq, Sq])."""
+    return _decode_paged16("fa_decode_splitkv_paged_window", q, k_pages, v_pages, block_table, kv_lens, None,
+                           (min(int(window_left), 2**31 - 1), min(int(sinks), 2**31 - 1)), scale, workspace, out, lse, stream)

@@ -148,6 +148,14 @@ bool encode_tmap_4d_box(CUtensorMap* map, const void* base, bool bf16, uint64_t 
     return true;
 }
 
+bool current_device(int* num_sms, int** dev_status) {
+    DeviceInfo di;
+    if (!device_info(&di)) return false;
+    *num_sms = di.num_sms;
+    *dev_status = di.status;
+    return true;
+}
+
 bool ensure_smem_attr(const void* func, int bytes, int* done_flags) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;

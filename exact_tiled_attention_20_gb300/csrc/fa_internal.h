@@ -28,6 +28,7 @@ struct FwdArgs {
     bool bf16;
     int num_sms;
     int* dev_status;
+    int sinks = 0;  // first keys that stay visible outside the window
 };
 
 // Arguments of one split-KV decode call after validation.
@@ -78,6 +79,10 @@ fa_status launch_decode_d256(const DecodeArgs& a, cudaStream_t s);
 fa_status decode_check_args(const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* kv_lens, const void* o, const float* lse, int B, int Sq,
                             int Hq, int Hkv, int D, int Smax, float scale, fa_dtype dtype);
+
+// SMs of the current device and the device address of its status word; false where the device
+// cannot be queried.
+bool current_device(int* num_sms, int** dev_status);
 
 // Sets the dynamic shared-memory limit of `func` once per device.
 bool ensure_smem_attr(const void* func, int bytes, int* done_flags);

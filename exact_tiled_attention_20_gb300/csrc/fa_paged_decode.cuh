@@ -1,0 +1,972 @@
+// fa_paged_decode.cuh -- split-KV attention of a few query tokens over the 16-bit paged cache,
+// under the mask of a draft tree or of a causal window with sinks (tcgen05 + TMA).
+//
+// For sequence b of n keys, its query tokens being its last Sq keys, token i and query head h:
+//     s_j = scale * (q . k_j),  o = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+// over the keys j that token i sees:
+//     tree:    j < n - Sq, and n - Sq + t where bit t of the token's mask is set;
+//     window:  j <= p = n - Sq + i, and j >= p - window_left or j < sinks.
+//
+// A sub-tile holds the query rows of T tokens of one kv head (row = token * group + head, at most
+// 128), a row block NQ sub-tiles.  One CTA streams key tiles through shared memory for a row
+// block: a TMA warp, an MMA warp (S = Q K^T with A and B from shared memory, O += P V with P from
+// TMEM), and a softmax warpgroup per sub-tile, thread = row = TMEM lane, as in the forward.
+//
+// Why tcgen05 although few rows may be in use: an M = 128 product costs the same for 1 row as for
+// 128, and that is less than the tile's way from HBM (D = 128, 128 keys: 1100 cycles of products
+// against some 2800 for 64 KB at an SM's share of the bandwidth), so it is the bytes that bound
+// the kernel for anything up to about 256 rows.
+//
+// Plan: the visible key tiles of a sequence are counted as units, those of the sinks first and
+// then those from the first token's window on; the units of all entries (sequence, group of kv
+// heads), each led by kPagedLead units for what starting and finishing one costs, lie end to end
+// and are cut into equal ranges.  A range is worked on by G CTAs, one for each head of the group
+// (and for each row block, where there are few): they read the same keys at about the same time,
+// whose rows lie side by side in a page.  A cut entry leaves a partial output and log-sum-exp in
+// each range, at most two per CTA, which the merge kernel joins.
+//
+// Infinities and NaNs: the scores of hidden keys are replaced, not added to.  In tiles that hide a
+// key from some row, V's values that are not finite are taken out before the product (0 * inf is
+// NaN) and added to the rows that see them in the epilogue, from memory.
+#pragma once
+
+#include <algorithm>
+
+#include "fa_kv8_decode.cuh"  // shared-memory loads, 16-bit conversions, prefer_shared
+#include "fa_paged.cuh"
+
+namespace fa {
+
+// 4-D map over [dim3][dim2][dim1][dim0] in 16 bits, box (64, box1, box2, 1), 128-byte swizzle;
+// encoded anew for each call.
+bool encode_paged_tmap(CUtensorMap* map, const void* base, bool bf16, uint64_t dim0, uint64_t dim1, uint64_t dim2,
+                       uint64_t dim3, uint32_t box1, uint32_t box2);
+
+struct PagedDecParams {
+    int B, Sq, Hq, Hkv, group;
+    int T;               // query tokens of a sub-tile
+    int row_blocks;      // of a (sequence, kv head)
+    int g, rg;           // heads and row blocks of an entry: G = g * rg CTAs work on a range
+    int entries;         // of a sequence
+    int ranges, whole;   // whole: entries are not cut, a range has those that begin in it
+    int capacity, page_size, num_pages, max_pages, box_rows;
+    unsigned page_recip;  // floor(2^32 / page_size) + 1
+    int window_left, sinks;
+    int words;            // of a token's tree mask
+    const int32_t* table;
+    const int32_t* kv_lens;
+    const int32_t* tree;
+    float scale_log2;
+    const uint16_t* v_pages;
+    void* o;
+    float* lse;
+    float* o_part;    // [G, 2 * ranges, block rows, D]
+    float* lse_part;  // [G, 2 * ranges, block rows]
+    int* status;
+};
+
+constexpr int kPagedLead = 1;      // units charged to each entry beside its keys
+constexpr int kPagedMinWidth = 6;  // least units of a range: a cut costs the merge kernel
+constexpr int kPagedMaxB = 1024;
+constexpr float kPagedLn2 = 0.69314718055994531f;
+
+template <int D_, int NQ_>
+struct PagedCfg {
+    static constexpr int D = D_, NQ = NQ_;
+    static constexpr int BM = 128;
+    static constexpr int BN = D == 256 ? 64 : 128;  // keys of a tile
+    static constexpr int DA = (D + 63) / 64;        // 128-byte column atoms per row
+    static constexpr int kQBytes = BM * DA * 128;
+    static constexpr int kTileBytes = BN * DA * 128;
+    // K and V tiles take turns in one ring of NB buffers.
+    static constexpr int NB = D == 64 ? 10 : (D == 256 || NQ == 2) ? 4 : 5;
+    static constexpr int kSlots = 2;  // S buffers in TMEM: two of one sub-tile, or one of each
+    static constexpr int kOCol0 = kSlots * BN;
+    static constexpr int kTmemCols = 512;
+    static_assert(kOCol0 + NQ * D <= kTmemCols, "TMEM budget");
+    static constexpr int kThreads = 128 * NQ + 64;
+    static constexpr int kProducerWarp = 4 * NQ;
+    static constexpr int kMmaWarp = 4 * NQ + 1;
+    static constexpr int kBarQFull = 0;
+    static constexpr int kBarQEmpty = kBarQFull + NQ;
+    static constexpr int kBarFull = kBarQEmpty + NQ;
+    static constexpr int kBarEmpty = kBarFull + NB;
+    static constexpr int kBarSFull = kBarEmpty + NB;
+    static constexpr int kBarPFull = kBarSFull + kSlots;
+    static constexpr int kBarODone = kBarPFull + NQ;
+    static constexpr int kBarODrained = kBarODone + NQ;
+    static constexpr int kBarFinal = kBarODrained + NQ;
+    static constexpr int kNumBars = kBarFinal + 1;
+    static constexpr int kFixedBytes = 1024 + NQ * kQBytes + NB * kTileBytes + 8 * kNumBars + 32;
+    static constexpr int plan_bytes(int B) { return (2 * B + 1) * 4; }
+    static_assert(kFixedBytes + (2 * kPagedMaxB + 1) * 4 + 256 <= 232448, "shared memory of a CTA");
+};
+
+__device__ __forceinline__ int paged_len(const PagedDecParams& p, int b) {
+    return min(max(__ldcg(p.kv_lens + b), 0), p.capacity);
+}
+
+// The visible tiles of a sequence: tiles 0 .. sink_tiles - 1 and first .. last.
+struct PagedTiles {
+    int sink_tiles, first, count;
+    __device__ __forceinline__ int tile(int u) const { return u < sink_tiles ? u : first + u - sink_tiles; }
+};
+
+template <int BN>
+__device__ __forceinline__ PagedTiles paged_tiles(const PagedDecParams& p, int len) {
+    PagedTiles t;
+    t.first = p.window_left >= 0 ? max(len - p.Sq - p.window_left, 0) / BN : 0;
+    t.sink_tiles = min((min(p.sinks, len) + BN - 1) / BN, t.first);
+    t.count = len > 0 ? t.sink_tiles + (len + BN - 1) / BN - t.first : 0;
+    return t;
+}
+
+template <int BN>
+__device__ __forceinline__ int paged_units(const PagedDecParams& p, int len) {
+    const int n = paged_tiles<BN>(p, len).count;
+    return n > 0 ? n + kPagedLead : 0;
+}
+
+// Units of a range, from the units of one entry of each sequence summed.
+__device__ __forceinline__ int paged_width(const PagedDecParams& p, int sum_units) {
+    const unsigned total = (unsigned)sum_units * (unsigned)p.entries;
+    return max((int)((total + (unsigned)p.ranges - 1u) / (unsigned)p.ranges), kPagedMinWidth);
+}
+
+// The pieces of an entry of `units` units from unit `start` on: the first range that holds keys of
+// it, and how many ranges do.
+__device__ __forceinline__ int paged_first_piece(int start, int w) { return (start + kPagedLead) / w; }
+__device__ __forceinline__ int paged_pieces(int start, int units, int w) {
+    return units > 0 ? (start + units - 1) / w - paged_first_piece(start, w) + 1 : 0;
+}
+// The slot of an entry's piece in range r: a range has at most one piece of an entry that began
+// before it, and one that goes on behind it.
+__device__ __forceinline__ int paged_slot(const PagedDecParams& p, int r, bool first) { return first ? p.ranges + r : r; }
+
+struct PagedSeg {
+    int b, hk, rb, len;
+    int u0, u1;  // its visible tiles u0 .. u1 - 1
+    PagedTiles tiles;
+    int slot;
+    bool cut;
+};
+
+// Walks the segments of one range.
+struct PagedWalk {
+    const int* len;     // [B]
+    const int* prefix;  // [B + 1], of the units of one entry
+    int x, x_end, b, e, start, units, rng, W;
+
+    template <int BN>
+    __device__ __forceinline__ void init(const PagedDecParams& p, const int* len_, const int* prefix_, int rng_) {
+        len = len_;
+        prefix = prefix_;
+        rng = rng_;
+        W = paged_width(p, prefix[p.B]);
+        const int total = prefix[p.B] * p.entries;
+        x = (int)min((long long)rng * W, (long long)total);
+        x_end = (int)min((long long)x + W, (long long)total);
+        if (x >= x_end) return;
+        int lo = 0, hi = p.B;  // largest b with entries * prefix[b] <= x: it has keys
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.entries * prefix[mid] <= x) lo = mid; else hi = mid;
+        }
+        b = lo;
+        units = prefix[lo + 1] - prefix[lo];
+        e = (x - p.entries * prefix[lo]) / units;
+        start = p.entries * prefix[lo] + e * units;
+    }
+
+    template <int BN>
+    __device__ __forceinline__ bool next(const PagedDecParams& p, int member, PagedSeg& s) {
+        while (x < x_end) {
+            if (x >= start + units) {
+                start += units;
+                if (++e == p.entries) {
+                    e = 0;
+                    do {
+                        ++b;
+                        units = prefix[b + 1] - prefix[b];
+                    } while (units == 0);
+                }
+            }
+            if (p.whole && x > start) {  // the range before has it
+                x = start + units;
+                continue;
+            }
+            const int end = p.whole ? start + units : min(x_end, start + units);
+            const int blocks = p.row_blocks / p.rg;  // entries of one group of heads
+            s.b = b;
+            s.hk = e / blocks * p.g + member % p.g;
+            s.rb = e % blocks * p.rg + member / p.g;
+            s.len = len[b];
+            s.tiles = paged_tiles<BN>(p, s.len);
+            s.u0 = max(x - start - kPagedLead, 0);
+            s.u1 = end - start - kPagedLead;
+            s.slot = paged_slot(p, rng, rng == paged_first_piece(start, W));
+            s.cut = !p.whole && paged_pieces(start, units, W) > 1;
+            x = end;
+            if (s.u1 > s.u0) return true;  // else the range ends within the lead
+        }
+        return false;
+    }
+};
+
+// Bits i of a word with a <= i <= b.
+__device__ __forceinline__ uint32_t paged_bits(int a, int b) {
+    a = max(a, 0);
+    b = min(b, 31);
+    return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
+}
+
+// Bit i: whether token `tok` of a sequence of `len` keys sees key k + i.
+__device__ __forceinline__ uint32_t paged_sees(const PagedDecParams& p, int b, int tok, int len, int k) {
+    if (p.tree) {
+        const int ctx = len - p.Sq, t = k - ctx;  // bit i is draft t + i
+        uint32_t w = paged_bits(0, ctx - 1 - k);
+        if (t > -32 && t < p.Sq) {
+            const int32_t* m = p.tree + ((size_t)b * p.Sq + tok) * p.words;
+            uint32_t d;
+            if (t < 0) {
+                d = (uint32_t)__ldg(m) << -t;
+            } else {
+                const int i = t >> 5;
+                d = __funnelshift_r((uint32_t)__ldg(m + i), i + 1 < p.words ? (uint32_t)__ldg(m + i + 1) : 0u, t & 31);
+            }
+            w |= d & paged_bits(-t, len - 1 - k);
+        }
+        return w;
+    }
+    const int last = len - p.Sq + tok;
+    const uint32_t w = paged_bits(p.window_left >= 0 ? last - k - p.window_left : 0, last - k);
+    return w | paged_bits(0, min(p.sinks - 1, last) - k);
+}
+
+// Whether the tile of keys n0 .. n0 + BN - 1 hides a key from some token.
+template <int BN>
+__device__ __forceinline__ bool paged_masked(const PagedDecParams& p, int len, int n0) {
+    const int ctx = len - p.Sq;
+    if (p.tree) return n0 + BN > ctx;
+    return n0 + BN - 1 > ctx || (p.window_left >= 0 && n0 < len - 1 - p.window_left && n0 + BN > p.sinks);
+}
+
+// Whether one of a word's 16-bit values is an infinity or NaN.
+template <bool kBF16>
+__device__ __forceinline__ bool paged_nonfinite(uint32_t w) {
+    constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+    return (((w & 0x7fff7fffu) + (0x8000u - kInf) * 0x10001u) & 0x80008000u) != 0;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ float paged_from16(uint32_t x) {
+    if constexpr (kBF16) {
+        return __uint_as_float(x << 16);
+    } else {
+        float f;
+        asm("{\n.reg .b16 a;\ncvt.u16.u32 a, %1;\ncvt.f32.f16 %0, a;\n}" : "=f"(f) : "r"(x));
+        return f;
+    }
+}
+
+// Page and row within it of key `key` of sequence b; page -1: none.
+__device__ __forceinline__ int2 paged_place(const PagedDecParams& p, int b, int key) {
+    unsigned pi = __umulhi((unsigned)key, p.page_recip);  // the quotient, or one more
+    int row = (int)((unsigned)key - pi * (unsigned)p.page_size);
+    if (row < 0) {
+        --pi;
+        row += p.page_size;
+    }
+    const int page = __ldg(p.table + (size_t)b * p.max_pages + pi);
+    return make_int2(page >= 0 && page < p.num_pages ? page : -1, row);
+}
+
+// Fills len[B] and prefix[B + 1] (all threads; ends with a barrier).
+template <int BN, int kThreads>
+__device__ __forceinline__ void paged_make_plan(const PagedDecParams& p, int* len, int* prefix, int* warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = threadIdx.x * per + i;
+        if (b < p.B) {
+            const int n = paged_len(p, b);
+            len[b] = n;
+            sum += prefix[b] = paged_units<BN>(p, n);
+        }
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += warp_sum[w];
+    for (int i = 0; i < per; ++i) {
+        const int b = threadIdx.x * per + i;
+        if (b < p.B) {
+            const int units = prefix[b];
+            prefix[b] = run;
+            run += units;
+        }
+    }
+    if (threadIdx.x == kThreads - 1) prefix[p.B] = run;
+    __syncthreads();
+}
+
+template <int D, int NQ, bool kBF16>
+__global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
+    paged_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PagedDecParams p) {
+    using C = PagedCfg<D, NQ>;
+    constexpr int BN = C::BN, DA = C::DA, NB = C::NB;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_warp_sum[C::kThreads / 32];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t sQ = base, sRing = sQ + NQ * C::kQBytes, sBar = sRing + NB * C::kTileBytes;
+    uint32_t* tmem_slot =
+        reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + NQ * C::kQBytes + NB * C::kTileBytes + 8 * C::kNumBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    // Of the last two segments the one (counted from 1) whose V held a value that is not finite in a
+    // tile with hidden keys.
+    volatile int* odd_seg = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    int* plan_len = reinterpret_cast<int*>(tmem_slot + 8);
+    int* plan_prefix = plan_len + p.B;
+    auto bar = [&](int i) -> uint32_t { return sBar + 8u * (uint32_t)i; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WaitCtx wc{abort_flag, p.status};
+    const float kNegInf = -__int_as_float(0x7f800000);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kNumBars; ++i) {
+            const bool by_warpgroup = (i >= C::kBarPFull && i < C::kBarPFull + NQ) ||
+                                      (i >= C::kBarODrained && i < C::kBarODrained + NQ);
+            mbar_init(bar(i), by_warpgroup ? 4u : 1u);  // one arrive per warp
+        }
+        *abort_flag = 0;
+        odd_seg[0] = odd_seg[1] = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == C::kProducerWarp && lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    grid_dependency_wait();
+    tc_fence_before();
+    paged_make_plan<BN, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const int G = p.g * p.rg, rng = (int)blockIdx.x / G, member = (int)blockIdx.x - rng * G;
+    PagedWalk walk;
+    walk.init<BN>(p, plan_len, plan_prefix, rng);
+    PagedSeg s;
+
+    if (warp == C::kProducerWarp) {
+        // ------------------------------------------------------------ TMA producer --
+        // A tile is nb boxes of box_rows keys and DA column atoms; lane i issues box i % nb of atom
+        // i / nb.  Table entries are loaded for 32 / nb tiles at a time, one such window ahead.
+        const int nb = BN / p.box_rows, per_window = 32 / nb;
+        const int box = lane % nb, atom = lane / nb, ahead = lane / nb;
+        uint32_t loads = 0, tcount = 0;  // tiles issued (K and V count one each), segments
+        bool ok = true;
+        auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(b, parity, wc));
+        };
+        auto fetch = [&](const PagedSeg& sg, int u) -> int2 {
+            u += ahead;
+            const int key = u < sg.u1 ? sg.tiles.tile(u) * BN + box * p.box_rows : sg.len;
+            return key < sg.len ? paged_place(p, sg.b, key) : make_int2(-1, 0);
+        };
+        auto issue = [&](const CUtensorMap* map, int hk, int page, int row) -> bool {
+            const uint32_t st = loads % NB;
+            if (!wait(bar(C::kBarEmpty + st), ((loads / NB) & 1u) ^ 1u)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarFull + st), C::kTileBytes);
+            __syncwarp();
+            if (atom < DA)  // keys on no page read as zeros: a page past the last one
+                tma_load_4d(sRing + st * C::kTileBytes + atom * (BN * 128) + box * p.box_rows * 128, map,
+                            bar(C::kBarFull + st), atom * 64, hk, row, page < 0 ? p.num_pages : page);
+            ++loads;
+            return true;
+        };
+        const uint32_t q_bytes = (uint32_t)(DA * p.T * p.group * 128);
+        auto load_q = [&](const PagedSeg& sg) -> bool {
+            for (int q = 0; q < NQ; ++q) {
+                if (!wait(bar(C::kBarQEmpty + q), (tcount & 1u) ^ 1u)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(C::kBarQFull + q), q_bytes);
+                    for (int a = 0; a < DA; ++a)
+                        tma_load_4d(sQ + q * C::kQBytes + a * (C::BM * 128), &tm_q, bar(C::kBarQFull + q), a * 64,
+                                    sg.hk * p.group, (sg.rb * NQ + q) * p.T, sg.b);
+                }
+            }
+            ++tcount;
+            return true;
+        };
+        bool more = walk.next<BN>(p, member, s);
+        int2 ids = more ? fetch(s, s.u0) : make_int2(-1, 0);
+        while (more && ok) {
+            PagedSeg nxt;
+            const bool again = walk.next<BN>(p, member, nxt);
+            // The first segment's queries go first; those of a later one, which wait for the products of
+            // the segment before, behind its first tile.
+            bool need_q = tcount > 0;
+            if (!need_q) ok = load_q(s);
+            for (int u = s.u0; u < s.u1 && ok; u += per_window) {
+                const int2 use = ids;
+                if (u + per_window < s.u1)
+                    ids = fetch(s, u + per_window);
+                else if (again)
+                    ids = fetch(nxt, nxt.u0);
+                const int n = min(per_window, s.u1 - u);
+                for (int k = 0; k < n && ok; ++k) {
+                    const int page = __shfl_sync(0xffffffffu, use.x, k * nb + box);
+                    const int row = __shfl_sync(0xffffffffu, use.y, k * nb + box);
+                    ok = issue(&tm_k, s.hk, page, row) && issue(&tm_v, s.hk, page, row);
+                    if (ok && need_q) {
+                        ok = load_q(s);
+                        need_q = false;
+                    }
+                }
+            }
+            s = nxt;
+            more = again;
+        }
+        grid_launch_dependents();  // only now: the merge kernel's CTAs share the SM with this one
+        __syncwarp();
+        // Every copy this warp started has landed before shared memory goes.
+        if (lane == 0) {
+            for (uint32_t d = 0; d < (uint32_t)NB && d < loads; ++d) {
+                const uint32_t last = loads - 1 - d;
+                mbar_wait_drain(bar(C::kBarFull + last % NB), (last / NB) & 1u);
+            }
+            if (tcount > 0)
+                for (int q = 0; q < NQ; ++q) mbar_wait_drain(bar(C::kBarQFull + q), (tcount - 1) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == C::kMmaWarp) {
+        // ------------------------------------------------------------- MMA issuer ----
+        // One sub-tile: S of the next tile is issued ahead of P.V of this one, S having two buffers.  Two
+        // sub-tiles: P.V and the next S of one run while the other's softmax does.
+        constexpr uint32_t idesc_s = make_idesc_f16(128, BN, kBF16, false, false);
+        constexpr uint32_t idesc_o = make_idesc_f16(128, D, kBF16, false, true);
+        uint32_t kv_it = 0, tcount = 0;  // tiles and segments done
+        bool ok = true;
+        auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(b, parity, wc));
+        };
+        // K of tile n is load 2 n of the ring, V is load 2 n + 1.
+        auto wait_load = [&](uint32_t load) -> bool { return wait(bar(C::kBarFull + load % NB), (load / NB) & 1u); };
+        auto free_load = [&](uint32_t load) { umma_commit_elect(bar(C::kBarEmpty + load % NB)); };
+        const uint64_t dq = make_sdesc_sw128(sQ, 16, 1024);
+        const uint64_t dk = make_sdesc_sw128(sRing, 16, 1024);
+        const uint64_t dv = make_sdesc_sw128(sRing, BN * 128, 1024);
+        const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32);
+        const uint32_t k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
+        const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+        auto issue_s = [&](int q, uint32_t load, uint32_t slot) {
+            const uint32_t d = tmem + slot * BN;
+            const uint32_t a = q_lo + (uint32_t)((q * C::kQBytes) >> 4);
+            const uint32_t b = k_lo + (((load % NB) * C::kTileBytes) >> 4);
+            umma_ss_elect<false>(d, a, q_hi, b, k_hi, idesc_s);
+#pragma unroll
+            for (int kk = 1; kk < D / 16; ++kk)
+                umma_ss_elect<true>(d, a + (((kk >> 2) * (C::BM * 128) + (kk & 3) * 32) >> 4), q_hi,
+                                    b + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), k_hi, idesc_s);
+        };
+        auto issue_pv = [&](int q, uint32_t load, uint32_t slot, bool acc) {
+            const uint32_t d = tmem + C::kOCol0 + q * D;
+            const uint32_t a = tmem + slot * BN;
+            const uint32_t b = v_lo + (((load % NB) * C::kTileBytes) >> 4);
+            if (acc)
+                umma_ts_elect<true>(d, a, b, v_hi, idesc_o);
+            else
+                umma_ts_elect<false>(d, a, b, v_hi, idesc_o);
+#pragma unroll
+            for (int kk = 1; kk < BN / 16; ++kk)
+                umma_ts_elect<true>(d, a + kk * 8, b + ((kk * (16 * 128)) >> 4), v_hi, idesc_o);
+        };
+        while (ok && walk.next<BN>(p, member, s)) {
+            const int n = s.u1 - s.u0;
+            for (int q = 0; q < NQ && ok; ++q) ok = wait(bar(C::kBarQFull + q), tcount & 1u);
+            ok = ok && wait_load(2 * kv_it);
+            if (!ok) break;
+            for (int q = 0; q < NQ; ++q) {
+                const uint32_t slot = NQ == 1 ? kv_it & 1u : (uint32_t)q;
+                issue_s(q, 2 * kv_it, slot);
+                umma_commit_elect(bar(C::kBarSFull + slot));
+                if (n == 1) umma_commit_elect(bar(C::kBarQEmpty + q));
+            }
+            free_load(2 * kv_it);
+            for (int j = 0; j < n && ok; ++j) {
+                const bool next = j + 1 < n;
+                if (NQ == 1 && next) {
+                    ok = wait_load(2 * kv_it + 2);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(0, 2 * kv_it + 2, (kv_it + 1) & 1u);
+                    umma_commit_elect(bar(C::kBarSFull + ((kv_it + 1) & 1u)));
+                    free_load(2 * kv_it + 2);
+                    if (j + 2 == n) umma_commit_elect(bar(C::kBarQEmpty));
+                }
+                ok = wait_load(2 * kv_it + 1);
+                for (int q = 0; q < NQ && ok; ++q) {
+                    ok = wait(bar(C::kBarPFull + q), kv_it & 1u);
+                    if (ok && j == 0 && tcount > 0) ok = wait(bar(C::kBarODrained + q), (tcount - 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(q, 2 * kv_it + 1, NQ == 1 ? kv_it & 1u : (uint32_t)q, j > 0);
+                    if (NQ == 1 || !next) umma_commit_elect(bar(C::kBarODone + q));
+                    if (q == NQ - 1) free_load(2 * kv_it + 1);
+                    if (NQ > 1 && next) {
+                        if (q == 0) {
+                            ok = wait_load(2 * kv_it + 2);
+                            if (!ok) break;
+                        }
+                        issue_s(q, 2 * kv_it + 2, (uint32_t)q);
+                        umma_commit_elect(bar(C::kBarSFull + q));
+                        if (q == NQ - 1) free_load(2 * kv_it + 2);
+                        if (j + 2 == n) umma_commit_elect(bar(C::kBarQEmpty + q));
+                    }
+                }
+                ++kv_it;
+            }
+            ++tcount;
+        }
+        // Every product issued is done before TMEM and shared memory are released.
+        umma_commit_elect(bar(C::kBarFinal));
+        mbar_wait_drain(bar(C::kBarFinal), 0);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ softmax warpgroups ----
+        const int q = warp >> 2, wq = warp & 3;
+        const int r = wq * 32 + lane;  // row of the sub-tile
+        const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t tO = lane_base + C::kOCol0 + q * D;
+        constexpr int kSC = BN / 32;
+        constexpr float kRescaleLog2 = 8.0f;  // O is rescaled only when a maximum grows by more than 2^8
+        const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+        const int block_rows = min(NQ * p.T, p.Sq) * p.group;
+        uint16_t* o16 = static_cast<uint16_t*>(p.o);
+        uint32_t it = 0, tcount = 0;
+        bool ok = true;
+
+        // Sequences without keys.
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (plan_len[b] > 0) continue;
+            const long long vals = (long long)p.Sq * p.Hq * D, rows = (long long)p.Sq * p.Hq;
+            for (long long i = (long long)threadIdx.x * 8; i < vals; i += 128 * NQ * 8)
+                st_global_v4(o16 + b * vals + i, 0u, 0u, 0u, 0u);
+            if (p.lse)
+                for (long long i = threadIdx.x; i < rows; i += 128 * NQ) p.lse[b * rows + i] = kNegInf;
+        }
+
+        while (ok && walk.next<BN>(p, member, s)) {
+            const int n = s.u1 - s.u0, tok_l = r / p.group, h_l = r - tok_l * p.group;
+            const int tok = (s.rb * NQ + q) * p.T + tok_l;
+            const bool live = tok_l < p.T && tok < p.Sq;
+            const bool any = __any_sync(0xffffffffu, live);  // whether the warp has rows
+            float m_run = kNegInf;
+            uint64_t l2 = f2_pack(0.f, 0.f);
+            for (int j = 0; j < n; ++j) {
+                const int n0 = s.tiles.tile(s.u0 + j) * BN;
+                const bool masked = paged_masked<BN>(p, s.len, n0);
+                if (masked && q == 0) {
+                    // V's values that are not finite give way to zeros, the warpgroup's threads
+                    // taking 16 bytes each in turn.
+                    const uint32_t load = 2 * it + 1, at = sRing + (load % NB) * C::kTileBytes;
+                    ok = mbar_wait(bar(C::kBarFull + load % NB), (load / NB) & 1u, wc);
+                    if (!ok) break;
+                    bool odd = false;
+                    for (int i = r; i < C::kTileBytes / 16; i += 128) {
+                        uint32_t w[4];
+                        lds128(at + i * 16, w);
+                        if (paged_nonfinite<kBF16>(w[0]) | paged_nonfinite<kBF16>(w[1]) | paged_nonfinite<kBF16>(w[2]) |
+                            paged_nonfinite<kBF16>(w[3])) {
+                            odd = true;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] &= (paged_nonfinite<kBF16>(w[k] & 0xffffu) ? 0u : 0xffffu) |
+                                        (paged_nonfinite<kBF16>(w[k] & 0xffff0000u) ? 0u : 0xffff0000u);
+                            st_shared_v4(at + i * 16, w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    if (odd) odd_seg[tcount & 1u] = (int)tcount + 1;
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                }
+                const uint32_t slot = NQ == 1 ? it & 1u : (uint32_t)q;
+                ok = mbar_wait(bar(C::kBarSFull + slot), NQ == 1 ? (it >> 1) & 1u : it & 1u, wc);
+                if (!ok) break;
+                tc_fence_after();
+                float alpha = 1.f;
+                if (any) {
+                    const uint32_t tS = lane_base + slot * BN;  // P goes over S
+                    uint32_t u[kSC][32];
+#pragma unroll
+                    for (int ch = 0; ch < kSC; ++ch) tmem_ld_32x32b_x32(tS + ch * 32, u[ch]);
+                    tmem_wait_ld(u[0]);
+#pragma unroll
+                    for (int ch = 1; ch < kSC; ++ch) reg_fence(u[ch]);
+                    if (masked) {
+#pragma unroll
+                        for (int ch = 0; ch < kSC; ++ch) {
+                            const uint32_t w = live ? paged_sees(p, s.b, tok, s.len, n0 + ch * 32) : 0u;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[ch][i] = (w >> i) & 1u ? u[ch][i] : 0xff800000u;
+                        }
+                        __syncwarp();
+                    }
+                    auto sv = [&](int k) -> float { return __uint_as_float(u[k >> 5][k & 31]); };
+                    float mx[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = sv(k);
+#pragma unroll
+                    for (int k = 4; k + 8 <= BN; k += 8)
+#pragma unroll
+                        for (int c4 = 0; c4 < 4; ++c4) mx[c4] = max3f(mx[c4], sv(k + c4), sv(k + c4 + 4));
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) mx[c4] = fmaxf(mx[c4], sv(BN - 4 + c4));
+                    const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float m_blk = raw_max == kNegInf ? kNegInf : raw_max * p.scale_log2;
+                    const bool bump = m_blk > m_run + kRescaleLog2;
+                    const float m_new = bump ? m_blk : m_run;
+                    alpha = bump ? ex2_approx(m_run - m_new) : 1.0f;
+                    m_run = m_new;
+                    const float m_sub = m_run == kNegInf ? 0.f : m_run;
+                    const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
+                    // P = exp2(s * scale * log2 e - m), rounded to the inputs' 16 bits for the product (a
+                    // relative error of half a step each, independent, so of a row's output about that
+                    // of its own rounding); the sum l takes it unrounded.
+                    uint64_t sum2 = f2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int ch = 0; ch < kSC; ++ch) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint64_t a = fma2(f2_pack(sv(ch * 32 + 2 * i), sv(ch * 32 + 2 * i + 1)), c2, nm2);
+                            float a0, a1;
+                            f2_unpack(a, a0, a1);
+                            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+                            sum2 = add2(sum2, f2_pack(p0, p1));
+                            pk[i] = pack2<kBF16>(p0, p1);
+                        }
+                        tmem_st_32x32b_x16(tS + ch * 16, pk);
+                    }
+                    l2 = fma2(l2, f2_pack(alpha, alpha), sum2);
+                }
+                if (NQ == 1 && j > 0) {
+                    // the product before may still be adding to O (with two sub-tiles, S of this tile
+                    // was issued behind it)
+                    ok = mbar_wait(bar(C::kBarODone + q), (it - 1) & 1u, wc);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (any && j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t ov[32];
+                        tmem_ld_32x32b_x32(tO + ch * 32, ov);
+                        tmem_wait_ld(ov);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tmem_st_32x32b_x32(tO + ch * 32, ov);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kBarPFull + q));
+                ++it;
+            }
+            if (!ok) break;
+
+            // ------------------------------------------------------------ epilogue ----
+            ok = mbar_wait(bar(C::kBarODone + q), NQ == 1 ? (it - 1) & 1u : tcount & 1u, wc);
+            if (!ok) break;
+            tc_fence_after();
+            if (any) {
+                const bool odd = odd_seg[tcount & 1u] == (int)tcount + 1;
+                float l0, l1;
+                f2_unpack(l2, l0, l1);
+                const float l_run = l0 + l1;
+                const bool none = l_run == 0.f;  // the row sees no key of the segment
+                const float inv_l = 1.0f / l_run;
+                const int h = s.hk * p.group + h_l;
+                const size_t row = ((size_t)s.b * p.Sq + tok) * p.Hq + h;
+                const size_t part = ((size_t)member * 2 * p.ranges + s.slot) * block_rows + q * p.T * p.group + r;
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t ov[32];
+                    tmem_ld_32x32b_x32(tO + ch * 32, ov);
+                    tmem_wait_ld(ov);
+                    if (live) {
+                        if (odd) {
+                            // What was taken out of V, to the rows that see it (rare: one copy of the code).
+                            for (int u = s.u0; u < s.u1; ++u) {
+                                const int n0 = s.tiles.tile(u) * BN;
+                                if (!paged_masked<BN>(p, s.len, n0)) continue;
+                                for (int c = 0; c < BN; ++c) {
+                                    if (!(paged_sees(p, s.b, tok, s.len, n0 + c) & 1u)) continue;
+                                    const int2 at = paged_place(p, s.b, n0 + c);
+                                    if (at.x < 0) continue;
+                                    const uint16_t* v = p.v_pages +
+                                                        (((size_t)at.x * p.page_size + at.y) * p.Hkv + s.hk) * D + ch * 32;
+    #pragma unroll
+                                    for (int i = 0; i < 32; ++i) {
+                                        const uint32_t x = v[i];
+                                        if (paged_nonfinite<kBF16>(x))
+                                            ov[i] = __float_as_uint(__uint_as_float(ov[i]) + paged_from16<kBF16>(x));
+                                    }
+                                }
+                            }
+                        }
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = none ? 0u : __float_as_uint(__uint_as_float(ov[i]) * inv_l);
+                        if (s.cut) {
+                            float* to = p.o_part + part * D + ch * 32;
+    #pragma unroll
+                            for (int i = 0; i < 32; i += 4) st_global_v4(to + i, ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                        } else {
+                            uint32_t w[16];
+    #pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = pack2<kBF16>(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1]));
+                            uint16_t* to = o16 + row * D + ch * 32;
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                st_global_v4(to + i * 8, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                        }
+                    }
+                    __syncwarp();  // the next TMEM load is the whole warp's
+                }
+                if (live) {
+                    const float lse = none ? kNegInf : (m_run + lg2_approx(l_run)) * kPagedLn2;
+                    if (s.cut)
+                        p.lse_part[part] = lse;
+                    else if (p.lse)
+                        p.lse[((size_t)s.b * p.Hq + h) * p.Sq + tok] = lse;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kBarODrained + q));
+            ++tcount;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// Joins the pieces of each row (b, token, head): lse = log sum_c exp(lse_c), and the outputs
+// weighted with exp(lse_c - lse).  WPR warps share a row, each taking every WPR-th piece; a lane
+// holds D / 32 dims.  Where the pieces lie is worked out before the split kernel is done.
+template <int D, int NQ, int WPR, bool kBF16>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p) {
+    constexpr int V = D / 32, Rows = 8 / WPR, NP = V <= 4 ? 8 : 4, BN = PagedCfg<D, NQ>::BN;
+    constexpr int Vec = V % 4 == 0 ? 4 : V % 2 == 0 ? 2 : 1;  // values of a lane side by side
+    __shared__ __align__(16) float s_acc[WPR > 1 ? 8 : 1][D];
+    __shared__ float s_sum[8], s_max[8];
+    __shared__ int s_units[kPagedMaxB];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = (long long)blockIdx.x * Rows + warp / WPR;
+    const int part = warp % WPR;
+    const float kNegInf = -__int_as_float(0x7f800000);
+    const int per_seq = p.Sq * p.Hq;
+    const int b = (int)(row / per_seq), in_seq = (int)(row - (long long)b * per_seq);
+    const int tok = in_seq / p.Hq, h = in_seq - tok * p.Hq;
+    for (int i = threadIdx.x; i < p.B; i += 256) s_units[i] = paged_units<BN>(p, paged_len(p, i));
+    __syncthreads();
+    int before = 0, sum = 0, units = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const int t = s_units[i];
+        before += i < b ? t : 0;
+        units += i == b ? t : 0;
+        sum += t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    const int hk = h / p.group, rb = tok / (NQ * p.T);
+    const int e = hk / p.g * (p.row_blocks / p.rg) + rb / p.rg, member = hk % p.g + rb % p.rg * p.g;
+    const int W = paged_width(p, sum), start = p.entries * before + e * units;
+    const int n = paged_pieces(start, units, W), first = paged_first_piece(start, W);
+    const int block_rows = min(NQ * p.T, p.Sq) * p.group;
+    const int in_block = (tok - rb * NQ * p.T) * p.group + h - hk * p.group;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    // Rows with one piece or none have been written by the split kernel.  n is the same in all of a
+    // row's warps.
+    if (row >= (long long)p.B * per_seq || n < 2) return;
+    float acc[V], s = 0.f, m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int c0 = part; c0 < n; c0 += WPR * NP) {
+        float w[NP], v[NP][V], top = m;
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {  // pieces past n: the last one, with weight 0
+            const int c = min(c0 + u * WPR, n - 1);
+            const size_t at =
+                ((size_t)member * 2 * p.ranges + paged_slot(p, first + c, c == 0)) * block_rows + in_block;
+            w[u] = p.lse_part[at];
+#pragma unroll
+            for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
+        }
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+            if (c0 + u * WPR >= n) w[u] = kNegInf;
+            top = fmaxf(top, w[u]);
+        }
+        const float ref = top == kNegInf ? 0.f : top;
+        const float f = ex2_approx((m - ref) * (1.f / kPagedLn2));
+        m = top;
+        s *= f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= f;
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+            const float x = ex2_approx((w[u] - ref) * (1.f / kPagedLn2));
+            s += x;
+            // a weight of 0 must not meet a NaN or an infinity of a piece read twice
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(x, w[u] == kNegInf ? 0.f : v[u][i], acc[i]);
+        }
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_acc[warp][i / Vec * Vec * 32 + lane * Vec + i % Vec] = acc[i];
+        if (lane == 0) {
+            s_sum[warp] = s;
+            s_max[warp] = m;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) m = fmaxf(m, s_max[w]);
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        const float ref = m == kNegInf ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+            const float f = ex2_approx((s_max[w] - ref) * (1.f / kPagedLn2));
+            s += f * s_sum[w];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                acc[i] = fmaf(f, s_acc[w][i / Vec * Vec * 32 + lane * Vec + i % Vec], acc[i]);
+        }
+    }
+    const float inv = 1.f / s;  // s == 0: no piece holds a visible key
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = s == 0.f ? 0.f : acc[i] * inv;
+    uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * Vec;
+#pragma unroll
+    for (int i = 0; i < V; i += Vec) {
+        if constexpr (Vec == 1)
+            out[i * 32] = float_to16<kBF16>(acc[i]);
+        else if constexpr (Vec == 2)
+            *reinterpret_cast<uint32_t*>(out + i * 32) = pack2<kBF16>(acc[i], acc[i + 1]);
+        else
+            *reinterpret_cast<uint2*>(out + i * 32) =
+                make_uint2(pack2<kBF16>(acc[i], acc[i + 1]), pack2<kBF16>(acc[i + 2], acc[i + 3]));
+    }
+    if (p.lse && lane == 0)
+        p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kPagedLn2;
+}
+
+template <int D, int NQ, int WPR>
+fa_status launch_paged_merge(const PagedDecParams& p, bool bf16, cudaStream_t s) {
+    static int attr[64] = {0};
+    if (!prefer_shared((const void*)paged_merge_kernel<D, NQ, WPR, true>,
+                       (const void*)paged_merge_kernel<D, NQ, WPR, false>, attr))
+        return FA_ERR_CUDA;
+    const long long rows = (long long)p.B * p.Sq * p.Hq;
+    const unsigned grid = (unsigned)((rows + 8 / WPR - 1) / (8 / WPR));
+    return bf16 ? launch_overlapped(paged_merge_kernel<D, NQ, WPR, true>, grid, 256, 0, s, p)
+                : launch_overlapped(paged_merge_kernel<D, NQ, WPR, false>, grid, 256, 0, s, p);
+}
+
+template <int D, int NQ, bool kBF16>
+fa_status launch_paged_split(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedDecParams& p, cudaStream_t s) {
+    using C = PagedCfg<D, NQ>;
+    static int attr[64] = {0};
+    if (!ensure_smem_attr((const void*)paged_split_kernel<D, NQ, kBF16>, C::kFixedBytes + C::plan_bytes(kPagedMaxB), attr))
+        return FA_ERR_CUDA;
+    return launch_overlapped(paged_split_kernel<D, NQ, kBF16>, (unsigned)(p.ranges * p.g * p.rg), C::kThreads,
+                             C::kFixedBytes + C::plan_bytes(p.B), s, tq, tk, tv, p);
+}
+
+template <int D, int NQ>
+fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
+    using C = PagedCfg<D, NQ>;
+    PagedDecParams p;
+    p.B = a.B, p.Sq = a.Sq, p.Hq = a.Hq, p.Hkv = a.Hkv;
+    p.group = a.Hq / a.Hkv;
+    p.T = std::min(a.Sq, C::BM / p.group);
+    p.row_blocks = (a.Sq + NQ * p.T - 1) / (NQ * p.T);
+    p.g = a.Hkv % 8 == 0 ? 8 : a.Hkv % 4 == 0 ? 4 : a.Hkv % 2 == 0 ? 2 : 1;
+    p.rg = p.g * p.row_blocks <= 16 ? p.row_blocks : 1;
+    const int G = p.g * p.rg;
+    if (G > a.num_sms) return FA_ERR_UNSUPPORTED;
+    p.entries = a.Hkv / p.g * (p.row_blocks / p.rg);
+    p.capacity = a.page_size * a.max_pages;
+    p.page_size = a.page_size, p.num_pages = a.num_pages, p.max_pages = a.max_pages;
+    p.box_rows = std::min(a.page_size & -a.page_size, C::BN);
+    p.page_recip = (unsigned)((1ull << 32) / (unsigned)a.page_size) + 1u;
+    p.window_left = a.window_left, p.sinks = a.sinks;
+    p.words = (a.Sq + 31) / 32;
+    p.table = a.table, p.kv_lens = a.kv_lens, p.tree = a.tree;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.o = a.o, p.lse = a.lse, p.o_part = a.o_part, p.lse_part = a.lse_part;
+    p.v_pages = static_cast<const uint16_t*>(a.v_pages);
+    p.status = a.dev_status;
+    // The most tiles that a sequence can have.
+    long long most = (p.capacity + C::BN - 1) / C::BN;
+    if (a.window_left >= 0)
+        most = std::min(most, ((long long)a.window_left + a.Sq + C::BN - 1) / C::BN + 1 +
+                                  ((long long)a.sinks + C::BN - 1) / C::BN);
+    const long long units = (most + kPagedLead) * p.entries * a.B;  // of all entries at most
+    if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    p.whole = most + kPagedLead <= kPagedMinWidth ? 1 : 0;
+    p.ranges = (int)std::min((long long)(a.num_sms / G), (units + kPagedMinWidth - 1) / kPagedMinWidth);
+    CUtensorMap tq, tk, tv;
+    if (!encode_paged_tmap(&tq, a.q, a.bf16, D, a.Hq, a.Sq, a.B, p.group, p.T) ||
+        !encode_paged_tmap(&tk, a.k_pages, a.bf16, D, a.Hkv, a.page_size, a.num_pages, 1, p.box_rows) ||
+        !encode_paged_tmap(&tv, a.v_pages, a.bf16, D, a.Hkv, a.page_size, a.num_pages, 1, p.box_rows))
+        return FA_ERR_CUDA;
+    const fa_status st = a.bf16 ? launch_paged_split<D, NQ, true>(tq, tk, tv, p, s)
+                                : launch_paged_split<D, NQ, false>(tq, tk, tv, p, s);
+    if (st != FA_OK || p.whole) return st;
+    // Few rows are cut into many pieces: eight warps each.
+    return (long long)a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_paged_merge<D, NQ, 8>(p, a.bf16, s)
+                                                         : launch_paged_merge<D, NQ, 1>(p, a.bf16, s);
+}
+
+// Two sub-tiles share each key tile where one does not hold a kv head's rows (at D = 256 TMEM has
+// room for one: row blocks then share the keys through L2).
+template <int D>
+fa_status launch_paged_decode_d(const PagedDecodeArgs& a, cudaStream_t s) {
+    if constexpr (D != 256) {
+        const int group = a.Hq / a.Hkv;
+        if (a.Sq > 128 / group) return launch_paged_nq<D, 2>(a, s);
+    }
+    return launch_paged_nq<D, 1>(a, s);
+}
+
+}  // namespace fa

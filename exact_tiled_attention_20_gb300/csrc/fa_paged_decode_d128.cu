@@ -1,0 +1,8 @@
+// fa_paged_decode_d128.cu -- instantiation of the decode over the 16-bit paged cache for head dim 128.
+#include "fa_paged_decode.cuh"
+
+namespace fa {
+
+fa_status launch_paged_decode_d128(const PagedDecodeArgs& a, cudaStream_t s) { return launch_paged_decode_d<128>(a, s); }
+
+}  // namespace fa

@@ -342,6 +342,104 @@ FA_API fa_status fa_decode_splitkv_paged_fp8(const void *q, const void *k_pages,
                                              size_t workspace_bytes, fa_dtype dtype,
                                              fa_stream_t stream);
 
+/*
+ * The 16-bit paged cache, written and attended over.  fa_decode_splitkv_paged reads it; these
+ * entry points write it and attend over it with several query tokens, under other masks than
+ * "all keys".  The pool is the same:
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, D] (dtype)
+ *   block_table       device int32 [B, max_pages_per_seq]: key r of sequence b is row
+ *                     r % page_size of page block_table[b][r / page_size]
+ * D in {64, 96, 128, 256}; B <= 1024; Hkv <= 65536; page_size <= 2^28;
+ * page_size * max_pages_per_seq <= 2^31 - 4096.  Table entries outside [0, num_pages) that a call
+ * meets are the caller's error: nothing is read or written outside the pool.  Outputs and the
+ * workspace must not overlap the inputs, but for q_out below.
+ *
+ * fa_kv_append_paged_rope writes new rows, keys and queries turned by their positions on the way.
+ *   q, k_new, v_new  token t, head h at element t * q_stride (k_stride, v_stride) + h * D, so the
+ *                    rows may lie inside a fused projection's output; strides in elements,
+ *                    multiples of 8, at least Hq * D (Hkv * D); 16-byte aligned
+ *   q_out            [total_new, Hq, D]: the turned queries; may be q where q_stride is Hq * D.
+ *                    Hq == 0: no queries, and q and q_out are not used
+ *   cu_seqlens_new   device int32 [B + 1]: sequence b's new tokens are packed rows
+ *                    [cu_seqlens_new[b], cu_seqlens_new[b + 1]), non-decreasing, ending at most at
+ *                    total_new; rows of no sequence are neither written to the pool nor to q_out.
+ *                    NULL: every sequence has total_new / B new tokens (B must divide total_new)
+ *   kv_lens          device int32 [B]: sequence b's keys INCLUDING the new ones, which become its
+ *                    last keys, kv_lens[b] - n .. kv_lens[b] - 1
+ *   positions        device int32 [total_new]; NULL: a token's position is its key.  (Drafts of a
+ *                    tree, several of which have one position, need them.)
+ *   cos, sin         device fp32 [max_pos, rot_dim / 2], 16-byte aligned: of the angles of each
+ *                    position.  Positions outside [0, max_pos) are the caller's error and clamped
+ *   rot_dim          the first dims of a row that turn: a multiple of 16, 0 .. D (0: none; cos and
+ *                    sin may then be NULL); dims from there on are copied
+ *   interleaved      zero: pairs (d, d + rot_dim / 2); nonzero: pairs (2 d, 2 d + 1).  A pair
+ *                    (x, y) becomes (x cos - y sin, y cos + x sin), in fp32, rounded once
+ * Any page_size >= 1.  V's rows are copied.  Rows whose key is outside [0, page_size *
+ * max_pages_per_seq) or whose page is outside the pool are dropped (their queries are still
+ * written).  total_new == 0 writes nothing.  Two tokens that name one row of a page are the
+ * caller's error.  total_new * (Hq + 2 Hkv) < 2^31.
+ */
+FA_API fa_status fa_kv_append_paged_rope(const void *q, const void *k_new, const void *v_new,
+                                         int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                         void *q_out, const int32_t *cu_seqlens_new,
+                                         const int32_t *block_table, const int32_t *kv_lens,
+                                         const int32_t *positions, const float *cos,
+                                         const float *sin, void *k_pages, void *v_pages, int B,
+                                         int total_new, int Hq, int Hkv, int D, int rot_dim,
+                                         int interleaved, int max_pos, int num_pages, int page_size,
+                                         int max_pages_per_seq, fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * Bytes of workspace of the two decodes below: two partial results for each SM, of at most 256
+ * query rows each, whatever the lengths.  num_sms <= 0 queries the current device.  0 for invalid
+ * sizes, or when no device can be queried.
+ */
+FA_API size_t fa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int num_sms);
+
+/*
+ * Attention of a tree of drafted tokens: Sq query tokens per sequence, which are the last Sq keys
+ * of its cache (appended before).  Draft t of sequence b is key kv_lens[b] - Sq + t; token i sees
+ * every key before the drafts, and draft t where bit t % 32 of word t / 32 of its mask is set.
+ *   q, o       [B, Sq, Hq, D] (dtype)     lse [B, Hq, Sq] fp32 (may be NULL)
+ *   tree_mask  device int32 [B, Sq, ceil(Sq / 32)]; a token sees itself only if its own bit is
+ *              set; bits from Sq on are not used.  Trees of fewer than Sq drafts are padded with
+ *              drafts that no mask names (their outputs are computed and meaningless)
+ *   kv_lens    device int32 [B], 0 <= kv_lens[b] <= page_size * max_pages_per_seq, clamped on the
+ *              device.  Where kv_lens[b] < Sq the drafts before the first key do not exist
+ *   workspace  at least fa_decode_paged_workspace_bytes(...) bytes; no initialisation.  Calls that
+ *              may overlap on the GPU need one each
+ * page_size is a multiple of 16; Sq <= 256; Hq / Hkv <= 128.  A token that sees no key gets O = 0
+ * and LSE = -inf.  What lies in the pool behind a sequence's last key, and a key hidden from a
+ * token, is not used for it, NaN and infinities included.  Keys on a page outside the pool count
+ * as zero rows.  Accumulation is fp32; P is rounded to the input dtype before the P.V product; O is
+ * rounded once.  The same inputs give the same bits.
+ */
+FA_API fa_status fa_decode_splitkv_paged_tree(const void *q, const void *k_pages,
+                                              const void *v_pages, const int32_t *block_table,
+                                              const int32_t *kv_lens, const int32_t *tree_mask,
+                                              void *o, float *lse, int B, int Sq, int Hq, int Hkv,
+                                              int D, int num_pages, int page_size,
+                                              int max_pages_per_seq, float scale, void *workspace,
+                                              size_t workspace_bytes, fa_dtype dtype,
+                                              fa_stream_t stream);
+
+/*
+ * Decode with a sliding window and sinks: Sq query tokens per sequence, the last ones of its
+ * cache.  Token i, at key p = kv_lens[b] - Sq + i, sees the keys j <= p with
+ *     j >= p - window_left    or    j < sinks;
+ * window_left == -1 leaves the window unbounded (a causal decode).  Pages that hold no visible key
+ * are not read, and their table entries may be anything.  window_left >= -1 and sinks >= 0, else
+ * FA_ERR_INVALID_ARG; everything else as fa_decode_splitkv_paged_tree.
+ */
+FA_API fa_status fa_decode_splitkv_paged_window(const void *q, const void *k_pages,
+                                                const void *v_pages, const int32_t *block_table,
+                                                const int32_t *kv_lens, void *o, float *lse, int B,
+                                                int Sq, int Hq, int Hkv, int D, int num_pages,
+                                                int page_size, int max_pages_per_seq, float scale,
+                                                int window_left, int sinks, void *workspace,
+                                                size_t workspace_bytes, fa_dtype dtype,
+                                                fa_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 FA_API const char *fa_status_string(fa_status s);
 
