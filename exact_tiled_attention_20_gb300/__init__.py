@@ -6,6 +6,8 @@ generators (``inputs``).  The binding's names mirror the C entry points:
 
 * ``fa_fwd`` -- exact attention forward with per-row log-sum-exp;
 * ``fa_fwd(..., window=(left, right))`` -- sliding-window local attention (fa_fwd_window);
+* ``fa_fwd(..., window=(left, right), sinks=n)``, ``fa_fwd_varlen(..., sinks=n)`` -- with the first n
+  keys visible left of the window (fa_fwd_sinks, fa_fwd_varlen_sinks);
 * ``fa_fwd_varlen`` -- variable-length batches packed along the rows (cu_seqlens);
 * ``fa_decode_splitkv`` -- split-KV (Flash-Decoding) single-token decode;
 * ``fa_decode_splitkv_multi`` -- the same with several query tokens per sequence;

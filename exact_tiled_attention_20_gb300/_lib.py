@@ -52,6 +52,8 @@ def load():
         lib.fa_fwd.restype = I
         lib.fa_fwd_window.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, P]
         lib.fa_fwd_window.restype = I
+        lib.fa_fwd_sinks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P]
+        lib.fa_fwd_sinks.restype = I
         lib.fa_decode_workspace_bytes.argtypes = [I, I, I, I]
         lib.fa_decode_workspace_bytes.restype = SZ
         lib.fa_decode_default_splits.argtypes = [I, I, I, I]
@@ -102,9 +104,10 @@ def fa_selftest_bounded_wait(result, stream=None) -> int:
 
 
 def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None,
-           return_lse: bool = True, stream=None, window=None):
+           return_lse: bool = True, stream=None, window=None, sinks: int = 0):
     """Exact attention forward through fa_fwd (or fa_fwd_window when ``window=(left,
-    right)`` is given; -1 = unbounded side).  q [B,Sq,Hq,D], k/v [B,Sk,Hkv,D].
+    right)`` is given; -1 = unbounded side; fa_fwd_sinks with ``sinks`` > 0, the first keys that
+    stay visible left of the window).  q [B,Sq,Hq,D], k/v [B,Sk,Hkv,D].
 
     Returns (o, lse): o like q, lse fp32 [B, Hq, Sq] (None if return_lse is False and no
     lse buffer was given).  scale defaults to 1/sqrt(D).
@@ -131,7 +134,12 @@ def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, 
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     with torch.cuda.device(q.device):
         lp = lse.data_ptr() if lse is not None else None
-        if window is None:
+        if sinks:
+            left, right = window if window is not None else (-1, -1)
+            st = load().fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, B, Sq, Sk, Hq,
+                                     Hkv, D, sc, int(bool(causal)), int(left), int(right), min(int(sinks), 2**31 - 1),
+                                     _DTYPE[q.dtype], _stream_handle(stream))
+        elif window is None:
             st = load().fa_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, B, Sq,
                                Sk, Hq, Hkv, D, sc, int(bool(causal)), _DTYPE[q.dtype],
                                _stream_handle(stream))
@@ -140,7 +148,7 @@ def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, 
                                       B, Sq, Sk, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
                                       int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
     if st != FA_OK:
-        raise FaError(st, "fa_fwd_window" if window is not None else "fa_fwd")
+        raise FaError(st, "fa_fwd_sinks" if sinks else "fa_fwd_window" if window is not None else "fa_fwd")
     return out, lse
 
 
@@ -297,15 +305,19 @@ _varlen_declared = False
 
 
 def fa_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, causal: bool = False,
-                  scale: float | None = None, window=(-1, -1), out=None, lse=None, stream=None):
-    """Variable-length batch through fa_fwd_varlen: q [total_q, Hq, D], k/v [total_k, Hkv, D],
-    cu_seqlens_q/k int32 [B+1] on the device.  Returns (o [total_q, Hq, D], lse [Hq, total_q])."""
+                  scale: float | None = None, window=(-1, -1), out=None, lse=None, stream=None, sinks: int = 0):
+    """Variable-length batch through fa_fwd_varlen (fa_fwd_varlen_sinks with ``sinks`` > 0, the
+    first keys of a sequence that stay visible left of the window): q [total_q, Hq, D], k/v
+    [total_k, Hkv, D], cu_seqlens_q/k int32 [B+1] on the device.  Returns (o [total_q, Hq, D],
+    lse [Hq, total_q])."""
     global _varlen_declared
     lib = load()
     if not _varlen_declared:
         P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
         lib.fa_fwd_varlen.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, P]
         lib.fa_fwd_varlen.restype = I
+        lib.fa_fwd_varlen_sinks.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P]
+        lib.fa_fwd_varlen_sinks.restype = I
         _varlen_declared = True
     if q.dtype not in _DTYPE:
         raise TypeError("q/k/v must be bf16 or fp16")
@@ -324,12 +336,15 @@ def fa_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, causal: bool = False,
         lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     with torch.cuda.device(q.device):
-        st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                               lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B,
-                               total_q, total_k, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
-                               int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
+        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(),
+                cu_seqlens_k.data_ptr(), B, total_q, total_k, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
+                int(window[1]))
+        if sinks:
+            st = lib.fa_fwd_varlen_sinks(*args, min(int(sinks), 2**31 - 1), _DTYPE[q.dtype], _stream_handle(stream))
+        else:
+            st = lib.fa_fwd_varlen(*args, _DTYPE[q.dtype], _stream_handle(stream))
     if st != FA_OK:
-        raise FaError(st, "fa_fwd_varlen")
+        raise FaError(st, "fa_fwd_varlen_sinks" if sinks else "fa_fwd_varlen")
     return out, lse
 
 

@@ -231,15 +231,36 @@ using namespace fa;
 
 extern "C" {
 
-fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B,
-                        int Sq, int Sk, int Hq, int Hkv, int D, float scale, int causal,
-                        int window_left, int window_right, fa_dtype dtype, fa_stream_t stream) {
+namespace {
+
+// Sinks count where a window that is shorter than the keys ends on the left of them.
+fa_status launch_fwd(FwdArgs& a, int sinks, int keys, cudaStream_t s) {
+    if (sinks > 0 && a.window_left >= 0 && a.window_left < keys) {
+        a.sinks = sinks < keys ? sinks : keys;
+        switch (a.D) {
+            case 64: return launch_sinks_d64(a, s);
+            case 96: return launch_sinks_d96(a, s);
+            case 128: return launch_sinks_d128(a, s);
+            default: return launch_sinks_d256(a, s);
+        }
+    }
+    switch (a.D) {
+        case 64: return launch_fwd_d64(a, s);
+        case 96: return launch_fwd_d96(a, s);
+        case 128: return launch_fwd_d128(a, s);
+        default: return launch_fwd_d256(a, s);
+    }
+}
+
+fa_status fwd_fixed(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Sq, int Sk, int Hq,
+                    int Hkv, int D, float scale, int causal, int window_left, int window_right, int sinks,
+                    fa_dtype dtype, fa_stream_t stream) {
     if (!q || !k || !v || !o) return FA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return FA_ERR_INVALID_ARG;
     if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return FA_ERR_INVALID_ARG;
     if (B <= 0 || Sq <= 0 || Sk <= 0 || Hq <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
     if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-    if (window_left < -1 || window_right < -1) return FA_ERR_INVALID_ARG;
+    if (window_left < -1 || window_right < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
     if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
     if (D != 64 && D != 96 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;
@@ -251,18 +272,12 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
     FwdArgs a{q, k, v, o, lse, B, Sq, Sk, Hq, Hkv, D, scale, causal, window_left, window_right,
               nullptr, nullptr, 0, 0, dtype == FA_BF16, di.num_sms, di.status};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    switch (D) {
-        case 64: return launch_fwd_d64(a, s);
-        case 96: return launch_fwd_d96(a, s);
-        case 128: return launch_fwd_d128(a, s);
-        default: return launch_fwd_d256(a, s);
-    }
+    return launch_fwd(a, sinks, Sk, s);
 }
 
-fa_status fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
-                        const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
-                        int total_q, int total_k, int Hq, int Hkv, int D, float scale, int causal,
-                        int window_left, int window_right, fa_dtype dtype, fa_stream_t stream) {
+fa_status fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_seqlens_q,
+                     const int32_t* cu_seqlens_k, int B, int total_q, int total_k, int Hq, int Hkv, int D, float scale,
+                     int causal, int window_left, int window_right, int sinks, fa_dtype dtype, fa_stream_t stream) {
     if (!q || !k || !v || !o || !cu_seqlens_q || !cu_seqlens_k) return FA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return FA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) ||
@@ -271,7 +286,7 @@ fa_status fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, fl
     if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return FA_ERR_INVALID_ARG;
     if (B <= 0 || total_q <= 0 || total_k <= 0 || Hq <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
     if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
-    if (window_left < -1 || window_right < -1) return FA_ERR_INVALID_ARG;
+    if (window_left < -1 || window_right < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
     if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
     if (D != 64 && D != 96 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;
@@ -284,12 +299,38 @@ fa_status fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, fl
               cu_seqlens_q, cu_seqlens_k, total_q, total_k, dtype == FA_BF16, di.num_sms,
               di.status};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    switch (D) {
-        case 64: return launch_fwd_d64(a, s);
-        case 96: return launch_fwd_d96(a, s);
-        case 128: return launch_fwd_d128(a, s);
-        default: return launch_fwd_d256(a, s);
-    }
+    return launch_fwd(a, sinks, total_k, s);
+}
+
+}  // namespace
+
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                        int Sq, int Sk, int Hq, int Hkv, int D, float scale, int causal,
+                        int window_left, int window_right, fa_dtype dtype, fa_stream_t stream) {
+    return fwd_fixed(q, k, v, o, lse, B, Sq, Sk, Hq, Hkv, D, scale, causal, window_left, window_right, 0, dtype, stream);
+}
+
+fa_status fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Sq, int Sk, int Hq,
+                       int Hkv, int D, float scale, int causal, int window_left, int window_right, int sinks,
+                       fa_dtype dtype, fa_stream_t stream) {
+    return fwd_fixed(q, k, v, o, lse, B, Sq, Sk, Hq, Hkv, D, scale, causal, window_left, window_right, sinks, dtype,
+                     stream);
+}
+
+fa_status fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                        const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
+                        int total_q, int total_k, int Hq, int Hkv, int D, float scale, int causal,
+                        int window_left, int window_right, fa_dtype dtype, fa_stream_t stream) {
+    return fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, B, total_q, total_k, Hq, Hkv, D, scale, causal,
+                      window_left, window_right, 0, dtype, stream);
+}
+
+fa_status fa_fwd_varlen_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int total_q, int total_k,
+                              int Hq, int Hkv, int D, float scale, int causal, int window_left, int window_right,
+                              int sinks, fa_dtype dtype, fa_stream_t stream) {
+    return fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, B, total_q, total_k, Hq, Hkv, D, scale, causal,
+                      window_left, window_right, sinks, dtype, stream);
 }
 
 fa_status fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Sq,

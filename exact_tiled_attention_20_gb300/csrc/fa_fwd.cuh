@@ -27,7 +27,9 @@
 //    where S, P and O of both tiles fit in TMEM side by side, P has columns of its own and
 //    the next S of a tile is issued as soon as the softmax has read the current one.
 //  * Sliding windows (fixed-length batches) use an instantiation that skips, per Q tile,
-//    the blocks outside that tile's window.
+//    the blocks outside that tile's window.  Windows with sinks, first keys that stay visible
+//    left of the window, have instantiations of their own (kSink): the sinks' blocks come first,
+//    then the window's.
 //  * Epilogue: O / l rounded to 16 bits, staged in shared memory in the TMA layout and
 //    written by a store warp with TMA stores (row stores for packed variable-length
 //    batches); LSE = (m + log2 l) ln 2.
@@ -68,6 +70,11 @@ struct FwdParams {
     void* o;           // [B, Sq, Hq, D]
     float* lse;        // [B, Hq, Sq] or null
     int* status;       // sticky device status word
+    // Sinks (the kSink instantiations): keys 0 .. sinks - 1 stay visible left of the window.
+    int sinks;
+    const void* q;  // what the tensor maps are of
+    const void* k;
+    const void* v;
 };
 
 constexpr int kMaxVarlenB = 1024;
@@ -160,13 +167,14 @@ struct FwdConfig {
 
 struct TileCoord {
     int b, h, hk, m0, j0, n_kv;  // K/V blocks j0 .. j0 + n_kv - 1; n_kv < 0: no such tile
+    int ns;                      // kSink: of the n_kv blocks the first ns are 0 .. ns - 1, then j0 ...
     int sq, sk;                  // this sequence's query and key lengths
     int q_base, k_base, tb;      // TMA row offsets and outer coordinate of the sequence
     long long o_row0;            // packed output row of query 0 of this sequence
     long long lse0;              // LSE index of (this sequence, this head, query 0)
 };
 
-template <class C>
+template <class C, bool kSink = false>
 __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const VarlenTable* vt, int t) {
     TileCoord c;
     int qb_raw, bh_local, nqb;
@@ -255,11 +263,23 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
     if (kv_end > kv_begin) {
         c.j0 = (int)(kv_begin / C::BN);
         c.n_kv = (int)((kv_end + C::BN - 1) / C::BN) - c.j0;
+        if constexpr (kSink) {
+            c.ns = min((int)((min((long long)p.sinks, kv_end) + C::BN - 1) / C::BN), c.j0);
+            c.n_kv += c.ns;
+        }
     } else {
         c.j0 = 0;
         c.n_kv = 0;
+        if constexpr (kSink) c.ns = 0;
     }
     return c;
+}
+
+// The K/V block of index j of a tile's n_kv.
+template <bool kSink>
+__device__ __forceinline__ int tile_block(const TileCoord& c, int j) {
+    if constexpr (kSink) return j < c.ns ? j : c.j0 + j - c.ns;
+    return c.j0 + j;
 }
 
 // Blocks [lo, hi] of tile c (indices into its n_kv blocks) that hold a key visible to some
@@ -291,7 +311,87 @@ __device__ __forceinline__ void sub_tile_blocks(const FwdParams& p, const TileCo
     hi = min(hi, (int)(kmax / C::BN) - c.j0);
 }
 
-template <class C, bool kBF16, bool kVarlen, bool kSkip = false>
+// The same with sinks: the keys [kmin, kmax] of the sub-tile's windows (kmax < 0: none).  A block is
+// live if it holds one of them or a sink up to kmax; block 0, the first of every tile, is then
+// live for each sub-tile that sees a key.
+template <class C>
+__device__ __forceinline__ void sub_tile_keys(const FwdParams& p, const TileCoord& c, int q, int& kmin, int& kmax) {
+    const int r0 = c.m0 + q * C::BM;
+    const int r1 = min(r0 + C::BM, c.sq) - 1;
+    const int off = c.sk - c.sq;
+    long long hi = (long long)c.sk - 1;
+    if (p.has_hi) hi = min(hi, (long long)r1 + off + p.hi_off);
+    kmin = (int)max((long long)r0 + off - p.win_left, 0ll);
+    kmax = r0 >= c.sq || hi < 0 ? -1 : (int)hi;
+}
+
+template <class C>
+__device__ __forceinline__ bool sink_live(const FwdParams& p, int block, int kmin, int kmax) {
+    const int n0 = block * C::BN;
+    return n0 <= kmax && (n0 + C::BN > kmin || n0 < p.sinks);
+}
+
+// Bits i of a word with a <= i <= b.
+__device__ __forceinline__ uint32_t bits_between(int a, int b) {
+    a = max(a, 0);
+    b = min(b, 31);
+    return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
+}
+
+// One query row again, by a warp on its own: O[d] = sum of exp2(s scale log2 e - m) v[d] / l over the
+// row's visible keys, which V's infinities and NaNs behind the mask do not reach.  (The product of
+// a block's P, 0 where masked, and V has 0 * inf = NaN there, for the rows that do not see the
+// key.)  The epilogue calls it for rows that came out not finite although l did.  q, k, v: the row,
+// and key 0 of its sequence and head; dims col0 .. col0 + n - 1 go to the staging buffer's row at
+// `stage` (of index rr), or to `out` where that is 0.
+template <int D, int BM, bool kBF16>
+__device__ __noinline__ void sink_row(const uint16_t* q, const uint16_t* k, const uint16_t* v, long long stride,
+                                      int sinks, int lo, int hi, float scale_log2, float m, float inv_l, int col0,
+                                      int n, uint32_t stage, int rr, uint16_t* out) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    auto from16 = [](uint16_t x) -> float {
+        if constexpr (kBF16) return __uint_as_float((uint32_t)x << 16);
+        float f;
+        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(x));
+        return f;
+    };
+    float x[V], o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = from16(q[lane + i * 32]);
+        o[i] = 0.f;
+    }
+    sinks = min(sinks, lo);
+    for (int j = sinks > 0 ? 0 : lo; j <= hi; j = j + 1 == sinks ? lo : j + 1) {
+        const long long at = j * stride + lane;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s = fmaf(x[i], from16(k[at + i * 32]), s);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        const float w = ex2_approx(fmaf(s, scale_log2, -m));
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(w, from16(v[at + i * 32]), o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int col = lane + 32 * i, sc = col - col0;
+        if (sc < 0 || sc >= n) continue;
+        const uint16_t y = (uint16_t)(pack2<kBF16>(o[i] * inv_l, 0.f) & 0xffffu);
+        if (stage)
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage + (uint32_t)(sc / 64) * (BM * 128) +
+                                                          ((((sc % 64) / 8) ^ (rr & 7)) << 4) + (sc % 8) * 2),
+                         "h"(y)
+                         : "memory");
+        else
+            out[col] = y;
+    }
+}
+
+constexpr int kSinkRowKeys = 1 << 20;  // rows that see more keys are not done again (bounded time)
+
+template <class C, bool kBF16, bool kVarlen, bool kSkip = false, bool kSink = false>
 __global__ void __launch_bounds__(C::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -390,7 +490,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             uint32_t kv_it = 0, tcount = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-                const TileCoord c = decode_tile<C>(p, vtab, t);
+                const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 if (c.n_kv <= 0) continue;
                 for (int q = 0; q < C::NQ && ok; ++q) {
                     ok = mbar_wait(bar(C::kBarQEmpty + q), (tcount & 1u) ^ 1u, wc);
@@ -408,7 +508,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     mbar_arrive_expect_tx(bar(C::kBarKFull + st), C::kKVBytes);
                     for (int a = 0; a < C::DA; ++a)
                         tma_load_4d(sK + st * C::kKVBytes + a * (C::BN * 128), &tm_k,
-                                    bar(C::kBarKFull + st), a * 64, c.hk, c.k_base + (c.j0 + j) * C::BN, c.tb);
+                                    bar(C::kBarKFull + st), a * 64, c.hk, c.k_base + tile_block<kSink>(c, j) * C::BN, c.tb);
                     ok = mbar_wait(bar(C::kBarVEmpty + st), ph, wc);
                     if (!ok) {
                         // K of this iteration is in flight: account for it in the drain
@@ -418,7 +518,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     mbar_arrive_expect_tx(bar(C::kBarVFull + st), C::kKVBytes);
                     for (int a = 0; a < C::DA; ++a)
                         tma_load_4d(sV + st * C::kKVBytes + a * (C::BN * 128), &tm_v,
-                                    bar(C::kBarVFull + st), a * 64, c.hk, c.k_base + (c.j0 + j) * C::BN, c.tb);
+                                    bar(C::kBarVFull + st), a * 64, c.hk, c.k_base + tile_block<kSink>(c, j) * C::BN, c.tb);
                     ++kv_it;
                 }
                 ++tcount;
@@ -493,7 +593,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             // awaited exactly once: the S issued after block `it` is that of block it + 1,
             // in this tile or as the first block of the next one.
             for (int t = blockIdx.x; C::kSAhead && t < num_tiles && ok; t += gridDim.x) {
-                const TileCoord c = decode_tile<C>(p, vtab, t);
+                const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 const int n = c.n_kv;
                 if (n <= 0) continue;
                 for (int q = 0; q < C::NQ && ok; ++q) ok = wait(bar(C::kBarQFull + q), tcount & 1u);
@@ -543,7 +643,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 ++tcount;
             }
             for (int t = blockIdx.x; !C::kSAhead && t < num_tiles && ok; t += gridDim.x) {
-                const TileCoord c = decode_tile<C>(p, vtab, t);
+                const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 const int n = c.n_kv;
                 if (n <= 0) continue;
                 for (int q = 0; q < C::NQ && ok; ++q) ok = wait(bar(C::kBarQFull + q), tcount & 1u);
@@ -555,9 +655,15 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 for (int q = 0; q < C::NQ; ++q) {
                     blo[q] = 0;
                     bhi[q] = n - 1;
-                    if (kSkip) sub_tile_blocks<C>(p, c, q, blo[q], bhi[q]);
+                    if (kSkip && kSink)
+                        sub_tile_keys<C>(p, c, q, blo[q], bhi[q]);
+                    else if (kSkip)
+                        sub_tile_blocks<C>(p, c, q, blo[q], bhi[q]);
                 }
-                auto live = [&](int q, int j) -> bool { return !kSkip || (j >= blo[q] && j <= bhi[q]); };
+                auto live = [&](int q, int j) -> bool {
+                    if (kSkip && kSink) return sink_live<C>(p, tile_block<kSink>(c, j), blo[q], bhi[q]);
+                    return !kSkip || (j >= blo[q] && j <= bhi[q]);
+                };
                 {
                     const uint32_t st = kv_it % C::NS;
                     // TMA-filled operands need no tcgen05 fence: the mbarrier wait orders them.
@@ -594,7 +700,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         // the sub-tile's first live block initialises O
-                        if (live(q, j)) issue_pv(q, st, slot_of(q, it), j > (kSkip ? blo[q] : 0));
+                        if (live(q, j)) issue_pv(q, st, slot_of(q, it), j > (kSkip && !kSink ? blo[q] : 0));
                         if (kOPerIter || j + 1 == n) umma_commit_elect(bar(C::kBarODone + q));
                         if (C::NQ > 1 && more) {
                             if (q == 0) {
@@ -634,7 +740,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             uint32_t use = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-                const TileCoord c = decode_tile<C>(p, vtab, t);
+                const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 if (c.n_kv <= 0) continue;
                 for (int q = 0; q < C::NQ && ok; ++q) {
                     for (int rd = 0; rd < L::kStageRounds; ++rd) {
@@ -671,7 +777,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         bool ok = true;
 
         for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-            const TileCoord c = decode_tile<C>(p, vtab, t);
+            const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
             const int row = c.m0 + q * C::BM + r;
             const int off = c.sk - c.sq;  // bottom-right causal alignment
             // Rows are stored only inside the sequence and inside the packed tensor (the
@@ -692,7 +798,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             uint64_t l2 = f2_pack(0.f, 0.f);  // running sum, two interleaved partial sums
             const int tile_row0 = c.m0 + q * C::BM;
             int blo = 0, bhi = c.n_kv - 1;  // this sub-tile's live blocks (kSkip: others skipped)
-            if (kSkip) sub_tile_blocks<C>(p, c, q, blo, bhi);
+            if (kSkip && kSink)
+                sub_tile_keys<C>(p, c, q, blo, bhi);  // its keys
+            else if (kSkip)
+                sub_tile_blocks<C>(p, c, q, blo, bhi);
 
             for (int j = 0; j < c.n_kv; ++j) {
                 const uint32_t slot = (C::NQ == 1) ? (it & 1u) : (uint32_t)q;
@@ -705,7 +814,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     if (it >= C::kVReleaseLag)  // V of an earlier block
                         mbar_arrive(bar(C::kBarVEmpty + (it - C::kVReleaseLag) % C::NS));
                 }
-                if (kSkip && (j < blo || j > bhi)) {  // fully masked for this sub-tile: no S
+                if (kSkip && (kSink ? !sink_live<C>(p, tile_block<kSink>(c, j), blo, bhi) : j < blo || j > bhi)) {  // fully masked for this sub-tile: no S
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::kBarPFull + q));
                     ++it;
@@ -727,11 +836,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     if (lane == 0) mbar_arrive(bar(C::kBarSFree + q));
                 }
 
-                const int n0 = (c.j0 + j) * C::BN;
+                const int n0 = tile_block<kSink>(c, j) * C::BN;
                 const bool need_mask =
                     (n0 + C::BN > c.sk) ||
                     (p.has_hi && (n0 + C::BN - 1 > tile_row0 + off + p.hi_off)) ||
-                    (p.has_lo && (n0 < tile_row0 + C::BM - 1 + off - p.win_left));
+                    (p.has_lo && (n0 < tile_row0 + C::BM - 1 + off - p.win_left) && !(kSink && n0 + C::BN <= p.sinks));
                 // Two ways to mask (both exact).  The general fixed-length kernels compare
                 // and select per score on the integer pipe.  The others (sliding windows,
                 // packed variable-length batches, S ahead of P.V) add 2^126 times a mask
@@ -739,8 +848,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 // 2^126 is about -2^126 for any finite s, and its exponential 0.  The column
                 // and the bounds (clamped to [-1, BN]) are small integers, so t is exactly 0
                 // or 1.  A row with every score of the block masked then has no maximum here.
-                constexpr bool kFmaMask = kSkip || kVarlen || C::kSAhead;
-                if (need_mask) {
+                // With sinks a word holds which of 32 columns the row sees, and the others are replaced:
+                // a NaN of a key behind the mask stays there.
+                constexpr bool kFmaMask = (kSkip || kVarlen || C::kSAhead) && !kSink;
+                if (kSink && need_mask) {
+                    const int kmax = p.has_hi ? min(c.sk - 1, row + off + p.hi_off) : c.sk - 1;
+                    const int kmin = row + off - p.win_left;
+#pragma unroll
+                    for (int ch = 0; ch < kSC; ++ch) {
+                        const int k = n0 + ch * 32;
+                        const uint32_t w = bits_between(kmin - k, kmax - k) | bits_between(-k, min(p.sinks - 1, kmax) - k);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) u[ch][i] = (w >> i) & 1u ? u[ch][i] : 0xff800000u;
+                    }
+                } else if (need_mask) {
                     int kmax = c.sk - 1 - n0;
                     if (p.has_hi) kmax = min(kmax, row + off + p.hi_off - n0);
                     constexpr float kS = 18446744073709551616.0f;    // 2^64
@@ -850,7 +971,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 // NQ == 2: S of this block was issued after the previous P.V of this tile,
                 // so its completion (awaited above) implies that P.V has completed; with
                 // kSAhead that P.V was awaited before the P stores.
-                if (j > (kSkip ? blo : 0) && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                if (j > (kSkip && !kSink ? blo : 0) && __any_sync(0xffffffffu, alpha != 1.0f)) {
 #pragma unroll
                     for (int ch = 0; ch < C::D / 32; ++ch) {
                         uint32_t ov[32];
@@ -877,7 +998,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             float l0, l1;
             f2_unpack(l2, l0, l1);
             const float l_run = l0 + l1;
-            const float inv_l = (l_run > 0.f) ? 1.0f / l_run : 0.f;
+            const bool none = kSink ? l_run == 0.f : !(l_run > 0.f);  // (with sinks a NaN stays one)
+            const float inv_l = none ? 0.f : 1.0f / l_run;
+            const bool blank = kSink ? none : kSkip && !(inv_l > 0.f);
             // O goes through the staging buffer in the TMA layout (128-byte swizzle: 16-byte
             // chunk k of row r sits at chunk k ^ (r % 8)) and the store warp writes it; rows
             // past Sq are clipped by the tensor map.  Sub-tiles that are not staged (partial
@@ -897,12 +1020,20 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             };
             // 32 columns of this row (from TMEM, fp32) -> bf16/fp16, into the staging buffer
             // or out to global memory.  col is the first column within the row.
+            bool odd = false;  // kSink: a value of this row is not finite
             auto put_chunk = [&](int col, const uint32_t (&ov)[32]) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)  // kSkip: a sub-tile that saw no key left O unwritten
-                    w[i] = pack2<kBF16>(kSkip && !(inv_l > 0.f) ? 0.f : __uint_as_float(ov[2 * i]) * inv_l,
-                                        kSkip && !(inv_l > 0.f) ? 0.f : __uint_as_float(ov[2 * i + 1]) * inv_l);
+                    w[i] = pack2<kBF16>(blank ? 0.f : __uint_as_float(ov[2 * i]) * inv_l,
+                                        blank ? 0.f : __uint_as_float(ov[2 * i + 1]) * inv_l);
+                if constexpr (kSink) {
+                    constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+                    uint32_t carry = 0;  // a half at or past kInf carries into its top bit
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) carry |= (w[i] & 0x7fff7fffu) + (0x8000u - kInf) * 0x10001u;
+                    odd |= (carry & 0x80008000u) != 0;
+                }
                 if (use_stage) {
                     const int sc = col % (L::kStageAtoms * 64);  // column within the staged round
                     const uint32_t rowb = sStage + (uint32_t)(sc / 64) * (C::BM * 128) + (uint32_t)r * 128;
@@ -917,6 +1048,29 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     for (int v4 = 0; v4 < 4; ++v4)
                         st_global_v4(orow + col + v4 * 8, w[4 * v4], w[4 * v4 + 1], w[4 * v4 + 2],
                                      w[4 * v4 + 3]);
+                }
+            };
+            // kSink: rows that are not finite again (sink_row), into the staging buffer, whose round
+            // holds columns col0 .. col0 + n - 1, or out to global memory.
+            auto mend_rows = [&](int col0, int n) {
+                if constexpr (kSink) {
+                    const bool again = odd && row_ok && l_run > 0.f && l_run < __int_as_float(0x7f800000) &&
+                                       (long long)min(c.sk, p.win_left) + p.sinks <= kSinkRowKeys;
+                    uint32_t todo = __ballot_sync(0xffffffffu, again);
+                    while (todo) {
+                        const int from = __ffs((int)todo) - 1, at = row - lane + from, rr = r - lane + from;
+                        todo &= todo - 1;
+                        const long long q0 = ((c.o_row0 + at) * p.Hq + c.h) * C::D;
+                        const long long k0 = ((p.cu_q ? (long long)c.k_base : (long long)c.b * p.Sk) * p.Hkv + c.hk) * C::D;
+                        sink_row<C::D, C::BM, kBF16>(
+                            static_cast<const uint16_t*>(p.q) + q0, static_cast<const uint16_t*>(p.k) + k0,
+                            static_cast<const uint16_t*>(p.v) + k0, (long long)p.Hkv * C::D, p.sinks,
+                            (int)max((long long)at + off - p.win_left, 0ll),
+                            p.has_hi ? (int)min((long long)c.sk - 1, (long long)at + off + p.hi_off) : c.sk - 1,
+                            p.scale_log2, __shfl_sync(0xffffffffu, m_run, from), __shfl_sync(0xffffffffu, inv_l, from),
+                            col0, n, use_stage ? sStage + (uint32_t)rr * 128 : 0u, rr, static_cast<uint16_t*>(p.o) + q0);
+                    }
+                    __syncwarp();
                 }
             };
             constexpr int kChunksPerRound = L::kStageAtoms * 2;  // 32-column chunks per round
@@ -940,6 +1094,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         if (!ok) break;
                     }
                     put_chunk(ch * 32, ov[ch]);
+                    if (kSink && ch == C::D / 32 - 1) {  // one round holds the row
+                        __syncwarp();
+                        mend_rows(0, C::D);
+                    }
                     if (use_stage && (ch % kChunksPerRound == kChunksPerRound - 1 || ch == C::D / 32 - 1))
                         stage_done();
                 }
@@ -956,6 +1114,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     tmem_ld_32x32b_x32(tO + ch * 32, ov);
                     tmem_wait_ld(ov);
                     put_chunk(ch * 32, ov);
+                    if (kSink && (ch % kChunksPerRound == kChunksPerRound - 1 || ch == C::D / 32 - 1)) {
+                        __syncwarp();
+                        mend_rows(ch / kChunksPerRound * kChunksPerRound * 32, kChunksPerRound * 32);
+                        odd = false;
+                    }
                     if (use_stage && (ch % kChunksPerRound == kChunksPerRound - 1 || ch == C::D / 32 - 1))
                         stage_done();
                 }
@@ -965,8 +1128,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(C::kBarODrained + q));
             }
             if (p.lse && row_ok) {
-                const float lse = (l_run > 0.f) ? (m_run + lg2_approx(l_run)) * 0.69314718055994531f
-                                                : kNegInf;
+                const float lse = none ? kNegInf : (m_run + lg2_approx(l_run)) * 0.69314718055994531f;
                 p.lse[c.lse0 + row] = lse;
             }
         }
@@ -1009,8 +1171,8 @@ inline bool causal_pairs_balance_better(long long heads, int nqb, int sms) {
     return max_pr < max_rr;
 }
 
-// Host launcher for one configuration.
-template <class C>
+// Host launcher for one configuration; kSink: with sinks, a window on the left and sinks > 0.
+template <class C, bool kSink = false>
 fa_status launch_fwd_cfg(const FwdArgs& a, cudaStream_t stream) {
     static int attr_bf16[64] = {0};
     static int attr_f16[64] = {0};
@@ -1074,23 +1236,40 @@ fa_status launch_fwd_cfg(const FwdArgs& a, cudaStream_t stream) {
     p.o = a.o;
     p.lse = a.lse;
     p.status = a.dev_status;
-    auto kern = varlen ? (a.bf16 ? fa_fwd_kernel<C, true, true> : fa_fwd_kernel<C, false, true>)
-                       : (a.bf16 ? fa_fwd_kernel<C, true, false> : fa_fwd_kernel<C, false, false>);
-    // Fixed-length sliding windows take the instantiation that skips a sub-tile's blocks
-    // outside its window (two Q tiles with P over S only).
-    bool skip = false;
-    if constexpr (C::NQ == 2 && !C::kSAhead) {
-        if (!varlen && a.window_left >= 0) {
-            kern = a.bf16 ? fa_fwd_kernel<C, true, false, true> : fa_fwd_kernel<C, false, false, true>;
-            skip = true;
+    p.sinks = a.sinks;
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    if constexpr (kSink) {
+        // Two Q tiles with P over S skip a sub-tile's blocks, packed batches too.
+        constexpr bool kSkip = C::NQ == 2 && !C::kSAhead;
+        auto kern = varlen ? (a.bf16 ? fa_fwd_kernel<C, true, true, kSkip, true> : fa_fwd_kernel<C, false, true, kSkip, true>)
+                           : (a.bf16 ? fa_fwd_kernel<C, true, false, kSkip, true>
+                                     : fa_fwd_kernel<C, false, false, kSkip, true>);
+        const int smem = varlen ? C::template Layout<true>::kSmemBytes : C::template Layout<false>::kSmemBytes;
+        int* flags = varlen ? (a.bf16 ? attr_bf16_v : attr_f16_v) : (a.bf16 ? attr_bf16 : attr_f16);
+        if (!ensure_smem_attr((const void*)kern, smem, flags)) return FA_ERR_CUDA;
+        kern<<<grid, C::kThreads, smem, stream>>>(tq, tk, tv, to, p);
+        return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    } else {
+        auto kern = varlen ? (a.bf16 ? fa_fwd_kernel<C, true, true> : fa_fwd_kernel<C, false, true>)
+                           : (a.bf16 ? fa_fwd_kernel<C, true, false> : fa_fwd_kernel<C, false, false>);
+        // Fixed-length sliding windows take the instantiation that skips a sub-tile's blocks
+        // outside its window (two Q tiles with P over S only).
+        bool skip = false;
+        if constexpr (C::NQ == 2 && !C::kSAhead) {
+            if (!varlen && a.window_left >= 0) {
+                kern = a.bf16 ? fa_fwd_kernel<C, true, false, true> : fa_fwd_kernel<C, false, false, true>;
+                skip = true;
+            }
         }
+        const int smem = varlen ? C::template Layout<true>::kSmemBytes : C::template Layout<false>::kSmemBytes;
+        int* flags = varlen ? (a.bf16 ? attr_bf16_v : attr_f16_v)
+                            : skip ? (a.bf16 ? attr_bf16_s : attr_f16_s) : (a.bf16 ? attr_bf16 : attr_f16);
+        if (!ensure_smem_attr((const void*)kern, smem, flags)) return FA_ERR_CUDA;
+        kern<<<grid, C::kThreads, smem, stream>>>(tq, tk, tv, to, p);
+        return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
-    const int smem = varlen ? C::template Layout<true>::kSmemBytes : C::template Layout<false>::kSmemBytes;
-    int* flags = varlen ? (a.bf16 ? attr_bf16_v : attr_f16_v)
-                        : skip ? (a.bf16 ? attr_bf16_s : attr_f16_s) : (a.bf16 ? attr_bf16 : attr_f16);
-    if (!ensure_smem_attr((const void*)kern, smem, flags)) return FA_ERR_CUDA;
-    kern<<<grid, C::kThreads, smem, stream>>>(tq, tk, tv, to, p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace fa

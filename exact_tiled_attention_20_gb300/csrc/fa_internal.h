@@ -68,6 +68,12 @@ fa_status launch_fwd_d96(const FwdArgs& a, cudaStream_t s);
 fa_status launch_fwd_d128(const FwdArgs& a, cudaStream_t s);
 fa_status launch_fwd_d256(const FwdArgs& a, cudaStream_t s);
 
+// With a window on the left and sinks > 0.
+fa_status launch_sinks_d64(const FwdArgs& a, cudaStream_t s);
+fa_status launch_sinks_d96(const FwdArgs& a, cudaStream_t s);
+fa_status launch_sinks_d128(const FwdArgs& a, cudaStream_t s);
+fa_status launch_sinks_d256(const FwdArgs& a, cudaStream_t s);
+
 fa_status launch_decode(const DecodeArgs& a, cudaStream_t s);
 fa_status launch_decode_d64(const DecodeArgs& a, cudaStream_t s);
 fa_status launch_decode_d96(const DecodeArgs& a, cudaStream_t s);

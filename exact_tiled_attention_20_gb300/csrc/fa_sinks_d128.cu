@@ -1,0 +1,10 @@
+// fa_sinks_d128.cu -- forward kernel instantiations with sinks for head dim 128; tiles as without.
+#include "fa_fwd.cuh"
+
+namespace fa {
+
+fa_status launch_sinks_d128(const FwdArgs& a, cudaStream_t s) {
+    return launch_fwd_cfg<FwdConfig<128, 128, 2, 2>, true>(a, s);
+}
+
+}  // namespace fa

@@ -116,6 +116,29 @@ FA_API fa_status fa_fwd_varlen(const void *q, const void *k, const void *v, void
                                fa_stream_t stream);
 
 /*
+ * fa_fwd_window and fa_fwd_varlen with sinks: the first `sinks` keys of a sequence stay visible
+ * left of the window.  Query i sees the keys j with
+ *     j <= i + Sk - Sq + window_right  (the right side as without sinks), and
+ *     j >= i + Sk - Sq - window_left  or  j < sinks.
+ * Blocks of keys between the sinks and every row's window are skipped.  What a row does not see is
+ * not used for it, NaN and infinities included (rows that see over 2^20 keys excepted, where an
+ * infinity or NaN in V of a key that other rows of their block see gives NaN).  sinks >= 0, else
+ * FA_ERR_INVALID_ARG.  Where the sinks do not matter (sinks == 0, or window_left == -1 or at least
+ * the keys) the call is fa_fwd_window (fa_fwd_varlen); everything else as there.
+ */
+FA_API fa_status fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
+                              int B, int Sq, int Sk, int Hq, int Hkv, int D, float scale,
+                              int causal, int window_left, int window_right, int sinks,
+                              fa_dtype dtype, fa_stream_t stream);
+
+FA_API fa_status fa_fwd_varlen_sinks(const void *q, const void *k, const void *v, void *o,
+                                     float *lse, const int32_t *cu_seqlens_q,
+                                     const int32_t *cu_seqlens_k, int B, int total_q, int total_k,
+                                     int Hq, int Hkv, int D, float scale, int causal,
+                                     int window_left, int window_right, int sinks, fa_dtype dtype,
+                                     fa_stream_t stream);
+
+/*
  * Bytes of decode workspace fa_decode_splitkv needs for these sizes and `num_splits`
  * (the partial outputs [B, Hq, num_splits, D] fp32 and their log-sum-exps
  * [B, Hq, num_splits] fp32, each region 256-byte aligned).  0 for invalid sizes.
