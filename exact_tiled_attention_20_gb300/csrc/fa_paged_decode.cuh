@@ -17,8 +17,10 @@
 // against some 2800 for 64 KB at an SM's share of the bandwidth), so it is the bytes that bound
 // the kernel for anything up to about 256 rows.
 //
-// Plan: the visible key tiles of a sequence are counted as units, those of the sinks first and
-// then those from the first token's window on; the units of all entries (sequence, group of kv
+// A tile is BN keys of the sequence's visible ones, in strips of 32: the strips of the sinks, then
+// those from the first token's window on.  Strips that hold no visible key are not read.
+//
+// Plan: a sequence's tiles are counted as units; the units of all entries (sequence, group of kv
 // heads), each led by kPagedLead units for what starting and finishing one costs, lie end to end
 // and are cut into equal ranges.  A range is worked on by G CTAs, one for each head of the group
 // (and for each row block, where there are few): they read the same keys at about the same time,
@@ -106,25 +108,25 @@ __device__ __forceinline__ int paged_len(const PagedDecParams& p, int b) {
     return min(max(__ldcg(p.kv_lens + b), 0), p.capacity);
 }
 
-// The visible tiles of a sequence: tiles 0 .. sink_tiles - 1 and first .. last.
-struct PagedTiles {
-    int sink_tiles, first, count;
-    __device__ __forceinline__ int tile(int u) const { return u < sink_tiles ? u : first + u - sink_tiles; }
+// The strips of 32 keys of a sequence that may be visible: 0 .. sinks - 1 and first, first + 1, ...
+struct PagedStrips {
+    int sinks, first;
+    // First key of strip i of the tiles; behind the last visible one it is past the sequence's keys.
+    __device__ __forceinline__ int key(int i) const { return (i < sinks ? i : first + i - sinks) * 32; }
 };
 
-template <int BN>
-__device__ __forceinline__ PagedTiles paged_tiles(const PagedDecParams& p, int len) {
-    PagedTiles t;
-    t.first = p.window_left >= 0 ? max(len - p.Sq - p.window_left, 0) / BN : 0;
-    t.sink_tiles = min((min(p.sinks, len) + BN - 1) / BN, t.first);
-    t.count = len > 0 ? t.sink_tiles + (len + BN - 1) / BN - t.first : 0;
+__device__ __forceinline__ PagedStrips paged_strips(const PagedDecParams& p, int len) {
+    PagedStrips t;
+    t.first = p.window_left >= 0 ? max(len - p.Sq - p.window_left, 0) / 32 : 0;
+    t.sinks = min((min(p.sinks, len) + 31) / 32, t.first);
     return t;
 }
 
 template <int BN>
 __device__ __forceinline__ int paged_units(const PagedDecParams& p, int len) {
-    const int n = paged_tiles<BN>(p, len).count;
-    return n > 0 ? n + kPagedLead : 0;
+    if (len <= 0) return 0;
+    const PagedStrips t = paged_strips(p, len);
+    return (t.sinks + (len + 31) / 32 - t.first + BN / 32 - 1) / (BN / 32) + kPagedLead;
 }
 
 // Units of a range, from the units of one entry of each sequence summed.
@@ -145,8 +147,8 @@ __device__ __forceinline__ int paged_slot(const PagedDecParams& p, int r, bool f
 
 struct PagedSeg {
     int b, hk, rb, len;
-    int u0, u1;  // its visible tiles u0 .. u1 - 1
-    PagedTiles tiles;
+    int u0, u1;  // its tiles u0 .. u1 - 1
+    PagedStrips strips;
     int slot;
     bool cut;
 };
@@ -201,7 +203,7 @@ struct PagedWalk {
             s.hk = e / blocks * p.g + member % p.g;
             s.rb = e % blocks * p.rg + member / p.g;
             s.len = len[b];
-            s.tiles = paged_tiles<BN>(p, s.len);
+            s.strips = paged_strips(p, s.len);
             s.u0 = max(x - start - kPagedLead, 0);
             s.u1 = end - start - kPagedLead;
             s.slot = paged_slot(p, rng, rng == paged_first_piece(start, W));
@@ -243,12 +245,11 @@ __device__ __forceinline__ uint32_t paged_sees(const PagedDecParams& p, int b, i
     return w | paged_bits(0, min(p.sinks - 1, last) - k);
 }
 
-// Whether the tile of keys n0 .. n0 + BN - 1 hides a key from some token.
-template <int BN>
-__device__ __forceinline__ bool paged_masked(const PagedDecParams& p, int len, int n0) {
+// Whether one of the 32 keys from k on is hidden from some token.
+__device__ __forceinline__ bool paged_masked(const PagedDecParams& p, int len, int k) {
     const int ctx = len - p.Sq;
-    if (p.tree) return n0 + BN > ctx;
-    return n0 + BN - 1 > ctx || (p.window_left >= 0 && n0 < len - 1 - p.window_left && n0 + BN > p.sinks);
+    if (p.tree) return k + 32 > ctx;
+    return k + 31 > ctx || (p.window_left >= 0 && k < len - 1 - p.window_left && k + 32 > p.sinks);
 }
 
 // Whether one of a word's 16-bit values is an infinity or NaN.
@@ -382,7 +383,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
         };
         auto fetch = [&](const PagedSeg& sg, int u) -> int2 {
             u += ahead;
-            const int key = u < sg.u1 ? sg.tiles.tile(u) * BN + box * p.box_rows : sg.len;
+            const int row = box * p.box_rows;
+            const int key = u < sg.u1 ? sg.strips.key(u * (BN / 32) + row / 32) + row % 32 : sg.len;
             return key < sg.len ? paged_place(p, sg.b, key) : make_int2(-1, 0);
         };
         auto issue = [&](const CUtensorMap* map, int hk, int page, int row) -> bool {
@@ -576,26 +578,37 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
             float m_run = kNegInf;
             uint64_t l2 = f2_pack(0.f, 0.f);
             for (int j = 0; j < n; ++j) {
-                const int n0 = s.tiles.tile(s.u0 + j) * BN;
-                const bool masked = paged_masked<BN>(p, s.len, n0);
+                int key[kSC];       // first key of each strip of the tile
+                uint32_t masked = 0;  // bit ch: strip ch hides a key from some token
+#pragma unroll
+                for (int ch = 0; ch < kSC; ++ch) {
+                    key[ch] = s.strips.key((s.u0 + j) * kSC + ch);
+                    masked |= paged_masked(p, s.len, key[ch]) ? 1u << ch : 0u;
+                }
                 if (masked && q == 0) {
-                    // V's values that are not finite give way to zeros, the warpgroup's threads
-                    // taking 16 bytes each in turn.
+                    // V's values that are not finite give way to zeros in those strips, the warpgroup's
+                    // threads taking 16 bytes each in turn.
                     const uint32_t load = 2 * it + 1, at = sRing + (load % NB) * C::kTileBytes;
                     ok = mbar_wait(bar(C::kBarFull + load % NB), (load / NB) & 1u, wc);
                     if (!ok) break;
                     bool odd = false;
-                    for (int i = r; i < C::kTileBytes / 16; i += 128) {
-                        uint32_t w[4];
-                        lds128(at + i * 16, w);
-                        if (paged_nonfinite<kBF16>(w[0]) | paged_nonfinite<kBF16>(w[1]) | paged_nonfinite<kBF16>(w[2]) |
-                            paged_nonfinite<kBF16>(w[3])) {
-                            odd = true;
+#pragma unroll 1
+                    for (int ch = 0; ch < kSC; ++ch) {
+                        if (!(masked >> ch & 1u)) continue;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] &= (paged_nonfinite<kBF16>(w[k] & 0xffffu) ? 0u : 0xffffu) |
-                                        (paged_nonfinite<kBF16>(w[k] & 0xffff0000u) ? 0u : 0xffff0000u);
-                            st_shared_v4(at + i * 16, w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 2 * DA; ++i) {  // 32 rows of an atom are 4096 bytes
+                            const uint32_t a = at + (i >> 1) * (BN * 128) + ch * 4096 + (i & 1) * 2048 + r * 16;
+                            uint32_t w[4];
+                            lds128(a, w);
+                            if (paged_nonfinite<kBF16>(w[0]) | paged_nonfinite<kBF16>(w[1]) |
+                                paged_nonfinite<kBF16>(w[2]) | paged_nonfinite<kBF16>(w[3])) {
+                                odd = true;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] &= (paged_nonfinite<kBF16>(w[k] & 0xffffu) ? 0u : 0xffffu) |
+                                            (paged_nonfinite<kBF16>(w[k] & 0xffff0000u) ? 0u : 0xffff0000u);
+                                st_shared_v4(a, w[0], w[1], w[2], w[3]);
+                            }
                         }
                     }
                     if (odd) odd_seg[tcount & 1u] = (int)tcount + 1;
@@ -618,7 +631,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                     if (masked) {
 #pragma unroll
                         for (int ch = 0; ch < kSC; ++ch) {
-                            const uint32_t w = live ? paged_sees(p, s.b, tok, s.len, n0 + ch * 32) : 0u;
+                            if (!(masked >> ch & 1u)) continue;
+                            const uint32_t w = live ? paged_sees(p, s.b, tok, s.len, key[ch]) : 0u;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) u[ch][i] = (w >> i) & 1u ? u[ch][i] : 0xff800000u;
                         }
@@ -710,16 +724,17 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                     if (live) {
                         if (odd) {
                             // What was taken out of V, to the rows that see it (rare: one copy of the code).
-                            for (int u = s.u0; u < s.u1; ++u) {
-                                const int n0 = s.tiles.tile(u) * BN;
-                                if (!paged_masked<BN>(p, s.len, n0)) continue;
-                                for (int c = 0; c < BN; ++c) {
-                                    if (!(paged_sees(p, s.b, tok, s.len, n0 + c) & 1u)) continue;
-                                    const int2 at = paged_place(p, s.b, n0 + c);
+                            for (int i = s.u0 * kSC; i < s.u1 * kSC; ++i) {
+                                const int k = s.strips.key(i);
+                                if (!paged_masked(p, s.len, k)) continue;
+                                const uint32_t sees = paged_sees(p, s.b, tok, s.len, k);
+                                for (int c = 0; c < 32; ++c) {
+                                    if (!(sees >> c & 1u)) continue;
+                                    const int2 at = paged_place(p, s.b, k + c);
                                     if (at.x < 0) continue;
                                     const uint16_t* v = p.v_pages +
                                                         (((size_t)at.x * p.page_size + at.y) * p.Hkv + s.hk) * D + ch * 32;
-    #pragma unroll
+#pragma unroll
                                     for (int i = 0; i < 32; ++i) {
                                         const uint32_t x = v[i];
                                         if (paged_nonfinite<kBF16>(x))
@@ -728,19 +743,19 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                                 }
                             }
                         }
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 32; ++i) ov[i] = none ? 0u : __float_as_uint(__uint_as_float(ov[i]) * inv_l);
                         if (s.cut) {
                             float* to = p.o_part + part * D + ch * 32;
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 32; i += 4) st_global_v4(to + i, ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
                         } else {
                             uint32_t w[16];
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 w[i] = pack2<kBF16>(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1]));
                             uint16_t* to = o16 + row * D + ch * 32;
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 st_global_v4(to + i * 8, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                         }
@@ -819,8 +834,12 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p
     for (int c0 = part; c0 < n; c0 += WPR * NP) {
         float w[NP], v[NP][V], top = m;
 #pragma unroll
-        for (int u = 0; u < NP; ++u) {  // pieces past n: the last one, with weight 0
-            const int c = min(c0 + u * WPR, n - 1);
+        for (int u = 0; u < NP; ++u) {
+            const int c = c0 + u * WPR;
+            w[u] = kNegInf;
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[u][i] = 0.f;
+            if (c >= n) continue;
             const size_t at =
                 ((size_t)member * 2 * p.ranges + paged_slot(p, first + c, c == 0)) * block_rows + in_block;
             w[u] = p.lse_part[at];
@@ -828,10 +847,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p
             for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
         }
 #pragma unroll
-        for (int u = 0; u < NP; ++u) {
-            if (c0 + u * WPR >= n) w[u] = kNegInf;
-            top = fmaxf(top, w[u]);
-        }
+        for (int u = 0; u < NP; ++u) top = fmaxf(top, w[u]);
         const float ref = top == kNegInf ? 0.f : top;
         const float f = ex2_approx((m - ref) * (1.f / kPagedLn2));
         m = top;
@@ -842,9 +858,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p
         for (int u = 0; u < NP; ++u) {
             const float x = ex2_approx((w[u] - ref) * (1.f / kPagedLn2));
             s += x;
-            // a weight of 0 must not meet a NaN or an infinity of a piece read twice
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(x, w[u] == kNegInf ? 0.f : v[u][i], acc[i]);
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(x, v[u][i], acc[i]);
         }
     }
     if constexpr (WPR > 1) {
@@ -927,7 +942,9 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     p.entries = a.Hkv / p.g * (p.row_blocks / p.rg);
     p.capacity = a.page_size * a.max_pages;
     p.page_size = a.page_size, p.num_pages = a.num_pages, p.max_pages = a.max_pages;
-    p.box_rows = std::min(a.page_size & -a.page_size, C::BN);
+    // Rows of a copy: a tile's where its keys lie side by side, a strip's where a window may begin with
+    // any of them; and the power of two that a page is made of.
+    p.box_rows = std::min(a.page_size & -a.page_size, a.window_left >= 0 ? 32 : C::BN);
     p.page_recip = (unsigned)((1ull << 32) / (unsigned)a.page_size) + 1u;
     p.window_left = a.window_left, p.sinks = a.sinks;
     p.words = (a.Sq + 31) / 32;
@@ -937,10 +954,10 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     p.v_pages = static_cast<const uint16_t*>(a.v_pages);
     p.status = a.dev_status;
     // The most tiles that a sequence can have.
-    long long most = (p.capacity + C::BN - 1) / C::BN;
+    long long strips = ((long long)p.capacity + 31) / 32;
     if (a.window_left >= 0)
-        most = std::min(most, ((long long)a.window_left + a.Sq + C::BN - 1) / C::BN + 1 +
-                                  ((long long)a.sinks + C::BN - 1) / C::BN);
+        strips = std::min(strips, ((long long)a.window_left + a.Sq + 31) / 32 + 1 + ((long long)a.sinks + 31) / 32);
+    const long long most = (strips + C::BN / 32 - 1) / (C::BN / 32);
     const long long units = (most + kPagedLead) * p.entries * a.B;  // of all entries at most
     if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     p.whole = most + kPagedLead <= kPagedMinWidth ? 1 : 0;
