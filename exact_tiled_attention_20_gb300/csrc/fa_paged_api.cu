@@ -75,8 +75,9 @@ fa_status decode(const void* q, const void* k_pages, const void* v_pages, const 
     if (window_left >= capacity) window_left = -1;
     if (sinks > capacity) sinks = capacity;
     const size_t rows = (size_t)(2LL * sms * part_rows(Sq, Hq, Hkv));
-    float* o_part = static_cast<float*>(workspace);
-    float* lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * D * sizeof(float)));
+    char* part = static_cast<char*>(workspace) + (misaligned(workspace, 32) ? 16 : 0);
+    float* o_part = reinterpret_cast<float*>(part);
+    float* lse_part = reinterpret_cast<float*>(part + up256(rows * D * sizeof(float)));
     const PagedDecodeArgs a{q, k_pages, v_pages, block_table, kv_lens, tree, o, lse, B, Sq, Hq, Hkv, D, num_pages,
                             page_size, max_pages, scale, window_left, sinks, o_part, lse_part, dtype == FA_BF16, sms,
                             status};
@@ -149,7 +150,7 @@ size_t fa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, in
         if (!current_device(&num_sms, &status)) return 0;
     }
     const size_t rows = (size_t)(2LL * num_sms * part_rows(Sq, Hq, Hkv));
-    return up256(rows * D * sizeof(float)) + up256(rows * sizeof(float));
+    return up256(rows * D * sizeof(float)) + up256(rows * sizeof(float)) + 16;  // 16: to a 32-byte boundary
 }
 
 fa_status fa_decode_splitkv_paged_tree(const void* q, const void* k_pages, const void* v_pages,

@@ -49,9 +49,10 @@ struct PagedDecParams {
     int T;               // query tokens of a sub-tile
     int row_blocks;      // of a (sequence, kv head)
     int g, rg;           // heads and row blocks of an entry: G = g * rg CTAs work on a range
-    int entries;         // of a sequence
+    int groups, blocks;  // entries of a sequence: groups of heads, by row blocks over rg
     int ranges, whole;   // whole: entries are not cut, a range has those that begin in it
     int capacity, page_size, num_pages, max_pages, box_rows;
+    int nb_log;           // log2 of the boxes of a tile, BN / box_rows
     unsigned page_recip;  // floor(2^32 / page_size) + 1
     int window_left, sinks;
     int words;            // of a token's tree mask
@@ -131,7 +132,7 @@ __device__ __forceinline__ int paged_units(const PagedDecParams& p, int len) {
 
 // Units of a range, from the units of one entry of each sequence summed.
 __device__ __forceinline__ int paged_width(const PagedDecParams& p, int sum_units) {
-    const unsigned total = (unsigned)sum_units * (unsigned)p.entries;
+    const unsigned total = (unsigned)sum_units * (unsigned)(p.groups * p.blocks);
     return max((int)((total + (unsigned)p.ranges - 1u) / (unsigned)p.ranges), kPagedMinWidth);
 }
 
@@ -153,44 +154,52 @@ struct PagedSeg {
     bool cut;
 };
 
-// Walks the segments of one range.
+// Walks the segments of one range; no division but at its start.
 struct PagedWalk {
     const int* len;     // [B]
     const int* prefix;  // [B + 1], of the units of one entry
-    int x, x_end, b, e, start, units, rng, W;
+    int x0, W, x, x_end, rng;
+    int b, group, block, start, units;  // the entry that holds unit x, or ends there
+    int head, sub;                      // this CTA's head of the group and row block of the entry
 
-    template <int BN>
-    __device__ __forceinline__ void init(const PagedDecParams& p, const int* len_, const int* prefix_, int rng_) {
+    __device__ __forceinline__ void init(const PagedDecParams& p, const int* len_, const int* prefix_, int rng_,
+                                         int member) {
         len = len_;
         prefix = prefix_;
         rng = rng_;
+        head = member & (p.g - 1);
+        sub = member / p.g;
+        const int entries = p.groups * p.blocks, total = prefix[p.B] * entries;
         W = paged_width(p, prefix[p.B]);
-        const int total = prefix[p.B] * p.entries;
-        x = (int)min((long long)rng * W, (long long)total);
+        x = x0 = (int)min((long long)rng * W, (long long)total);
         x_end = (int)min((long long)x + W, (long long)total);
         if (x >= x_end) return;
         int lo = 0, hi = p.B;  // largest b with entries * prefix[b] <= x: it has keys
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (p.entries * prefix[mid] <= x) lo = mid; else hi = mid;
+            if (entries * prefix[mid] <= x) lo = mid; else hi = mid;
         }
         b = lo;
         units = prefix[lo + 1] - prefix[lo];
-        e = (x - p.entries * prefix[lo]) / units;
-        start = p.entries * prefix[lo] + e * units;
+        const int e = entries == 1 ? 0 : (int)((unsigned)(x - entries * prefix[lo]) / (unsigned)units);
+        start = entries * prefix[lo] + e * units;
+        group = p.blocks == 1 ? e : e / p.blocks;
+        block = e - group * p.blocks;
     }
 
-    template <int BN>
-    __device__ __forceinline__ bool next(const PagedDecParams& p, int member, PagedSeg& s) {
+    __device__ __forceinline__ bool next(const PagedDecParams& p, PagedSeg& s) {
         while (x < x_end) {
             if (x >= start + units) {
                 start += units;
-                if (++e == p.entries) {
-                    e = 0;
-                    do {
-                        ++b;
-                        units = prefix[b + 1] - prefix[b];
-                    } while (units == 0);
+                if (++block == p.blocks) {
+                    block = 0;
+                    if (++group == p.groups) {
+                        group = 0;
+                        do {
+                            ++b;
+                            units = prefix[b + 1] - prefix[b];
+                        } while (units == 0);
+                    }
                 }
             }
             if (p.whole && x > start) {  // the range before has it
@@ -198,16 +207,16 @@ struct PagedWalk {
                 continue;
             }
             const int end = p.whole ? start + units : min(x_end, start + units);
-            const int blocks = p.row_blocks / p.rg;  // entries of one group of heads
+            const bool first = start + kPagedLead >= x0;  // its first keys are this range's
             s.b = b;
-            s.hk = e / blocks * p.g + member % p.g;
-            s.rb = e % blocks * p.rg + member / p.g;
+            s.hk = group * p.g + head;
+            s.rb = block * p.rg + sub;
             s.len = len[b];
             s.strips = paged_strips(p, s.len);
             s.u0 = max(x - start - kPagedLead, 0);
             s.u1 = end - start - kPagedLead;
-            s.slot = paged_slot(p, rng, rng == paged_first_piece(start, W));
-            s.cut = !p.whole && paged_pieces(start, units, W) > 1;
+            s.slot = paged_slot(p, rng, first);
+            s.cut = !p.whole && !(first && start + units <= x0 + W);
             x = end;
             if (s.u1 > s.u0) return true;  // else the range ends within the lead
         }
@@ -245,11 +254,19 @@ __device__ __forceinline__ uint32_t paged_sees(const PagedDecParams& p, int b, i
     return w | paged_bits(0, min(p.sinks - 1, last) - k);
 }
 
-// Whether one of the 32 keys from k on is hidden from some token.
-__device__ __forceinline__ bool paged_masked(const PagedDecParams& p, int len, int k) {
-    const int ctx = len - p.Sq;
-    if (p.tree) return k + 32 > ctx;
-    return k + 31 > ctx || (p.window_left >= 0 && k < len - 1 - p.window_left && k + 32 > p.sinks);
+// The strips lo .. hi - 1 of a sequence's tiles hide no key from any token (some of the sinks' may
+// not either, and are masked all the same).
+struct PagedClear {
+    int lo, hi;
+    __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
+};
+
+__device__ __forceinline__ PagedClear paged_clear(const PagedDecParams& p, int len, const PagedStrips& t) {
+    const int ctx = len - p.Sq;  // keys up to ctx (of a tree: before it) are seen by all, windows aside
+    PagedClear c;
+    c.lo = p.window_left >= 0 ? (max(len - 1 - p.window_left, 0) + 31) / 32 - t.first + t.sinks : 0;
+    c.hi = max(p.tree ? ctx : ctx + 1, 0) / 32 - t.first + t.sinks;
+    return c;
 }
 
 // Whether one of a word's 16-bit values is an infinity or NaN.
@@ -268,6 +285,13 @@ __device__ __forceinline__ float paged_from16(uint32_t x) {
         asm("{\n.reg .b16 a;\ncvt.u16.u32 a, %1;\ncvt.f32.f16 %0, a;\n}" : "=f"(f) : "r"(x));
         return f;
     }
+}
+
+// 32 bytes to a 32-byte boundary: whole sectors, where each lane writes to a row of its own.
+__device__ __forceinline__ void st_global_v8(void* p, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 
 // Page and row within it of key `key` of sequence b; page -1: none.
@@ -318,10 +342,38 @@ __device__ __forceinline__ void paged_make_plan(const PagedDecParams& p, int* le
     __syncthreads();
 }
 
+// Adds V's values that were taken out of a segment's product to a row that it was written to, where
+// the row's token sees them.  (An infinity or NaN is the sum that it is in, whatever its weight.)
+template <int D, int BN, bool kBF16>
+__device__ __noinline__ void paged_add_odd(const PagedDecParams& p, int b, int hk, int len, int tok, int u0, int u1,
+                                           float* part, uint16_t* out) {
+    const PagedStrips strips = paged_strips(p, len);
+    const PagedClear clear = paged_clear(p, len, strips);
+    for (int i = u0 * (BN / 32); i < u1 * (BN / 32); ++i) {
+        if (clear.has(i)) continue;
+        const int k = strips.key(i);
+        const uint32_t sees = paged_sees(p, b, tok, len, k);
+        for (int c = 0; c < 32; ++c) {
+            if (!(sees >> c & 1u)) continue;
+            const int2 at = paged_place(p, b, k + c);
+            if (at.x < 0) continue;
+            const uint16_t* v = p.v_pages + (((size_t)at.x * p.page_size + at.y) * p.Hkv + hk) * D;
+            for (int d = 0; d < D; ++d) {
+                const uint32_t y = v[d];
+                if (!paged_nonfinite<kBF16>(y)) continue;
+                if (part)
+                    part[d] += paged_from16<kBF16>(y);
+                else
+                    out[d] = float_to16<kBF16>(paged_from16<kBF16>(out[d]) + paged_from16<kBF16>(y));
+            }
+        }
+    }
+}
+
 template <int D, int NQ, bool kBF16>
 __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     paged_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PagedDecParams p) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedDecParams p) {
     using C = PagedCfg<D, NQ>;
     constexpr int BN = C::BN, DA = C::DA, NB = C::NB;
     extern __shared__ uint8_t smem_raw[];
@@ -360,32 +412,45 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    grid_dependency_wait();
-    tc_fence_before();
-    paged_make_plan<BN, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    // While the kernel before may still be running: the plan, of lengths that may yet change.  If one
+    // has, it is made again.
     const int G = p.g * p.rg, rng = (int)blockIdx.x / G, member = (int)blockIdx.x - rng * G;
     PagedWalk walk;
-    walk.init<BN>(p, plan_len, plan_prefix, rng);
     PagedSeg s;
+    bool more = false;
+    // The producer: a tile is nb boxes of box_rows keys and DA column atoms; lane i issues box i % nb
+    // of atom i / nb.  Table entries are loaded for 32 / nb tiles at a time, one such window ahead.
+    const int nb_log = p.nb_log, box = lane & ((1 << nb_log) - 1), ahead = lane >> nb_log;
+    auto fetch = [&](const PagedSeg& sg, int u) -> int2 {
+        u += ahead;
+        const int row = box * p.box_rows;
+        const int key = u < sg.u1 ? sg.strips.key(u * (BN / 32) + row / 32) + row % 32 : sg.len;
+        return key < sg.len ? paged_place(p, sg.b, key) : make_int2(-1, 0);
+    };
+    int2 ids = make_int2(-1, 0);
+    tc_fence_before();
+    for (bool first = true;; first = false) {
+        paged_make_plan<BN, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
+        walk.init(p, plan_len, plan_prefix, rng, member);
+        if (warp == C::kProducerWarp) more = walk.next(p, s);
+        if (first) grid_dependency_wait();
+        if (more) ids = fetch(s, s.u0);
+        // (every warp by itself: after the wait all see the same lengths)
+        bool stale = false;
+        for (int b = lane; b < p.B; b += 32) stale |= paged_len(p, b) != plan_len[b];
+        if (!__any_sync(0xffffffffu, stale)) break;
+        __syncthreads();
+    }
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
     if (warp == C::kProducerWarp) {
         // ------------------------------------------------------------ TMA producer --
-        // A tile is nb boxes of box_rows keys and DA column atoms; lane i issues box i % nb of atom
-        // i / nb.  Table entries are loaded for 32 / nb tiles at a time, one such window ahead.
-        const int nb = BN / p.box_rows, per_window = 32 / nb;
-        const int box = lane % nb, atom = lane / nb, ahead = lane / nb;
+        const int nb = 1 << nb_log, per_window = 32 >> nb_log, atom = ahead;
         uint32_t loads = 0, tcount = 0;  // tiles issued (K and V count one each), segments
         bool ok = true;
         auto wait = [&](uint32_t b, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(b, parity, wc));
-        };
-        auto fetch = [&](const PagedSeg& sg, int u) -> int2 {
-            u += ahead;
-            const int row = box * p.box_rows;
-            const int key = u < sg.u1 ? sg.strips.key(u * (BN / 32) + row / 32) + row % 32 : sg.len;
-            return key < sg.len ? paged_place(p, sg.b, key) : make_int2(-1, 0);
         };
         auto issue = [&](const CUtensorMap* map, int hk, int page, int row) -> bool {
             const uint32_t st = loads % NB;
@@ -412,11 +477,9 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
             ++tcount;
             return true;
         };
-        bool more = walk.next<BN>(p, member, s);
-        int2 ids = more ? fetch(s, s.u0) : make_int2(-1, 0);
         while (more && ok) {
             PagedSeg nxt;
-            const bool again = walk.next<BN>(p, member, nxt);
+            const bool again = walk.next(p, nxt);
             // The first segment's queries go first; those of a later one, which wait for the products of
             // the segment before, behind its first tile.
             bool need_q = tcount > 0;
@@ -495,7 +558,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
             for (int kk = 1; kk < BN / 16; ++kk)
                 umma_ts_elect<true>(d, a + kk * 8, b + ((kk * (16 * 128)) >> 4), v_hi, idesc_o);
         };
-        while (ok && walk.next<BN>(p, member, s)) {
+        while (ok && walk.next(p, s)) {
             const int n = s.u1 - s.u0;
             for (int q = 0; q < NQ && ok; ++q) ok = wait(bar(C::kBarQFull + q), tcount & 1u);
             ok = ok && wait_load(2 * kv_it);
@@ -549,7 +612,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     } else {
         // ------------------------------------------------------ softmax warpgroups ----
         const int q = warp >> 2, wq = warp & 3;
-        const int r = wq * 32 + lane;  // row of the sub-tile
+        const int r = wq * 32 + lane;  // row of the sub-tile's 128 = TMEM lane
+        const int tok_l = r / p.group, h_l = r - tok_l * p.group;
         const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t tO = lane_base + C::kOCol0 + q * D;
         constexpr int kSC = BN / 32;
@@ -570,31 +634,27 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                 for (long long i = threadIdx.x; i < rows; i += 128 * NQ) p.lse[b * rows + i] = kNegInf;
         }
 
-        while (ok && walk.next<BN>(p, member, s)) {
-            const int n = s.u1 - s.u0, tok_l = r / p.group, h_l = r - tok_l * p.group;
+        while (ok && walk.next(p, s)) {
+            const int n = s.u1 - s.u0;
             const int tok = (s.rb * NQ + q) * p.T + tok_l;
             const bool live = tok_l < p.T && tok < p.Sq;
             const bool any = __any_sync(0xffffffffu, live);  // whether the warp has rows
+            const PagedClear clear = paged_clear(p, s.len, s.strips);
             float m_run = kNegInf;
             uint64_t l2 = f2_pack(0.f, 0.f);
             for (int j = 0; j < n; ++j) {
-                int key[kSC];       // first key of each strip of the tile
-                uint32_t masked = 0;  // bit ch: strip ch hides a key from some token
-#pragma unroll
-                for (int ch = 0; ch < kSC; ++ch) {
-                    key[ch] = s.strips.key((s.u0 + j) * kSC + ch);
-                    masked |= paged_masked(p, s.len, key[ch]) ? 1u << ch : 0u;
-                }
+                const int strip0 = (s.u0 + j) * kSC;
+                const bool masked = strip0 < clear.lo || strip0 + kSC > clear.hi;
                 if (masked && q == 0) {
-                    // V's values that are not finite give way to zeros in those strips, the warpgroup's
-                    // threads taking 16 bytes each in turn.
+                    // V's values that are not finite give way to zeros in strips that hide a key, the
+                    // warpgroup's threads taking 16 bytes each in turn.
                     const uint32_t load = 2 * it + 1, at = sRing + (load % NB) * C::kTileBytes;
                     ok = mbar_wait(bar(C::kBarFull + load % NB), (load / NB) & 1u, wc);
                     if (!ok) break;
                     bool odd = false;
 #pragma unroll 1
                     for (int ch = 0; ch < kSC; ++ch) {
-                        if (!(masked >> ch & 1u)) continue;
+                        if (clear.has(strip0 + ch)) continue;
 #pragma unroll
                         for (int i = 0; i < 2 * DA; ++i) {  // 32 rows of an atom are 4096 bytes
                             const uint32_t a = at + (i >> 1) * (BN * 128) + ch * 4096 + (i & 1) * 2048 + r * 16;
@@ -616,30 +676,75 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                     __syncwarp();
                 }
                 const uint32_t slot = NQ == 1 ? it & 1u : (uint32_t)q;
+                float alpha = 1.f;
                 ok = mbar_wait(bar(C::kBarSFull + slot), NQ == 1 ? (it >> 1) & 1u : it & 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
-                float alpha = 1.f;
-                if (any) {
-                    const uint32_t tS = lane_base + slot * BN;  // P goes over S
+                const uint32_t tS = lane_base + slot * BN;  // P goes over S
+                // P = exp2(s * scale * log2 e - m), rounded to the inputs' 16 bits for the product (a relative
+                // error of half a step each, independent, so of a row's output about that of its own
+                // rounding); the sum l takes it unrounded.
+                uint64_t sum2 = f2_pack(0.f, 0.f), nm2 = 0;
+                auto new_max = [&](float raw_max) {
+                    const float m_blk = raw_max == kNegInf ? kNegInf : raw_max * p.scale_log2;
+                    const bool bump = live && m_blk > m_run + kRescaleLog2;  // (other rows hold anything)
+                    const float m_new = bump ? m_blk : m_run;
+                    alpha = bump ? ex2_approx(m_run - m_new) : 1.0f;
+                    m_run = m_new;
+                    const float m_sub = m_run == kNegInf ? 0.f : m_run;
+                    nm2 = f2_pack(-m_sub, -m_sub);
+                };
+                auto put_p = [&](int ch, const uint32_t (&u)[32]) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t a =
+                            fma2(f2_pack(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), c2, nm2);
+                        float a0, a1;
+                        f2_unpack(a, a0, a1);
+                        const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+                        sum2 = add2(sum2, f2_pack(p0, p1));
+                        pk[i] = pack2<kBF16>(p0, p1);
+                    }
+                    tmem_st_32x32b_x16(tS + ch * 16, pk);
+                };
+                if (any && masked) {
+                    // A strip at a time and each twice, for the row maximum first: in little code, since what
+                    // the kernel's code is above an SM's instruction cache costs every tile (at 138 KB 30 % of
+                    // the time; P of a strip lies over S of one before it).
+                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll 1
+                    for (int i = 0; i < 2 * kSC; ++i) {
+                        const int ch = i & (kSC - 1);
+                        uint32_t u[32];
+                        tmem_ld_32x32b_x32(tS + ch * 32, u);
+                        uint32_t see = 0xffffffffu;
+                        if (!clear.has(strip0 + ch))
+                            see = live ? paged_sees(p, s.b, tok, s.len, s.strips.key(strip0 + ch)) : 0u;
+                        __syncwarp();
+                        tmem_wait_ld(u);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) u[k] = (see >> k) & 1u ? u[k] : 0xff800000u;
+                        if (i < kSC) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8)
+#pragma unroll
+                                for (int c4 = 0; c4 < 4; ++c4)
+                                    mx[c4] = max3f(mx[c4], __uint_as_float(u[k + c4]), __uint_as_float(u[k + c4 + 4]));
+                            if (i == kSC - 1) new_max(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                        } else {
+                            put_p(ch, u);
+                        }
+                    }
+                } else if (any) {
                     uint32_t u[kSC][32];
 #pragma unroll
                     for (int ch = 0; ch < kSC; ++ch) tmem_ld_32x32b_x32(tS + ch * 32, u[ch]);
                     tmem_wait_ld(u[0]);
 #pragma unroll
                     for (int ch = 1; ch < kSC; ++ch) reg_fence(u[ch]);
-                    if (masked) {
-#pragma unroll
-                        for (int ch = 0; ch < kSC; ++ch) {
-                            if (!(masked >> ch & 1u)) continue;
-                            const uint32_t w = live ? paged_sees(p, s.b, tok, s.len, key[ch]) : 0u;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) u[ch][i] = (w >> i) & 1u ? u[ch][i] : 0xff800000u;
-                        }
-                        __syncwarp();
-                    }
                     auto sv = [&](int k) -> float { return __uint_as_float(u[k >> 5][k & 31]); };
-                    float mx[4];
+                    float mx[4];  // four chains of 3-input maxima
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mx[k] = sv(k);
 #pragma unroll
@@ -648,34 +753,11 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                         for (int c4 = 0; c4 < 4; ++c4) mx[c4] = max3f(mx[c4], sv(k + c4), sv(k + c4 + 4));
 #pragma unroll
                     for (int c4 = 0; c4 < 4; ++c4) mx[c4] = fmaxf(mx[c4], sv(BN - 4 + c4));
-                    const float raw_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const float m_blk = raw_max == kNegInf ? kNegInf : raw_max * p.scale_log2;
-                    const bool bump = m_blk > m_run + kRescaleLog2;
-                    const float m_new = bump ? m_blk : m_run;
-                    alpha = bump ? ex2_approx(m_run - m_new) : 1.0f;
-                    m_run = m_new;
-                    const float m_sub = m_run == kNegInf ? 0.f : m_run;
-                    const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
-                    // P = exp2(s * scale * log2 e - m), rounded to the inputs' 16 bits for the product (a
-                    // relative error of half a step each, independent, so of a row's output about that
-                    // of its own rounding); the sum l takes it unrounded.
-                    uint64_t sum2 = f2_pack(0.f, 0.f);
+                    new_max(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
 #pragma unroll
-                    for (int ch = 0; ch < kSC; ++ch) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint64_t a = fma2(f2_pack(sv(ch * 32 + 2 * i), sv(ch * 32 + 2 * i + 1)), c2, nm2);
-                            float a0, a1;
-                            f2_unpack(a, a0, a1);
-                            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-                            sum2 = add2(sum2, f2_pack(p0, p1));
-                            pk[i] = pack2<kBF16>(p0, p1);
-                        }
-                        tmem_st_32x32b_x16(tS + ch * 16, pk);
-                    }
-                    l2 = fma2(l2, f2_pack(alpha, alpha), sum2);
+                    for (int ch = 0; ch < kSC; ++ch) put_p(ch, u[ch]);
                 }
+                l2 = fma2(l2, f2_pack(alpha, alpha), sum2);
                 if (NQ == 1 && j > 0) {
                     // the product before may still be adding to O (with two sub-tiles, S of this tile
                     // was issued behind it)
@@ -684,7 +766,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                     tc_fence_after();
                 }
                 if (any && j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
                         uint32_t ov[32];
                         tmem_ld_32x32b_x32(tO + ch * 32, ov);
@@ -706,69 +788,47 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
             ok = mbar_wait(bar(C::kBarODone + q), NQ == 1 ? (it - 1) & 1u : tcount & 1u, wc);
             if (!ok) break;
             tc_fence_after();
-            if (any) {
-                const bool odd = odd_seg[tcount & 1u] == (int)tcount + 1;
-                float l0, l1;
-                f2_unpack(l2, l0, l1);
-                const float l_run = l0 + l1;
-                const bool none = l_run == 0.f;  // the row sees no key of the segment
-                const float inv_l = 1.0f / l_run;
-                const int h = s.hk * p.group + h_l;
-                const size_t row = ((size_t)s.b * p.Sq + tok) * p.Hq + h;
-                const size_t part = ((size_t)member * 2 * p.ranges + s.slot) * block_rows + q * p.T * p.group + r;
+            const bool odd = odd_seg[tcount & 1u] == (int)tcount + 1;
+            float l0, l1;
+            f2_unpack(l2, l0, l1);
+            const float l_run = l0 + l1;
+            const bool none = l_run == 0.f;  // the row sees no key of the segment
+            const float inv_l = 1.0f / l_run;
+            const int h = s.hk * p.group + h_l;
+            const size_t row = ((size_t)s.b * p.Sq + tok) * p.Hq + h;
+            const size_t part = ((size_t)member * 2 * p.ranges + s.slot) * block_rows + q * p.T * p.group + r;
+            // Eight values from column c of the row on, to where the segment's result goes.
+            auto put8 = [&](int c, const float* v) {
+                if (s.cut) {
+                    st_global_v8(p.o_part + part * D + c, v);
+                } else {
+                    st_global_v4(o16 + row * D + c, pack2<kBF16>(v[0], v[1]), pack2<kBF16>(v[2], v[3]),
+                                 pack2<kBF16>(v[4], v[5]), pack2<kBF16>(v[6], v[7]));
+                }
+            };
 #pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    uint32_t ov[32];
-                    tmem_ld_32x32b_x32(tO + ch * 32, ov);
-                    tmem_wait_ld(ov);
-                    if (live) {
-                        if (odd) {
-                            // What was taken out of V, to the rows that see it (rare: one copy of the code).
-                            for (int i = s.u0 * kSC; i < s.u1 * kSC; ++i) {
-                                const int k = s.strips.key(i);
-                                if (!paged_masked(p, s.len, k)) continue;
-                                const uint32_t sees = paged_sees(p, s.b, tok, s.len, k);
-                                for (int c = 0; c < 32; ++c) {
-                                    if (!(sees >> c & 1u)) continue;
-                                    const int2 at = paged_place(p, s.b, k + c);
-                                    if (at.x < 0) continue;
-                                    const uint16_t* v = p.v_pages +
-                                                        (((size_t)at.x * p.page_size + at.y) * p.Hkv + s.hk) * D + ch * 32;
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) {
-                                        const uint32_t x = v[i];
-                                        if (paged_nonfinite<kBF16>(x))
-                                            ov[i] = __float_as_uint(__uint_as_float(ov[i]) + paged_from16<kBF16>(x));
-                                    }
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) ov[i] = none ? 0u : __float_as_uint(__uint_as_float(ov[i]) * inv_l);
-                        if (s.cut) {
-                            float* to = p.o_part + part * D + ch * 32;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) st_global_v4(to + i, ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
-                        } else {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                w[i] = pack2<kBF16>(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1]));
-                            uint16_t* to = o16 + row * D + ch * 32;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                st_global_v4(to + i * 8, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                        }
-                    }
-                    __syncwarp();  // the next TMEM load is the whole warp's
-                }
+            for (int ch = 0; any && ch < D / 32; ++ch) {
+                uint32_t ov[32];
+                tmem_ld_32x32b_x32(tO + ch * 32, ov);
+                tmem_wait_ld(ov);
                 if (live) {
-                    const float lse = none ? kNegInf : (m_run + lg2_approx(l_run)) * kPagedLn2;
-                    if (s.cut)
-                        p.lse_part[part] = lse;
-                    else if (p.lse)
-                        p.lse[((size_t)s.b * p.Hq + h) * p.Sq + tok] = lse;
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = none ? 0.f : __uint_as_float(ov[i]) * inv_l;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) put8(ch * 32 + i, v + i);
                 }
+                __syncwarp();  // the next TMEM load is the whole warp's
+            }
+            if (live) {
+                if (odd)
+                    paged_add_odd<D, BN, kBF16>(p, s.b, s.hk, s.len, tok, s.u0, s.u1, s.cut ? p.o_part + part * D : nullptr,
+                                                o16 + row * D);
+                const float lse = none ? kNegInf : (m_run + lg2_approx(l_run)) * kPagedLn2;
+                if (s.cut)
+                    p.lse_part[part] = lse;
+                else if (p.lse)
+                    p.lse[((size_t)s.b * p.Hq + h) * p.Sq + tok] = lse;
             }
             tc_fence_before();
             __syncwarp();
@@ -787,133 +847,128 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
 
 // Joins the pieces of each row (b, token, head): lse = log sum_c exp(lse_c), and the outputs
 // weighted with exp(lse_c - lse).  WPR warps share a row, each taking every WPR-th piece; a lane
-// holds D / 32 dims.  Where the pieces lie is worked out before the split kernel is done.
+// holds D / 32 dims.  The CTAs walk over the rows, and make the plan once, before the split kernel
+// is done.
 template <int D, int NQ, int WPR, bool kBF16>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p) {
-    constexpr int V = D / 32, Rows = 8 / WPR, NP = V <= 4 ? 8 : 4, BN = PagedCfg<D, NQ>::BN;
+    constexpr int V = D / 32, Rows = 8 / WPR, NP = 4, BN = PagedCfg<D, NQ>::BN;
     constexpr int Vec = V % 4 == 0 ? 4 : V % 2 == 0 ? 2 : 1;  // values of a lane side by side
     __shared__ __align__(16) float s_acc[WPR > 1 ? 8 : 1][D];
     __shared__ float s_sum[8], s_max[8];
-    __shared__ int s_units[kPagedMaxB];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = (long long)blockIdx.x * Rows + warp / WPR;
-    const int part = warp % WPR;
+    __shared__ int s_warp_sum[8];
+    extern __shared__ int s_plan[];  // as large as the batch: the next call's split kernel fits beside this
+    int *s_len = s_plan, *s_prefix = s_plan + p.B;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
     const float kNegInf = -__int_as_float(0x7f800000);
-    const int per_seq = p.Sq * p.Hq;
-    const int b = (int)(row / per_seq), in_seq = (int)(row - (long long)b * per_seq);
-    const int tok = in_seq / p.Hq, h = in_seq - tok * p.Hq;
-    for (int i = threadIdx.x; i < p.B; i += 256) s_units[i] = paged_units<BN>(p, paged_len(p, i));
-    __syncthreads();
-    int before = 0, sum = 0, units = 0;
-    for (int i = lane; i < p.B; i += 32) {
-        const int t = s_units[i];
-        before += i < b ? t : 0;
-        units += i == b ? t : 0;
-        sum += t;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        units += __shfl_xor_sync(0xffffffffu, units, o);
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const int hk = h / p.group, rb = tok / (NQ * p.T);
-    const int e = hk / p.g * (p.row_blocks / p.rg) + rb / p.rg, member = hk % p.g + rb % p.rg * p.g;
-    const int W = paged_width(p, sum), start = p.entries * before + e * units;
-    const int n = paged_pieces(start, units, W), first = paged_first_piece(start, W);
-    const int block_rows = min(NQ * p.T, p.Sq) * p.group;
-    const int in_block = (tok - rb * NQ * p.T) * p.group + h - hk * p.group;
+    paged_make_plan<BN, 256>(p, s_len, s_prefix, s_warp_sum);
+    const int W = paged_width(p, s_prefix[p.B]), block_rows = min(NQ * p.T, p.Sq) * p.group;
+    const int rows = p.B * p.Sq * p.Hq;
     grid_launch_dependents();
     grid_dependency_wait();
-    // Rows with one piece or none have been written by the split kernel.  n is the same in all of a
-    // row's warps.
-    if (row >= (long long)p.B * per_seq || n < 2) return;
-    float acc[V], s = 0.f, m = kNegInf;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int c0 = part; c0 < n; c0 += WPR * NP) {
-        float w[NP], v[NP][V], top = m;
-#pragma unroll
-        for (int u = 0; u < NP; ++u) {
-            const int c = c0 + u * WPR;
-            w[u] = kNegInf;
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[u][i] = 0.f;
-            if (c >= n) continue;
-            const size_t at =
-                ((size_t)member * 2 * p.ranges + paged_slot(p, first + c, c == 0)) * block_rows + in_block;
-            w[u] = p.lse_part[at];
-#pragma unroll
-            for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
-        }
-#pragma unroll
-        for (int u = 0; u < NP; ++u) top = fmaxf(top, w[u]);
-        const float ref = top == kNegInf ? 0.f : top;
-        const float f = ex2_approx((m - ref) * (1.f / kPagedLn2));
-        m = top;
-        s *= f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] *= f;
-#pragma unroll
-        for (int u = 0; u < NP; ++u) {
-            const float x = ex2_approx((w[u] - ref) * (1.f / kPagedLn2));
-            s += x;
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(x, v[u][i], acc[i]);
-        }
-    }
-    if constexpr (WPR > 1) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) s_acc[warp][i / Vec * Vec * 32 + lane * Vec + i % Vec] = acc[i];
-        if (lane == 0) {
-            s_sum[warp] = s;
-            s_max[warp] = m;
-        }
-        __syncthreads();
-        if (warp != 0) return;
-#pragma unroll
-        for (int w = 1; w < WPR; ++w) m = fmaxf(m, s_max[w]);
-        s = 0.f;
+    for (int row = (int)blockIdx.x * Rows + warp / WPR; row < rows; row += (int)gridDim.x * Rows) {
+        const int seq_tok = row / p.Hq, h = row - seq_tok * p.Hq, b = seq_tok / p.Sq, tok = seq_tok - b * p.Sq;
+        const int hk = h / p.group, rb = tok / (NQ * p.T), units = s_prefix[b + 1] - s_prefix[b];
+        const int block = rb / p.rg, e = hk / p.g * p.blocks + block, member = hk % p.g + (rb - block * p.rg) * p.g;
+        const int start = p.groups * p.blocks * s_prefix[b] + e * units;
+        // Rows with one piece or none have been written by the split kernel.  n is the same in all of a
+        // row's warps.
+        const int n = paged_pieces(start, units, W), first = paged_first_piece(start, W);
+        if (n < 2) continue;
+        const int in_block = (tok - rb * NQ * p.T) * p.group + h - hk * p.group;
+        float acc[V], s = 0.f, m = kNegInf;
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        const float ref = m == kNegInf ? 0.f : m;
+        for (int c0 = part; c0 < n; c0 += WPR * NP) {
+            float w[NP], v[NP][V], top = m;
 #pragma unroll
-        for (int w = 0; w < WPR; ++w) {
-            const float f = ex2_approx((s_max[w] - ref) * (1.f / kPagedLn2));
-            s += f * s_sum[w];
+            for (int u = 0; u < NP; ++u) {
+                const int c = c0 + u * WPR;
+                w[u] = kNegInf;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                acc[i] = fmaf(f, s_acc[w][i / Vec * Vec * 32 + lane * Vec + i % Vec], acc[i]);
+                for (int i = 0; i < V; ++i) v[u][i] = 0.f;
+                if (c >= n) continue;
+                const size_t at =
+                    ((size_t)member * 2 * p.ranges + paged_slot(p, first + c, c == 0)) * block_rows + in_block;
+                w[u] = p.lse_part[at];
+#pragma unroll
+                for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
+            }
+#pragma unroll
+            for (int u = 0; u < NP; ++u) top = fmaxf(top, w[u]);
+            const float ref = top == kNegInf ? 0.f : top;
+            const float f = ex2_approx((m - ref) * (1.f / kPagedLn2));
+            m = top;
+            s *= f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] *= f;
+#pragma unroll
+            for (int u = 0; u < NP; ++u) {
+                const float x = ex2_approx((w[u] - ref) * (1.f / kPagedLn2));
+                s += x;
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(x, v[u][i], acc[i]);
+            }
         }
-    }
-    const float inv = 1.f / s;  // s == 0: no piece holds a visible key
+        if constexpr (WPR > 1) {
+            __syncthreads();  // the row before has been read
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = s == 0.f ? 0.f : acc[i] * inv;
-    uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * Vec;
+            for (int i = 0; i < V; ++i) s_acc[warp][i / Vec * Vec * 32 + lane * Vec + i % Vec] = acc[i];
+            if (lane == 0) {
+                s_sum[warp] = s;
+                s_max[warp] = m;
+            }
+            __syncthreads();
+            if (warp != 0) continue;
 #pragma unroll
-    for (int i = 0; i < V; i += Vec) {
-        if constexpr (Vec == 1)
-            out[i * 32] = float_to16<kBF16>(acc[i]);
-        else if constexpr (Vec == 2)
-            *reinterpret_cast<uint32_t*>(out + i * 32) = pack2<kBF16>(acc[i], acc[i + 1]);
-        else
-            *reinterpret_cast<uint2*>(out + i * 32) =
-                make_uint2(pack2<kBF16>(acc[i], acc[i + 1]), pack2<kBF16>(acc[i + 2], acc[i + 3]));
+            for (int w = 1; w < WPR; ++w) m = fmaxf(m, s_max[w]);
+            s = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            const float ref = m == kNegInf ? 0.f : m;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                const float f = ex2_approx((s_max[w] - ref) * (1.f / kPagedLn2));
+                s += f * s_sum[w];
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    acc[i] = fmaf(f, s_acc[w][i / Vec * Vec * 32 + lane * Vec + i % Vec], acc[i]);
+            }
+        }
+        const float inv = 1.f / s;  // s == 0: no piece holds a visible key
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = s == 0.f ? 0.f : acc[i] * inv;
+        uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * Vec;
+#pragma unroll
+        for (int i = 0; i < V; i += Vec) {
+            if constexpr (Vec == 1)
+                out[i * 32] = float_to16<kBF16>(acc[i]);
+            else if constexpr (Vec == 2)
+                *reinterpret_cast<uint32_t*>(out + i * 32) = pack2<kBF16>(acc[i], acc[i + 1]);
+            else
+                *reinterpret_cast<uint2*>(out + i * 32) =
+                    make_uint2(pack2<kBF16>(acc[i], acc[i + 1]), pack2<kBF16>(acc[i + 2], acc[i + 3]));
+        }
+        if (p.lse && lane == 0)
+            p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kPagedLn2;
     }
-    if (p.lse && lane == 0)
-        p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kPagedLn2;
 }
 
+// CTAs of the merge on an SM: what 256 threads of some 64 registers leave room for beside the split
+// kernel's last CTA.
+constexpr int kPagedMergeCtas = 4;
+
 template <int D, int NQ, int WPR>
-fa_status launch_paged_merge(const PagedDecParams& p, bool bf16, cudaStream_t s) {
+fa_status launch_paged_merge(const PagedDecParams& p, bool bf16, int num_sms, cudaStream_t s) {
     static int attr[64] = {0};
     if (!prefer_shared((const void*)paged_merge_kernel<D, NQ, WPR, true>,
                        (const void*)paged_merge_kernel<D, NQ, WPR, false>, attr))
         return FA_ERR_CUDA;
     const long long rows = (long long)p.B * p.Sq * p.Hq;
-    const unsigned grid = (unsigned)((rows + 8 / WPR - 1) / (8 / WPR));
-    return bf16 ? launch_overlapped(paged_merge_kernel<D, NQ, WPR, true>, grid, 256, 0, s, p)
-                : launch_overlapped(paged_merge_kernel<D, NQ, WPR, false>, grid, 256, 0, s, p);
+    const unsigned grid =
+        (unsigned)std::min((rows + 8 / WPR - 1) / (8 / WPR), (long long)num_sms * (WPR > 1 ? 8 : kPagedMergeCtas));
+    const size_t smem = PagedCfg<D, NQ>::plan_bytes(p.B);
+    return bf16 ? launch_overlapped(paged_merge_kernel<D, NQ, WPR, true>, grid, 256, smem, s, p)
+                : launch_overlapped(paged_merge_kernel<D, NQ, WPR, false>, grid, 256, smem, s, p);
 }
 
 template <int D, int NQ, bool kBF16>
@@ -939,12 +994,15 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     p.rg = p.g * p.row_blocks <= 16 ? p.row_blocks : 1;
     const int G = p.g * p.rg;
     if (G > a.num_sms) return FA_ERR_UNSUPPORTED;
-    p.entries = a.Hkv / p.g * (p.row_blocks / p.rg);
+    p.groups = a.Hkv / p.g;
+    p.blocks = p.row_blocks / p.rg;
     p.capacity = a.page_size * a.max_pages;
     p.page_size = a.page_size, p.num_pages = a.num_pages, p.max_pages = a.max_pages;
     // Rows of a copy: a tile's where its keys lie side by side, a strip's where a window may begin with
     // any of them; and the power of two that a page is made of.
     p.box_rows = std::min(a.page_size & -a.page_size, a.window_left >= 0 ? 32 : C::BN);
+    p.nb_log = 0;
+    while (p.box_rows << p.nb_log < C::BN) ++p.nb_log;
     p.page_recip = (unsigned)((1ull << 32) / (unsigned)a.page_size) + 1u;
     p.window_left = a.window_left, p.sinks = a.sinks;
     p.words = (a.Sq + 31) / 32;
@@ -958,7 +1016,7 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     if (a.window_left >= 0)
         strips = std::min(strips, ((long long)a.window_left + a.Sq + 31) / 32 + 1 + ((long long)a.sinks + 31) / 32);
     const long long most = (strips + C::BN / 32 - 1) / (C::BN / 32);
-    const long long units = (most + kPagedLead) * p.entries * a.B;  // of all entries at most
+    const long long units = (most + kPagedLead) * (p.groups * p.blocks) * a.B;  // of all entries at most
     if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     p.whole = most + kPagedLead <= kPagedMinWidth ? 1 : 0;
     p.ranges = (int)std::min((long long)(a.num_sms / G), (units + kPagedMinWidth - 1) / kPagedMinWidth);
@@ -971,8 +1029,8 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
                                 : launch_paged_split<D, NQ, false>(tq, tk, tv, p, s);
     if (st != FA_OK || p.whole) return st;
     // Few rows are cut into many pieces: eight warps each.
-    return (long long)a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_paged_merge<D, NQ, 8>(p, a.bf16, s)
-                                                         : launch_paged_merge<D, NQ, 1>(p, a.bf16, s);
+    return (long long)a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_paged_merge<D, NQ, 8>(p, a.bf16, a.num_sms, s)
+                                                         : launch_paged_merge<D, NQ, 1>(p, a.bf16, a.num_sms, s);
 }
 
 // Two sub-tiles share each key tile where one does not hold a kv head's rows (at D = 256 TMEM has

@@ -84,8 +84,8 @@ def test_valid_calls_without_a_device_fail_loudly(lib):
 def test_workspace_bytes(lib):
     f = lib.fa_decode_paged_workspace_bytes
     rows = 2 * 152 * 12
-    assert f(8, 3, 32, 8, 128, 152) == (rows * 512 + 255) // 256 * 256 + (rows * 4 + 255) // 256 * 256
-    assert f(8, 64, 64, 8, 64, 152) == 2 * 152 * 256 * 65 * 4      # 512 query rows: row blocks of 256
+    assert f(8, 3, 32, 8, 128, 152) == (rows * 512 + 255) // 256 * 256 + (rows * 4 + 255) // 256 * 256 + 16
+    assert f(8, 64, 64, 8, 64, 152) == 2 * 152 * 256 * 65 * 4 + 16      # 512 query rows: row blocks of 256
     for bad in ((0, 1, 8, 8, 64), (1, 0, 8, 8, 64), (1, 1, 0, 8, 64), (1, 1, 9, 8, 64), (1, 1, 8, 8, 0)):
         assert f(*bad, 152) == 0
 
