@@ -21,7 +21,7 @@
 // those from the first token's window on.  Strips that hold no visible key are not read.
 //
 // Plan: a sequence's tiles are counted as units; the units of all entries (sequence, group of kv
-// heads), each led by kPagedLead units for what starting and finishing one costs, lie end to end
+// heads), each led by C::Lead units for what starting and finishing one costs, lie end to end
 // and are cut into equal ranges.  A range is worked on by G CTAs, one for each head of the group
 // (and for each row block, where there are few): they read the same keys at about the same time,
 // whose rows lie side by side in a page.  A cut entry leaves a partial output and log-sum-exp in
@@ -68,8 +68,6 @@ struct PagedDecParams {
     int* status;
 };
 
-constexpr int kPagedLead = 1;      // units charged to each entry beside its keys
-constexpr int kPagedMinWidth = 6;  // least units of a range: a cut costs the merge kernel
 constexpr int kPagedMaxB = 1024;
 constexpr float kPagedLn2 = 0.69314718055994531f;
 
@@ -83,6 +81,12 @@ struct PagedCfg {
     static constexpr int kTileBytes = BN * DA * 128;
     // K and V tiles take turns in one ring of NB buffers.
     static constexpr int NB = D == 64 ? 10 : (D == 256 || NQ == 2) ? 4 : 5;
+    // Units charged to each entry beside its tiles, and the least units of a range, since a cut costs the
+    // merge kernel.  Measured (us) with leads of 1, 2, 3, 4, 6: 64 drafts of 4 heads 107.5, 105.0,
+    // 102.7, 98.4, 96.4; window steps at D = 128 53.6, 53.2, 54.2, 53.4, 54.6 and at D = 96 20.3, 19.3, 18.5,
+    // 18.9, 19.2; D = 256 31.8, 31.1, 31.0, 30.6, 30.4.
+    static constexpr int Lead = NQ == 1 ? 4 : 6;
+    static constexpr int MinWidth = Lead + 4;
     static constexpr int kSlots = 2;  // S buffers in TMEM: two of one sub-tile, or one of each
     static constexpr int kOCol0 = kSlots * BN;
     static constexpr int kTmemCols = 512;
@@ -100,7 +104,12 @@ struct PagedCfg {
     static constexpr int kBarODrained = kBarODone + NQ;
     static constexpr int kBarFinal = kBarODrained + NQ;
     static constexpr int kNumBars = kBarFinal + 1;
-    static constexpr int kFixedBytes = 1024 + NQ * kQBytes + NB * kTileBytes + 8 * kNumBars + 32;
+    // Results leave through shared memory, OC columns of a warp's 32 rows at a time, so that lanes side by
+    // side write memory side by side (a lane that wrote its own row took 32 lines for each instruction:
+    // 256 rows of D = 128 8800 cycles).  Rows are 4 words more than OC apart: no bank is met twice.
+    static constexpr int OC = NQ == 1 ? 32 : 16;
+    static constexpr int kOutBytes = 4 * NQ * 32 * (OC + 4) * 4;
+    static constexpr int kFixedBytes = 1024 + NQ * kQBytes + NB * kTileBytes + kOutBytes + 8 * kNumBars + 32;
     static constexpr int plan_bytes(int B) { return (2 * B + 1) * 4; }
     static_assert(kFixedBytes + (2 * kPagedMaxB + 1) * 4 + 256 <= 232448, "shared memory of a CTA");
 };
@@ -123,24 +132,29 @@ __device__ __forceinline__ PagedStrips paged_strips(const PagedDecParams& p, int
     return t;
 }
 
-template <int BN>
+template <class C>
 __device__ __forceinline__ int paged_units(const PagedDecParams& p, int len) {
     if (len <= 0) return 0;
     const PagedStrips t = paged_strips(p, len);
-    return (t.sinks + (len + 31) / 32 - t.first + BN / 32 - 1) / (BN / 32) + kPagedLead;
+    return (t.sinks + (len + 31) / 32 - t.first + C::BN / 32 - 1) / (C::BN / 32) + C::Lead;
 }
 
 // Units of a range, from the units of one entry of each sequence summed.
+template <class C>
 __device__ __forceinline__ int paged_width(const PagedDecParams& p, int sum_units) {
     const unsigned total = (unsigned)sum_units * (unsigned)(p.groups * p.blocks);
-    return max((int)((total + (unsigned)p.ranges - 1u) / (unsigned)p.ranges), kPagedMinWidth);
+    return max((int)((total + (unsigned)p.ranges - 1u) / (unsigned)p.ranges), C::MinWidth);
 }
 
 // The pieces of an entry of `units` units from unit `start` on: the first range that holds keys of
 // it, and how many ranges do.
-__device__ __forceinline__ int paged_first_piece(int start, int w) { return (start + kPagedLead) / w; }
+template <class C>
+__device__ __forceinline__ int paged_first_piece(int start, int w) {
+    return (start + C::Lead) / w;
+}
+template <class C>
 __device__ __forceinline__ int paged_pieces(int start, int units, int w) {
-    return units > 0 ? (start + units - 1) / w - paged_first_piece(start, w) + 1 : 0;
+    return units > 0 ? (start + units - 1) / w - paged_first_piece<C>(start, w) + 1 : 0;
 }
 // The slot of an entry's piece in range r: a range has at most one piece of an entry that began
 // before it, and one that goes on behind it.
@@ -155,6 +169,7 @@ struct PagedSeg {
 };
 
 // Walks the segments of one range; no division but at its start.
+template <class C>
 struct PagedWalk {
     const int* len;     // [B]
     const int* prefix;  // [B + 1], of the units of one entry
@@ -170,7 +185,7 @@ struct PagedWalk {
         head = member & (p.g - 1);
         sub = member / p.g;
         const int entries = p.groups * p.blocks, total = prefix[p.B] * entries;
-        W = paged_width(p, prefix[p.B]);
+        W = paged_width<C>(p, prefix[p.B]);
         x = x0 = (int)min((long long)rng * W, (long long)total);
         x_end = (int)min((long long)x + W, (long long)total);
         if (x >= x_end) return;
@@ -207,14 +222,14 @@ struct PagedWalk {
                 continue;
             }
             const int end = p.whole ? start + units : min(x_end, start + units);
-            const bool first = start + kPagedLead >= x0;  // its first keys are this range's
+            const bool first = start + C::Lead >= x0;  // its first keys are this range's
             s.b = b;
             s.hk = group * p.g + head;
             s.rb = block * p.rg + sub;
             s.len = len[b];
             s.strips = paged_strips(p, s.len);
-            s.u0 = max(x - start - kPagedLead, 0);
-            s.u1 = end - start - kPagedLead;
+            s.u0 = max(x - start - C::Lead, 0);
+            s.u1 = end - start - C::Lead;
             s.slot = paged_slot(p, rng, first);
             s.cut = !p.whole && !(first && start + units <= x0 + W);
             x = end;
@@ -231,27 +246,28 @@ __device__ __forceinline__ uint32_t paged_bits(int a, int b) {
     return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
 }
 
-// Bit i: whether token `tok` of a sequence of `len` keys sees key k + i.
-__device__ __forceinline__ uint32_t paged_sees(const PagedDecParams& p, int b, int tok, int len, int k) {
-    if (p.tree) {
-        const int ctx = len - p.Sq, t = k - ctx;  // bit i is draft t + i
-        uint32_t w = paged_bits(0, ctx - 1 - k);
-        if (t > -32 && t < p.Sq) {
-            const int32_t* m = p.tree + ((size_t)b * p.Sq + tok) * p.words;
-            uint32_t d;
-            if (t < 0) {
-                d = (uint32_t)__ldg(m) << -t;
-            } else {
-                const int i = t >> 5;
-                d = __funnelshift_r((uint32_t)__ldg(m + i), i + 1 < p.words ? (uint32_t)__ldg(m + i + 1) : 0u, t & 31);
-            }
-            w |= d & paged_bits(-t, len - 1 - k);
-        }
-        return w;
+// The keys that token `tok` of a sequence of `len` keys sees: lo .. hi and those before sink (of a
+// tree: those before the drafts).
+__device__ __forceinline__ void paged_row(const PagedDecParams& p, int len, int tok, int& lo, int& hi, int& sink) {
+    const int ctx = len - p.Sq;
+    hi = p.tree ? ctx - 1 : ctx + tok;
+    lo = p.window_left >= 0 ? max(hi, 0) - p.window_left : 0;
+    sink = min(p.sinks, hi + 1);
+}
+
+// Bit i: whether key k + i is a draft that token `tok` sees.
+static __device__ __noinline__ uint32_t paged_drafts(const PagedDecParams& p, int b, int tok, int len, int k) {
+    const int t = k - (len - p.Sq);  // bit i is draft t + i
+    if (t <= -32 || t >= p.Sq) return 0u;
+    const int32_t* m = p.tree + ((size_t)b * p.Sq + tok) * p.words;
+    uint32_t d;
+    if (t < 0) {
+        d = (uint32_t)__ldg(m) << -t;
+    } else {
+        const int i = t >> 5;
+        d = __funnelshift_r((uint32_t)__ldg(m + i), i + 1 < p.words ? (uint32_t)__ldg(m + i + 1) : 0u, t & 31);
     }
-    const int last = len - p.Sq + tok;
-    const uint32_t w = paged_bits(p.window_left >= 0 ? last - k - p.window_left : 0, last - k);
-    return w | paged_bits(0, min(p.sinks - 1, last) - k);
+    return d & paged_bits(-t, len - 1 - k);
 }
 
 // The strips lo .. hi - 1 of a sequence's tiles hide no key from any token (some of the sinks' may
@@ -287,13 +303,6 @@ __device__ __forceinline__ float paged_from16(uint32_t x) {
     }
 }
 
-// 32 bytes to a 32-byte boundary: whole sectors, where each lane writes to a row of its own.
-__device__ __forceinline__ void st_global_v8(void* p, const float* v) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-}
-
 // Page and row within it of key `key` of sequence b; page -1: none.
 __device__ __forceinline__ int2 paged_place(const PagedDecParams& p, int b, int key) {
     unsigned pi = __umulhi((unsigned)key, p.page_recip);  // the quotient, or one more
@@ -307,7 +316,7 @@ __device__ __forceinline__ int2 paged_place(const PagedDecParams& p, int b, int 
 }
 
 // Fills len[B] and prefix[B + 1] (all threads; ends with a barrier).
-template <int BN, int kThreads>
+template <class C, int kThreads>
 __device__ __forceinline__ void paged_make_plan(const PagedDecParams& p, int* len, int* prefix, int* warp_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -317,7 +326,7 @@ __device__ __forceinline__ void paged_make_plan(const PagedDecParams& p, int* le
         if (b < p.B) {
             const int n = paged_len(p, b);
             len[b] = n;
-            sum += prefix[b] = paged_units<BN>(p, n);
+            sum += prefix[b] = paged_units<C>(p, n);
         }
     }
     int incl = sum;
@@ -349,10 +358,13 @@ __device__ __noinline__ void paged_add_odd(const PagedDecParams& p, int b, int h
                                            float* part, uint16_t* out) {
     const PagedStrips strips = paged_strips(p, len);
     const PagedClear clear = paged_clear(p, len, strips);
+    int lo, hi, sink;
+    paged_row(p, len, tok, lo, hi, sink);
     for (int i = u0 * (BN / 32); i < u1 * (BN / 32); ++i) {
         if (clear.has(i)) continue;
         const int k = strips.key(i);
-        const uint32_t sees = paged_sees(p, b, tok, len, k);
+        uint32_t sees = paged_bits(lo - k, hi - k) | paged_bits(0, sink - 1 - k);
+        if (p.tree) sees |= paged_drafts(p, b, tok, len, k);
         for (int c = 0; c < 32; ++c) {
             if (!(sees >> c & 1u)) continue;
             const int2 at = paged_place(p, b, k + c);
@@ -379,9 +391,9 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_warp_sum[C::kThreads / 32];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    const uint32_t sQ = base, sRing = sQ + NQ * C::kQBytes, sBar = sRing + NB * C::kTileBytes;
+    const uint32_t sQ = base, sRing = sQ + NQ * C::kQBytes, sOut = sRing + NB * C::kTileBytes, sBar = sOut + C::kOutBytes;
     uint32_t* tmem_slot =
-        reinterpret_cast<uint32_t*>(smem_raw + (base - raw) + NQ * C::kQBytes + NB * C::kTileBytes + 8 * C::kNumBars);
+        reinterpret_cast<uint32_t*>(smem_raw + (sBar - raw) + 8 * C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // Of the last two segments the one (counted from 1) whose V held a value that is not finite in a
     // tile with hidden keys.
@@ -415,7 +427,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     // While the kernel before may still be running: the plan, of lengths that may yet change.  If one
     // has, it is made again.
     const int G = p.g * p.rg, rng = (int)blockIdx.x / G, member = (int)blockIdx.x - rng * G;
-    PagedWalk walk;
+    PagedWalk<C> walk;
     PagedSeg s;
     bool more = false;
     // The producer: a tile is nb boxes of box_rows keys and DA column atoms; lane i issues box i % nb
@@ -430,7 +442,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     int2 ids = make_int2(-1, 0);
     tc_fence_before();
     for (bool first = true;; first = false) {
-        paged_make_plan<BN, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
+        paged_make_plan<C, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
         walk.init(p, plan_len, plan_prefix, rng, member);
         if (warp == C::kProducerWarp) more = walk.next(p, s);
         if (first) grid_dependency_wait();
@@ -640,6 +652,9 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
             const bool live = tok_l < p.T && tok < p.Sq;
             const bool any = __any_sync(0xffffffffu, live);  // whether the warp has rows
             const PagedClear clear = paged_clear(p, s.len, s.strips);
+            const int tok_in = live ? tok : 0;
+            int lo, hi, sink;
+            paged_row(p, s.len, tok_in, lo, hi, sink);
             float m_run = kNegInf;
             uint64_t l2 = f2_pack(0.f, 0.f);
             for (int j = 0; j < n; ++j) {
@@ -708,41 +723,27 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
                     }
                     tmem_st_32x32b_x16(tS + ch * 16, pk);
                 };
-                if (any && masked) {
-                    // A strip at a time and each twice, for the row maximum first: in little code, since what
-                    // the kernel's code is above an SM's instruction cache costs every tile (at 138 KB 30 % of
-                    // the time; P of a strip lies over S of one before it).
-                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll 1
-                    for (int i = 0; i < 2 * kSC; ++i) {
-                        const int ch = i & (kSC - 1);
-                        uint32_t u[32];
-                        tmem_ld_32x32b_x32(tS + ch * 32, u);
-                        uint32_t see = 0xffffffffu;
-                        if (!clear.has(strip0 + ch))
-                            see = live ? paged_sees(p, s.b, tok, s.len, s.strips.key(strip0 + ch)) : 0u;
-                        __syncwarp();
-                        tmem_wait_ld(u);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) u[k] = (see >> k) & 1u ? u[k] : 0xff800000u;
-                        if (i < kSC) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 8)
-#pragma unroll
-                                for (int c4 = 0; c4 < 4; ++c4)
-                                    mx[c4] = max3f(mx[c4], __uint_as_float(u[k + c4]), __uint_as_float(u[k + c4 + 4]));
-                            if (i == kSC - 1) new_max(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                        } else {
-                            put_p(ch, u);
-                        }
-                    }
-                } else if (any) {
+                if (any) {
                     uint32_t u[kSC][32];
 #pragma unroll
                     for (int ch = 0; ch < kSC; ++ch) tmem_ld_32x32b_x32(tS + ch * 32, u[ch]);
                     tmem_wait_ld(u[0]);
 #pragma unroll
                     for (int ch = 1; ch < kSC; ++ch) reg_fence(u[ch]);
+                    if (masked) {
+#pragma unroll
+                        for (int ch = 0; ch < kSC; ++ch) {
+                            if (clear.has(strip0 + ch)) continue;
+                            // The row sees the keys lo .. hi and those before sink, and what the tree's mask says.
+                            const int k = s.strips.key(strip0 + ch);
+                            uint32_t w = paged_bits(lo - k, hi - k) | paged_bits(0, sink - 1 - k);
+                            if (p.tree) w |= paged_drafts(p, s.b, tok_in, s.len, k);
+                            if (!live) w = 0;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[ch][i] = (w >> i) & 1u ? u[ch][i] : 0xff800000u;
+                        }
+                        __syncwarp();
+                    }
                     auto sv = [&](int k) -> float { return __uint_as_float(u[k >> 5][k & 31]); };
                     float mx[4];  // four chains of 3-input maxima
 #pragma unroll
@@ -797,28 +798,53 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
             const int h = s.hk * p.group + h_l;
             const size_t row = ((size_t)s.b * p.Sq + tok) * p.Hq + h;
             const size_t part = ((size_t)member * 2 * p.ranges + s.slot) * block_rows + q * p.T * p.group + r;
-            // Eight values from column c of the row on, to where the segment's result goes.
-            auto put8 = [&](int c, const float* v) {
-                if (s.cut) {
-                    st_global_v8(p.o_part + part * D + c, v);
-                } else {
-                    st_global_v4(o16 + row * D + c, pack2<kBF16>(v[0], v[1]), pack2<kBF16>(v[2], v[3]),
-                                 pack2<kBF16>(v[4], v[5]), pack2<kBF16>(v[6], v[7]));
-                }
-            };
+            // The warp's live rows are its first ones; in the result they are part or row + ... of the first.
+            const int rows = __popc(__ballot_sync(0xffffffffu, live));
+            const uint32_t out = sOut + (uint32_t)warp * (32 * (C::OC + 4) * 4);
 #pragma unroll 1
-            for (int ch = 0; any && ch < D / 32; ++ch) {
-                uint32_t ov[32];
-                tmem_ld_32x32b_x32(tO + ch * 32, ov);
+            for (int c0 = 0; any && c0 < D; c0 += C::OC) {
+                uint32_t ov[C::OC];
+                if constexpr (C::OC == 32)
+                    tmem_ld_32x32b_x32(tO + c0, ov);
+                else
+                    tmem_ld_32x32b_x16(tO + c0, ov);
                 tmem_wait_ld(ov);
-                if (live) {
-                    float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = none ? 0.f : __uint_as_float(ov[i]) * inv_l;
+                for (int i = 0; i < C::OC; ++i) ov[i] = none ? 0u : __float_as_uint(__uint_as_float(ov[i]) * inv_l);
+                __syncwarp();  // the columns before have been read
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) put8(ch * 32 + i, v + i);
+                for (int i = 0; i < C::OC; i += 4)
+                    st_shared_v4(out + (lane * (C::OC + 4) + i) * 4, ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                __syncwarp();
+                if (s.cut) {
+                    constexpr int L = C::OC / 4, R = 32 / L;  // lanes of a row, rows at a time
+                    const int rr = lane / L, cc = lane % L * 4;
+                    float* to = p.o_part + (part - lane + rr) * D + c0 + cc;
+                    uint32_t w[32 / R][4];
+#pragma unroll
+                    for (int i = 0; i < 32 / R; ++i) lds128(out + ((i * R + rr) * (C::OC + 4) + cc) * 4, w[i]);
+#pragma unroll
+                    for (int i = 0; i < 32 / R; ++i)
+                        if (i * R + rr < rows) st_global_v4(to + i * R * D, w[i][0], w[i][1], w[i][2], w[i][3]);
+                } else {
+                    constexpr int L = C::OC / 8, R = 32 / L;
+                    const int rr = lane / L, cc = lane % L * 8;
+                    for (int i = 0; i < rows; i += R) {
+                        const int from = min(i + rr, rows - 1);
+                        const long long at = __shfl_sync(0xffffffffu, (long long)row, from);
+                        if (i + rr >= rows) continue;
+                        uint32_t w[4], x[4];
+                        lds128(out + (from * (C::OC + 4) + cc) * 4, w);
+                        lds128(out + (from * (C::OC + 4) + cc + 4) * 4, x);
+                        auto f = [](uint32_t y) { return __uint_as_float(y); };
+                        st_global_v4(o16 + at * D + c0 + cc, pack2<kBF16>(f(w[0]), f(w[1])), pack2<kBF16>(f(w[2]), f(w[3])),
+                                     pack2<kBF16>(f(x[0]), f(x[1])), pack2<kBF16>(f(x[2]), f(x[3])));
+                    }
                 }
-                __syncwarp();  // the next TMEM load is the whole warp's
+            }
+            if (odd) {  // other lanes' writes to the row come first
+                __threadfence_block();
+                __syncwarp();
             }
             if (live) {
                 if (odd)
@@ -851,7 +877,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
 // is done.
 template <int D, int NQ, int WPR, bool kBF16>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p) {
-    constexpr int V = D / 32, Rows = 8 / WPR, NP = 4, BN = PagedCfg<D, NQ>::BN;
+    constexpr int V = D / 32, Rows = 8 / WPR, NP = 4;
+    using C = PagedCfg<D, NQ>;
     constexpr int Vec = V % 4 == 0 ? 4 : V % 2 == 0 ? 2 : 1;  // values of a lane side by side
     __shared__ __align__(16) float s_acc[WPR > 1 ? 8 : 1][D];
     __shared__ float s_sum[8], s_max[8];
@@ -860,8 +887,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p
     int *s_len = s_plan, *s_prefix = s_plan + p.B;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
     const float kNegInf = -__int_as_float(0x7f800000);
-    paged_make_plan<BN, 256>(p, s_len, s_prefix, s_warp_sum);
-    const int W = paged_width(p, s_prefix[p.B]), block_rows = min(NQ * p.T, p.Sq) * p.group;
+    paged_make_plan<C, 256>(p, s_len, s_prefix, s_warp_sum);
+    const int W = paged_width<C>(p, s_prefix[p.B]), block_rows = min(NQ * p.T, p.Sq) * p.group;
     const int rows = p.B * p.Sq * p.Hq;
     grid_launch_dependents();
     grid_dependency_wait();
@@ -872,7 +899,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p
         const int start = p.groups * p.blocks * s_prefix[b] + e * units;
         // Rows with one piece or none have been written by the split kernel.  n is the same in all of a
         // row's warps.
-        const int n = paged_pieces(start, units, W), first = paged_first_piece(start, W);
+        const int n = paged_pieces<C>(start, units, W), first = paged_first_piece<C>(start, W);
         if (n < 2) continue;
         const int in_block = (tok - rb * NQ * p.T) * p.group + h - hk * p.group;
         float acc[V], s = 0.f, m = kNegInf;
@@ -1016,10 +1043,10 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     if (a.window_left >= 0)
         strips = std::min(strips, ((long long)a.window_left + a.Sq + 31) / 32 + 1 + ((long long)a.sinks + 31) / 32);
     const long long most = (strips + C::BN / 32 - 1) / (C::BN / 32);
-    const long long units = (most + kPagedLead) * (p.groups * p.blocks) * a.B;  // of all entries at most
+    const long long units = (most + C::Lead) * (p.groups * p.blocks) * a.B;  // of all entries at most
     if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    p.whole = most + kPagedLead <= kPagedMinWidth ? 1 : 0;
-    p.ranges = (int)std::min((long long)(a.num_sms / G), (units + kPagedMinWidth - 1) / kPagedMinWidth);
+    p.whole = most + C::Lead <= C::MinWidth ? 1 : 0;
+    p.ranges = (int)std::min((long long)(a.num_sms / G), (units + C::MinWidth - 1) / C::MinWidth);
     CUtensorMap tq, tk, tv;
     if (!encode_paged_tmap(&tq, a.q, a.bf16, D, a.Hq, a.Sq, a.B, p.group, p.T) ||
         !encode_paged_tmap(&tk, a.k_pages, a.bf16, D, a.Hkv, a.page_size, a.num_pages, 1, p.box_rows) ||
