@@ -91,9 +91,9 @@ struct PagedCfg {
     static constexpr int kOCol0 = kSlots * BN;
     static constexpr int kTmemCols = 512;
     static_assert(kOCol0 + NQ * D <= kTmemCols, "TMEM budget");
-    static constexpr int kThreads = 128 * NQ + 64;
-    static constexpr int kProducerWarp = 4 * NQ;
-    static constexpr int kMmaWarp = 4 * NQ + 1;
+    static constexpr int kThreads = 128 * NQ + 96;
+    static constexpr int kProducerWarp = 4 * NQ;  // Q and K; the next warp: V
+    static constexpr int kMmaWarp = 4 * NQ + 2;
     static constexpr int kBarQFull = 0;
     static constexpr int kBarQEmpty = kBarQFull + NQ;
     static constexpr int kBarFull = kBarQEmpty + NQ;
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     const int G = p.g * p.rg, rng = (int)blockIdx.x / G, member = (int)blockIdx.x - rng * G;
     PagedWalk<C> walk;
     PagedSeg s;
+    const bool producer = warp == C::kProducerWarp || warp == C::kProducerWarp + 1;
     bool more = false;
     // The producer: a tile is nb boxes of box_rows keys and DA column atoms; lane i issues box i % nb
     // of atom i / nb.  Table entries are loaded for 32 / nb tiles at a time, one such window ahead.
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     for (bool first = true;; first = false) {
         paged_make_plan<C, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
         walk.init(p, plan_len, plan_prefix, rng, member);
-        if (warp == C::kProducerWarp) more = walk.next(p, s);
+        if (producer) more = walk.next(p, s);
         if (first) grid_dependency_wait();
         if (more) ids = fetch(s, s.u0);
         // (every warp by itself: after the wait all see the same lengths)
@@ -456,60 +457,61 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
-    if (warp == C::kProducerWarp) {
-        // ------------------------------------------------------------ TMA producer --
+    if (producer) {
+        // ----------------------------------------------------------- TMA producers --
+        // One for Q and K, one for V: a copy takes a warp some 70 cycles, and a tile of 16-key pages is 16
+        // copies of K and as many of V.
         const int nb = 1 << nb_log, per_window = 32 >> nb_log, atom = ahead;
-        uint32_t loads = 0, tcount = 0;  // tiles issued (K and V count one each), segments
+        const int is_v = warp - C::kProducerWarp;
+        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+        uint32_t load = is_v, tcount = 0;  // the ring's loads: K of tile n is load 2 n, V is load 2 n + 1; segments
         bool ok = true;
         auto wait = [&](uint32_t b, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(b, parity, wc));
-        };
-        auto issue = [&](const CUtensorMap* map, int hk, int page, int row) -> bool {
-            const uint32_t st = loads % NB;
-            if (!wait(bar(C::kBarEmpty + st), ((loads / NB) & 1u) ^ 1u)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarFull + st), C::kTileBytes);
-            __syncwarp();
-            if (atom < DA)  // keys on no page read as zeros: a page past the last one
-                tma_load_4d(sRing + st * C::kTileBytes + atom * (BN * 128) + box * p.box_rows * 128, map,
-                            bar(C::kBarFull + st), atom * 64, hk, row, page < 0 ? p.num_pages : page);
-            ++loads;
-            return true;
         };
         const uint32_t q_bytes = (uint32_t)(DA * p.T * p.group * 128);
         auto load_q = [&](const PagedSeg& sg) -> bool {
             for (int q = 0; q < NQ; ++q) {
                 if (!wait(bar(C::kBarQEmpty + q), (tcount & 1u) ^ 1u)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(C::kBarQFull + q), q_bytes);
-                    for (int a = 0; a < DA; ++a)
-                        tma_load_4d(sQ + q * C::kQBytes + a * (C::BM * 128), &tm_q, bar(C::kBarQFull + q), a * 64,
-                                    sg.hk * p.group, (sg.rb * NQ + q) * p.T, sg.b);
-                }
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarQFull + q), q_bytes);
+                __syncwarp();
+                if (lane < DA)
+                    tma_load_4d(sQ + q * C::kQBytes + lane * (C::BM * 128), &tm_q, bar(C::kBarQFull + q), lane * 64,
+                                sg.hk * p.group, (sg.rb * NQ + q) * p.T, sg.b);
             }
             ++tcount;
             return true;
         };
         while (more && ok) {
             PagedSeg nxt;
-            const bool again = walk.next(p, nxt);
-            // The first segment's queries go first; those of a later one, which wait for the products of
-            // the segment before, behind its first tile.
-            bool need_q = tcount > 0;
-            if (!need_q) ok = load_q(s);
+            bool again = false, first = true;
             for (int u = s.u0; u < s.u1 && ok; u += per_window) {
                 const int2 use = ids;
-                if (u + per_window < s.u1)
-                    ids = fetch(s, u + per_window);
-                else if (again)
-                    ids = fetch(nxt, nxt.u0);
                 const int n = min(per_window, s.u1 - u);
                 for (int k = 0; k < n && ok; ++k) {
                     const int page = __shfl_sync(0xffffffffu, use.x, k * nb + box);
                     const int row = __shfl_sync(0xffffffffu, use.y, k * nb + box);
-                    ok = issue(&tm_k, s.hk, page, row) && issue(&tm_v, s.hk, page, row);
-                    if (ok && need_q) {
-                        ok = load_q(s);
-                        need_q = false;
+                    const uint32_t st = load % NB;
+                    ok = wait(bar(C::kBarEmpty + st), ((load / NB) & 1u) ^ 1u);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(C::kBarFull + st), C::kTileBytes);
+                    __syncwarp();
+                    if (atom < DA)  // keys on no page read as zeros: a page past the last one
+                        tma_load_4d(sRing + st * C::kTileBytes + atom * (BN * 128) + box * p.box_rows * 128, map,
+                                    bar(C::kBarFull + st), atom * 64, s.hk, row, page < 0 ? p.num_pages : page);
+                    load += 2;
+                    if (first) {
+                        // Behind the first tile: the queries, which may have to wait for the products of the
+                        // segment before, and what comes after this segment.
+                        if (!is_v) ok = load_q(s);
+                        again = walk.next(p, nxt);
+                        first = false;
+                    }
+                    if (k == 0) {  // the next window's table entries
+                        if (u + per_window < s.u1)
+                            ids = fetch(s, u + per_window);
+                        else if (again)
+                            ids = fetch(nxt, nxt.u0);
                     }
                 }
             }
@@ -520,10 +522,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
         __syncwarp();
         // Every copy this warp started has landed before shared memory goes.
         if (lane == 0) {
-            for (uint32_t d = 0; d < (uint32_t)NB && d < loads; ++d) {
-                const uint32_t last = loads - 1 - d;
-                mbar_wait_drain(bar(C::kBarFull + last % NB), (last / NB) & 1u);
-            }
+            // (the last use of each buffer: an earlier one's phase may have passed twice)
+            const uint32_t end = load - is_v;
+            for (uint32_t l = load; l >= 2 + (uint32_t)is_v && l - 2 + NB >= end; l -= 2)
+                mbar_wait_drain(bar(C::kBarFull + (l - 2) % NB), ((l - 2) / NB) & 1u);
             if (tcount > 0)
                 for (int q = 0; q < NQ; ++q) mbar_wait_drain(bar(C::kBarQFull + q), (tcount - 1) & 1u);
         }
