@@ -54,6 +54,8 @@ def load():
         lib.fa_fwd_window.restype = I
         lib.fa_fwd_sinks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P]
         lib.fa_fwd_sinks.restype = I
+        lib.fa_fwd_varlen_sinks.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P]
+        lib.fa_fwd_varlen_sinks.restype = I
         lib.fa_decode_workspace_bytes.argtypes = [I, I, I, I]
         lib.fa_decode_workspace_bytes.restype = SZ
         lib.fa_decode_default_splits.argtypes = [I, I, I, I]
@@ -112,6 +114,8 @@ def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, 
     Returns (o, lse): o like q, lse fp32 [B, Hq, Sq] (None if return_lse is False and no
     lse buffer was given).  scale defaults to 1/sqrt(D).
     """
+    if sinks:
+        return _fwd_sinks(q, k, v, causal, scale, window, sinks, out, lse, return_lse, stream)
     if q.dtype not in _DTYPE:
         raise TypeError("q/k/v must be bf16 or fp16")
     for name, t in (("q", q), ("k", k), ("v", v)):
@@ -134,12 +138,7 @@ def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, 
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     with torch.cuda.device(q.device):
         lp = lse.data_ptr() if lse is not None else None
-        if sinks:
-            left, right = window if window is not None else (-1, -1)
-            st = load().fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, B, Sq, Sk, Hq,
-                                     Hkv, D, sc, int(bool(causal)), int(left), int(right), min(int(sinks), 2**31 - 1),
-                                     _DTYPE[q.dtype], _stream_handle(stream))
-        elif window is None:
+        if window is None:
             st = load().fa_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, B, Sq,
                                Sk, Hq, Hkv, D, sc, int(bool(causal)), _DTYPE[q.dtype],
                                _stream_handle(stream))
@@ -148,7 +147,7 @@ def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, 
                                       B, Sq, Sk, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
                                       int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
     if st != FA_OK:
-        raise FaError(st, "fa_fwd_sinks" if sinks else "fa_fwd_window" if window is not None else "fa_fwd")
+        raise FaError(st, "fa_fwd_window" if window is not None else "fa_fwd")
     return out, lse
 
 
@@ -310,14 +309,14 @@ def fa_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, causal: bool = False,
     first keys of a sequence that stay visible left of the window): q [total_q, Hq, D], k/v
     [total_k, Hkv, D], cu_seqlens_q/k int32 [B+1] on the device.  Returns (o [total_q, Hq, D],
     lse [Hq, total_q])."""
+    if sinks:
+        return _fwd_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, window, sinks, out, lse, stream)
     global _varlen_declared
     lib = load()
     if not _varlen_declared:
         P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
         lib.fa_fwd_varlen.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, P]
         lib.fa_fwd_varlen.restype = I
-        lib.fa_fwd_varlen_sinks.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P]
-        lib.fa_fwd_varlen_sinks.restype = I
         _varlen_declared = True
     if q.dtype not in _DTYPE:
         raise TypeError("q/k/v must be bf16 or fp16")
@@ -336,15 +335,12 @@ def fa_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, causal: bool = False,
         lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     with torch.cuda.device(q.device):
-        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(),
-                cu_seqlens_k.data_ptr(), B, total_q, total_k, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
-                int(window[1]))
-        if sinks:
-            st = lib.fa_fwd_varlen_sinks(*args, min(int(sinks), 2**31 - 1), _DTYPE[q.dtype], _stream_handle(stream))
-        else:
-            st = lib.fa_fwd_varlen(*args, _DTYPE[q.dtype], _stream_handle(stream))
+        st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                               lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B,
+                               total_q, total_k, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
+                               int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
     if st != FA_OK:
-        raise FaError(st, "fa_fwd_varlen_sinks" if sinks else "fa_fwd_varlen")
+        raise FaError(st, "fa_fwd_varlen")
     return out, lse
 
 
@@ -713,6 +709,23 @@ def _pool16(k_pages, v_pages, block_table, kv_lens):
             ("block_table", block_table, _I32, device, None), ("kv_lens", kv_lens, _I32, device, (B,)))
 
 
+def _rows16(name, t, dtype, device, H, D):
+    """A tensor of new rows [..., H, D] (H None: any) whose heads are dense: (its shape, its tokens, their
+    stride).  Where the plain case does not hold, _new_rows finds out what to say."""
+    try:
+        if t.dtype is dtype and t.get_device() == device:
+            shape, strides = t.shape, t.stride()
+            if len(shape) == 3:
+                n, heads, d = shape
+                stride, s1, s2 = strides
+                if d == D and s2 == 1 and (heads == H or H is None) and (s1 == D or heads == 1) and n > 1:
+                    return shape, n, stride
+            H = shape[-2] if H is None else H
+    except (AttributeError, IndexError):
+        pass
+    return getattr(t, "shape", None), *_new_rows(name, t, dtype, device, 1 if H is None else H, D)
+
+
 def fa_kv_append_paged_rope(k_new, v_new, k_pages, v_pages, block_table, kv_lens, cos=None, sin=None, q=None,
                             q_out=None, positions=None, cu_seqlens_new=None, interleaved: bool = False, stream=None):
     """Writes new K/V rows into the 16-bit paged cache, keys and queries rotated by their
@@ -728,12 +741,11 @@ def fa_kv_append_paged_rope(k_new, v_new, k_pages, v_pages, block_table, kv_lens
     itself), or None without q."""
     lib = _paged16_lib or _load_paged16()
     dtype, device, num_pages, page, Hkv, D, B, max_pages = _pool16(k_pages, v_pages, block_table, kv_lens)
-    total, k_stride = _new_rows("k_new", k_new, dtype, device, Hkv, D)
-    v_stride = _new_rows("v_new", v_new, dtype, device, Hkv, D)[1]
-    shape = k_new.shape
-    if v_new.shape != shape:
+    shape, total, k_stride = _rows16("k_new", k_new, dtype, device, Hkv, D)
+    v_shape, _, v_stride = _rows16("v_new", v_new, dtype, device, Hkv, D)
+    if v_shape != shape:
         raise ValueError("k_new and v_new must have one shape")
-    cu = None
+    cu = at = None
     if cu_seqlens_new is not None:
         if not _is(cu_seqlens_new, _I32, device, (B + 1,)):
             _refuse(("cu_seqlens_new", cu_seqlens_new, _I32, device, (B + 1,)))
@@ -743,37 +755,40 @@ def fa_kv_append_paged_rope(k_new, v_new, k_pages, v_pages, block_table, kv_lens
     elif len(shape) != 4 or shape[0] != B:
         raise ValueError("without cu_seqlens_new, the new rows are [B, n, H, D]")
     rot = max_pos = 0
+    pc = ps = None
     if cos is not None or sin is not None:
-        if not isinstance(cos, torch.Tensor) or not isinstance(sin, torch.Tensor) or cos.dim() != 2:
-            raise TypeError("cos and sin must both be CUDA tensors [max_pos, rot_dim / 2]")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        if not (_is(cos, _F32, device, None) and _is(sin, _F32, device, cos.shape)):
+        if not (_is(cos, _F32, device, None) and _is(sin, _F32, device, cos.shape) and cos.dim() == 2):
+            if not isinstance(cos, torch.Tensor) or not isinstance(sin, torch.Tensor) or cos.dim() != 2:
+                raise TypeError("cos and sin must both be CUDA tensors [max_pos, rot_dim / 2]")
             _refuse(("cos", cos, _F32, device, None), ("sin", sin, _F32, device, cos.shape))
+        max_pos, rot = cos.shape
+        rot *= 2
         if rot == 0:
             raise ValueError("cos and sin must have rot_dim / 2 >= 8 columns")
-    if positions is not None and not _is(positions, _I32, device, shape[:-2]):
-        if not _is(positions, _I32, device, (total,)):
+        pc, ps = cos.data_ptr(), sin.data_ptr()
+    if positions is not None:
+        if not _is(positions, _I32, device, shape[:-2]) and not _is(positions, _I32, device, (total,)):
             _refuse(("positions", positions, _I32, device, (total,)))
+        at = positions.data_ptr()
     handle, other = _stream_on(device, stream)
     Hq = q_stride = 0
+    pq = po = None
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != len(shape):
-            raise ValueError("q must have as many dimensions as k_new")
-        Hq = q.shape[-2]
-        if q.shape[:-2] != shape[:-2]:
+        q_shape, _, q_stride = _rows16("q", q, dtype, device, None, D)
+        if q_shape[:-2] != shape[:-2]:
             raise ValueError("q must have the tokens of k_new")
-        q_stride = _new_rows("q", q, dtype, device, Hq, D)[1]
+        Hq = q_shape[-2]
         if q_out is None:
-            q_out = _made(q.shape, dtype, q.device, other)
-        elif not _is(q_out, dtype, device, q.shape):
-            _refuse(("q_out", q_out, dtype, device, q.shape))
+            q_out = _made(q_shape, dtype, q.device, other)
+        elif not _is(q_out, dtype, device, q_shape):
+            _refuse(("q_out", q_out, dtype, device, q_shape))
+        if Hq:
+            pq, po = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _call_on(device, lib.fa_kv_append_paged_rope, q.data_ptr() if Hq else None, k_new.data_ptr(), v_new.data_ptr(),
-             q_stride, k_stride, v_stride, q_out.data_ptr() if Hq else None, cu, block_table.data_ptr(),
-             kv_lens.data_ptr(), None if positions is None else positions.data_ptr(), cos.data_ptr() if rot else None,
-             sin.data_ptr() if rot else None, k_pages.data_ptr(), v_pages.data_ptr(), B, total, Hq, Hkv, D, rot,
-             1 if interleaved else 0, max_pos, num_pages, page, max_pages, _DTYPE[dtype], handle)
+    _call_on(device, lib.fa_kv_append_paged_rope, pq, k_new.data_ptr(), v_new.data_ptr(), q_stride, k_stride, v_stride,
+             po, cu, block_table.data_ptr(), kv_lens.data_ptr(), at, pc, ps, k_pages.data_ptr(), v_pages.data_ptr(), B,
+             total, Hq, Hkv, D, rot, 1 if interleaved else 0, max_pos, num_pages, page, max_pages, _DTYPE[dtype], handle)
     return q_out
 
 
@@ -845,3 +860,63 @@ def fa_decode_splitkv_paged_window(q, k_pages, v_pages, block_table, kv_lens, wi
     fa_decode_splitkv_paged_tree.  Returns (o like q, lse fp32 [B, Hq, Sq])."""
     return _decode_paged16("fa_decode_splitkv_paged_window", q, k_pages, v_pages, block_table, kv_lens, None,
                            (min(int(window_left), 2**31 - 1), min(int(sinks), 2**31 - 1)), scale, workspace, out, lse, stream)
+
+
+# ---- the forward with sinks, behind fa_fwd and fa_fwd_varlen.
+def _qkv(q, k, v, dims):
+    """Checks q, k and v of `dims` dimensions; returns (dtype, device index, q's shape, k's shape)."""
+    try:
+        dtype, device, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
+        if (dtype in _DTYPE and device >= 0 and len(qs) == dims and len(ks) == dims and ks[-1] == qs[-1]
+                and (dims == 3 or ks[0] == qs[0]) and q.is_contiguous() and _is(k, dtype, device, ks)
+                and _is(v, dtype, device, ks)):
+            return dtype, device, qs, ks
+    except AttributeError:
+        raise TypeError("q, k and v must be CUDA tensors") from None
+    if dtype not in _DTYPE:
+        raise TypeError("q/k/v must be bf16 or fp16")
+    _refuse_qkv = (("q", q, dtype, device, qs), ("k", k, dtype, device, ks), ("v", v, dtype, device, ks))
+    if len(qs) != dims or len(ks) != dims or ks[-1] != qs[-1] or (dims == 4 and ks[0] != qs[0]):
+        raise ValueError(f"shape mismatch q{tuple(qs)} k{tuple(ks)} v{tuple(v.shape)}")
+    _refuse(*_refuse_qkv)
+
+
+def _outputs(q, dtype, device, out, lse, lse_shape, want_lse, other):
+    """The output tensors, made where they are None."""
+    if out is None:
+        out = _made(q.shape, dtype, q.device, other)
+    elif not _is(out, dtype, device, q.shape):
+        _refuse(("out", out, dtype, device, q.shape))
+    if lse is None:
+        lse = _made(lse_shape, _F32, q.device, other) if want_lse else None
+    elif not _is(lse, _F32, device, lse_shape):
+        _refuse(("lse", lse, _F32, device, lse_shape))
+    return out, lse
+
+
+def _fwd_sinks(q, k, v, causal, scale, window, sinks, out, lse, return_lse, stream):
+    dtype, device, (B, Sq, Hq, D), (_, Sk, Hkv, _) = _qkv(q, k, v, 4)
+    handle, other = _stream_on(device, stream)
+    out, lse = _outputs(q, dtype, device, out, lse, (B, Hq, Sq), return_lse, other)
+    left, right = (-1, -1) if window is None else window
+    _call_on(device, (_lib or load()).fa_fwd_sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+             None if lse is None else lse.data_ptr(), B, Sq, Sk, Hq, Hkv, D,
+             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, min(int(left), 2**31 - 1),
+             min(int(right), 2**31 - 1), min(int(sinks), 2**31 - 1), _DTYPE[dtype], handle)
+    return out, lse
+
+
+def _fwd_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, window, sinks, out, lse, stream):
+    dtype, device, (total_q, Hq, D), (total_k, Hkv, _) = _qkv(q, k, v, 3)
+    n = cu_seqlens_q.shape if isinstance(cu_seqlens_q, torch.Tensor) else None
+    if not (_is(cu_seqlens_q, _I32, device, None) and _is(cu_seqlens_k, _I32, device, n) and len(n) == 1):
+        if n is not None and len(n) != 1:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k must be [B + 1]")
+        _refuse(("cu_seqlens_q", cu_seqlens_q, _I32, device, None), ("cu_seqlens_k", cu_seqlens_k, _I32, device, n))
+    handle, other = _stream_on(device, stream)
+    out, lse = _outputs(q, dtype, device, out, lse, (Hq, total_q), True, other)
+    _call_on(device, (_lib or load()).fa_fwd_varlen_sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+             lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), n[0] - 1, total_q, total_k, Hq, Hkv, D,
+             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, min(int(window[0]), 2**31 - 1),
+             min(int(window[1]), 2**31 - 1), min(int(sinks), 2**31 - 1), _DTYPE[dtype], handle)
+    return out, lse
