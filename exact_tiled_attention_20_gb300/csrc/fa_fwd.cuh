@@ -75,7 +75,20 @@ struct FwdParams {
     const void* q;  // what the tensor maps are of
     const void* k;
     const void* v;
+    unsigned rcp_qb, rcp_hq, rcp_group;  // reciprocals of num_qb, Hq and group (quotient)
 };
+
+// floor(2^32 / d), at most 2^32 - 1: the quotient n / d is umulhi(n, that) or one more.
+inline unsigned reciprocal(int d) { return d <= 1 ? 0xffffffffu : (unsigned)((1ull << 32) / (unsigned)d); }
+__device__ __forceinline__ int quotient(int n, int d, unsigned rcp, int& rest) {
+    int q = (int)__umulhi((unsigned)n, rcp);
+    rest = n - q * d;
+    if (rest >= d) {
+        rest -= d;
+        ++q;
+    }
+    return q;
+}
 
 constexpr int kMaxVarlenB = 1024;
 
@@ -181,7 +194,7 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
     if (vt) {
         // With pairing the prefix counts pairs of query blocks (see pair_tiles).
         int u = t, w = 0;
-        if (p.pair_tiles) {
+        if (!kSink && p.pair_tiles) {
             const int g = (int)gridDim.x;
             w = t / g;
             u = (w >> 1) * g + (t - w * g);
@@ -201,7 +214,7 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
         c.sq = vt->q0[lo + 1] - vt->q0[lo];
         c.sk = vt->k0[lo + 1] - vt->k0[lo];
         nqb = (c.sq + C::NQ * C::BM - 1) / (C::NQ * C::BM);
-        if (p.pair_tiles) {
+        if (!kSink && p.pair_tiles) {
             const int pairs = (nqb + 1) >> 1;
             bh_local = local / pairs;
             const int k = local - bh_local * pairs;
@@ -210,6 +223,12 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
                 c.n_kv = -1;
                 return c;
             }
+        } else if constexpr (kSink) {
+            // local / nqb by way of floats, and put right
+            bh_local = __float2int_rz(__fmul_rn(__int2float_rn(local), __frcp_rn(__int2float_rn(nqb))));
+            qb_raw = local - bh_local * nqb;
+            for (; qb_raw < 0; qb_raw += nqb) --bh_local;
+            for (; qb_raw >= nqb; qb_raw -= nqb) ++bh_local;
         } else {
             qb_raw = local % nqb;
             bh_local = local / nqb;
@@ -223,7 +242,7 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
     } else {
         nqb = p.num_qb;
         int bh;
-        if (p.pair_tiles) {
+        if (!kSink && p.pair_tiles) {
             const int g = (int)gridDim.x;
             const int w = t / g;
             const int pairs = (nqb + 1) >> 1;
@@ -237,12 +256,18 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
                 c.n_kv = -1;
                 return c;
             }
+        } else if constexpr (kSink) {
+            bh = quotient(t, nqb, p.rcp_qb, qb_raw);
         } else {
             qb_raw = t % nqb;
             bh = t / nqb;
         }
-        c.h = bh % p.Hq;
-        c.b = bh / p.Hq;
+        if constexpr (kSink) {
+            c.b = quotient(bh, p.Hq, p.rcp_hq, c.h);
+        } else {
+            c.h = bh % p.Hq;
+            c.b = bh / p.Hq;
+        }
         c.sq = p.Sq;
         c.sk = p.Sk;
         c.q_base = 0;
@@ -253,7 +278,12 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
     }
     // causal: the longest query block of each head first
     const int qb = p.causal ? (nqb - 1 - qb_raw) : qb_raw;
-    c.hk = c.h / p.group;
+    if constexpr (kSink) {
+        int rest;
+        c.hk = quotient(c.h, p.group, p.rcp_group, rest);
+    } else {
+        c.hk = c.h / p.group;
+    }
     c.m0 = qb * (C::NQ * C::BM);
     const int off = c.sk - c.sq;
     const int last_row = min(c.sq, c.m0 + C::NQ * C::BM) - 1;
@@ -273,6 +303,26 @@ __device__ __forceinline__ TileCoord decode_tile(const FwdParams& p, const Varle
         if constexpr (kSink) c.ns = 0;
     }
     return c;
+}
+
+// The products of a tile's first block where it holds at most 32 sinks and nothing else that is
+// visible: S and P.V of one sub-tile over 32 keys, out of line and apart from the others, whose rate
+// of issue counts.  d and a: TMEM columns or the low word of a descriptor, as there.
+template <class C, bool kBF16>
+__device__ __noinline__ void sink_s(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi) {
+    constexpr uint32_t idesc = make_idesc_f16(128, 32, kBF16, false, false);
+    umma_ss_elect<false>(d, a, a_hi, b, b_hi, idesc);
+#pragma unroll 1
+    for (int kk = 1; kk < C::D / 16; ++kk)
+        umma_ss_elect<true>(d, a + (((kk >> 2) * (C::BM * 128) + (kk & 3) * 32) >> 4), a_hi,
+                            b + (((kk >> 2) * (C::BN * 128) + (kk & 3) * 32) >> 4), b_hi, idesc);
+}
+
+template <class C, bool kBF16>
+__device__ __noinline__ void sink_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi) {
+    constexpr uint32_t idesc = make_idesc_f16(128, C::D, kBF16, false, true);
+    umma_ts_elect<false>(d, a, b, b_hi, idesc);
+    umma_ts_elect<true>(d, a + 8, b + ((16 * 128) >> 4), b_hi, idesc);
 }
 
 // The K/V block of index j of a tile's n_kv.
@@ -391,12 +441,16 @@ __device__ __noinline__ void sink_row(const uint16_t* q, const uint16_t* k, cons
 
 constexpr int kSinkRowKeys = 1 << 20;  // rows that see more keys are not done again (bounded time)
 
-template <class C, bool kBF16, bool kVarlen, bool kSkip = false, bool kSink = false>
+// kSinks: 0 for none; 1; or 2 for at most 32, whose block is then a short one (two Q tiles with P over S:
+// [2, 8192, 32, 128], window 1024, 4 sinks 309 -> 295 us; for more sinks the code that this adds costs
+// the others: with 64 309 -> 314, 8 packed prompts 268 -> 278).
+template <class C, bool kBF16, bool kVarlen, bool kSkip = false, int kSinks = 0>
 __global__ void __launch_bounds__(C::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const FwdParams p) {
     using L = typename C::template Layout<kVarlen>;
+    constexpr bool kSink = kSinks > 0, kShort = kSinks == 2;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t base = (raw_u32 + 1023u) & ~1023u;
@@ -561,20 +615,32 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32);
             const uint32_t k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
             const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
-            auto issue_s = [&](int q, uint32_t kst, uint32_t slot) {
+            auto issue_s = [&](int q, uint32_t kst, uint32_t slot, bool few = false) {
                 const uint32_t d = tmem + slot * C::BN;
                 const uint32_t a = q_lo + (uint32_t)((q * C::kQBytes) >> 4);
                 const uint32_t b = k_lo + ((kst * C::kKVBytes) >> 4);
+                if constexpr (kShort) {
+                    if (few) {
+                        sink_s<C, kBF16>(d, a, q_hi, b, k_hi);
+                        return;
+                    }
+                }
                 umma_ss_elect<false>(d, a, q_hi, b, k_hi, idesc_s);
 #pragma unroll
                 for (int kk = 1; kk < C::D / 16; ++kk)
                     umma_ss_elect<true>(d, a + (((kk >> 2) * (C::BM * 128) + (kk & 3) * 32) >> 4), q_hi,
                                         b + (((kk >> 2) * (C::BN * 128) + (kk & 3) * 32) >> 4), k_hi, idesc_s);
             };
-            auto issue_pv = [&](int q, uint32_t vst, uint32_t slot, bool acc) {
+            auto issue_pv = [&](int q, uint32_t vst, uint32_t slot, bool acc, bool few = false) {
                 const uint32_t d = tmem + C::kOCol0 + q * C::D;
                 const uint32_t a = C::kSAhead ? tmem + C::kPCol0 + q * (C::BN / 2) : tmem + slot * C::BN;
                 const uint32_t b = v_lo + ((vst * C::kKVBytes) >> 4);
+                if constexpr (kShort) {
+                    if (few) {
+                        sink_pv<C, kBF16>(d, a, b, v_hi);
+                        return;
+                    }
+                }
                 if (acc)
                     umma_ts_elect<true>(d, a, b, v_hi, idesc_o);
                 else
@@ -582,6 +648,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
                 for (int kk = 1; kk < C::BN / 16; ++kk)
                     umma_ts_elect<true>(d, a + kk * 8, b + ((kk * (16 * 128)) >> 4), v_hi, idesc_o);
+            };
+            // Whether block j of a tile is one of sinks alone.
+            auto few_keys = [&](const TileCoord& c, int j) -> bool {
+                if constexpr (kShort) return j == 0 && c.ns == 1;
+                return false;
             };
             auto slot_of = [&](int q, uint32_t iter) -> uint32_t {
                 return C::NQ == 1 ? (iter & 1u) : (uint32_t)q;
@@ -670,7 +741,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     ok = wait(bar(C::kBarKFull + st), (kv_it / C::NS) & 1u);
                     if (!ok) break;
                     for (int q = 0; q < C::NQ; ++q) {
-                        if (live(q, 0)) issue_s(q, st, slot_of(q, it));
+                        if (live(q, 0)) issue_s(q, st, slot_of(q, it), few_keys(c, 0));
                         umma_commit_elect(bar(C::kBarSFull + slot_of(q, it)));
                     }
                     if (!C::kRingBySoftmax) umma_commit_elect(bar(C::kBarKEmpty + st));
@@ -700,7 +771,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         // the sub-tile's first live block initialises O
-                        if (live(q, j)) issue_pv(q, st, slot_of(q, it), j > (kSkip && !kSink ? blo[q] : 0));
+                        if (live(q, j)) issue_pv(q, st, slot_of(q, it), j > (kSkip && !kSink ? blo[q] : 0), few_keys(c, j));
                         if (kOPerIter || j + 1 == n) umma_commit_elect(bar(C::kBarODone + q));
                         if (C::NQ > 1 && more) {
                             if (q == 0) {
@@ -823,6 +894,45 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const uint32_t tS = lane_base + slot * C::BN;
                 // P goes over S, or into its own columns with kSAhead.
                 const uint32_t tP = C::kSAhead ? lane_base + C::kPCol0 + q * (C::BN / 2) : tS;
+                if constexpr (kShort) {
+                    if (j == 0 && c.ns == 1) {
+                        // A block of at most 32 sinks.
+                        const int kmax = p.has_hi ? min(c.sk - 1, row + off + p.hi_off) : c.sk - 1;
+                        uint32_t u[32], pk[16];
+                        tmem_ld_32x32b_x32(tS, u);
+                        const uint32_t w = bits_between(0, min(p.sinks - 1, kmax));
+                        tmem_wait_ld(u);
+                        float m4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) u[k] = (w >> k) & 1u ? u[k] : 0xff800000u;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+#pragma unroll
+                            for (int c4 = 0; c4 < 4; ++c4)
+                                m4[c4] = max3f(m4[c4], __uint_as_float(u[k + c4]), __uint_as_float(u[k + c4 + 4]));
+                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        m_run = mx == kNegInf ? kNegInf : mx * p.scale_log2;
+                        const float m_sub = m_run == kNegInf ? 0.f : m_run;
+                        const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t a =
+                                fma2(f2_pack(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), c2, nm2);
+                            float a0, a1;
+                            f2_unpack(a, a0, a1);
+                            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+                            l2 = add2(l2, f2_pack(p0, p1));
+                            pk[k] = pack2<kBF16>(p0, p1);
+                        }
+                        tmem_st_32x32b_x16(tP, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::kBarPFull + q));
+                        ++it;
+                        continue;
+                    }
+                }
                 // All chunks of S are loaded before a single wait.
                 uint32_t u[kSC][32];
 #pragma unroll
@@ -972,7 +1082,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 // so its completion (awaited above) implies that P.V has completed; with
                 // kSAhead that P.V was awaited before the P stores.
                 if (j > (kSkip && !kSink ? blo : 0) && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll
+#pragma unroll(kSink ? 1 : C::D / 32)  // (rare; the code has to stay small)
                     for (int ch = 0; ch < C::D / 32; ++ch) {
                         uint32_t ov[32];
                         tmem_ld_32x32b_x32(tO + ch * 32, ov);
@@ -1171,8 +1281,9 @@ inline bool causal_pairs_balance_better(long long heads, int nqb, int sms) {
     return max_pr < max_rr;
 }
 
-// Host launcher for one configuration; kSink: with sinks, a window on the left and sinks > 0.
-template <class C, bool kSink = false>
+// Host launcher for one configuration; kSink: with sinks, a window on the left and sinks > 0 (kSinks as
+// the kernel's).
+template <class C, bool kSink = false, int kSinks = 1>
 fa_status launch_fwd_cfg(const FwdArgs& a, cudaStream_t stream) {
     static int attr_bf16[64] = {0};
     static int attr_f16[64] = {0};
@@ -1240,12 +1351,15 @@ fa_status launch_fwd_cfg(const FwdArgs& a, cudaStream_t stream) {
     p.q = a.q;
     p.k = a.k;
     p.v = a.v;
+    p.rcp_qb = reciprocal(p.num_qb);
+    p.rcp_hq = reciprocal(a.Hq);
+    p.rcp_group = reciprocal(p.group);
     if constexpr (kSink) {
         // Two Q tiles with P over S skip a sub-tile's blocks, packed batches too.
         constexpr bool kSkip = C::NQ == 2 && !C::kSAhead;
-        auto kern = varlen ? (a.bf16 ? fa_fwd_kernel<C, true, true, kSkip, true> : fa_fwd_kernel<C, false, true, kSkip, true>)
-                           : (a.bf16 ? fa_fwd_kernel<C, true, false, kSkip, true>
-                                     : fa_fwd_kernel<C, false, false, kSkip, true>);
+        auto kern = varlen ? (a.bf16 ? fa_fwd_kernel<C, true, true, kSkip, kSinks> : fa_fwd_kernel<C, false, true, kSkip, kSinks>)
+                           : (a.bf16 ? fa_fwd_kernel<C, true, false, kSkip, kSinks>
+                                     : fa_fwd_kernel<C, false, false, kSkip, kSinks>);
         const int smem = varlen ? C::template Layout<true>::kSmemBytes : C::template Layout<false>::kSmemBytes;
         int* flags = varlen ? (a.bf16 ? attr_bf16_v : attr_f16_v) : (a.bf16 ? attr_bf16 : attr_f16);
         if (!ensure_smem_attr((const void*)kern, smem, flags)) return FA_ERR_CUDA;

@@ -39,8 +39,7 @@
 
 namespace fa {
 
-// 4-D map over [dim3][dim2][dim1][dim0] in 16 bits, box (64, box1, box2, 1), 128-byte swizzle;
-// encoded anew for each call.
+// 4-D map over [dim3][dim2][dim1][dim0] in 16 bits, box (64, box1, box2, 1), 128-byte swizzle.
 bool encode_paged_tmap(CUtensorMap* map, const void* base, bool bf16, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                        uint64_t dim3, uint32_t box1, uint32_t box2);
 

@@ -3,7 +3,10 @@
 
 namespace fa {
 
+fa_status launch_sinks_few_d128(const FwdArgs& a, cudaStream_t s);
+
 fa_status launch_sinks_d128(const FwdArgs& a, cudaStream_t s) {
+    if (a.sinks <= 32) return launch_sinks_few_d128(a, s);
     return launch_fwd_cfg<FwdConfig<128, 128, 2, 2>, true>(a, s);
 }
 
