@@ -49,6 +49,7 @@ struct PagedDecParams {
     int row_blocks;      // of a (sequence, kv head)
     int g, rg;           // heads and row blocks of an entry: G = g * rg CTAs work on a range
     int groups, blocks;  // entries of a sequence: groups of heads, by row blocks over rg
+    int merge_ctas;      // of a range and member
     int ranges, whole;   // whole: entries are not cut, a range has those that begin in it
     int capacity, page_size, num_pages, max_pages, box_rows;
     int nb_log;           // log2 of the boxes of a tile, BN / box_rows
@@ -872,131 +873,139 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
     }
 }
 
-// Joins the pieces of each row (b, token, head): lse = log sum_c exp(lse_c), and the outputs
-// weighted with exp(lse_c - lse).  WPR warps share a row, each taking every WPR-th piece; a lane
-// holds D / 32 dims.  The CTAs walk over the rows, and make the plan once, before the split kernel
-// is done.
-template <int D, int NQ, int WPR, bool kBF16>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedDecParams p) {
-    constexpr int V = D / 32, Rows = 8 / WPR, NP = 4;
+// Joins the pieces of the entries that were cut: lse = log sum_c exp(lse_c), and the outputs weighted
+// with exp(lse_c - lse).  p.merge_ctas CTAs for each of the split kernel's: they walk the same range,
+// and of each cut entry that they meet they join the share of the rows that the CTAs of the entry's
+// other pieces do not.
+// Eight warps take a row each, or share one where there are few; a lane holds D / 32 dims.  The
+// plan is made before the split kernel is done.
+template <int D, int NQ, bool kBF16>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedDecParams p) {
     using C = PagedCfg<D, NQ>;
+    constexpr int V = D / 32, NP = V <= 4 ? 2 : 4;  // NP: pieces loaded together
     constexpr int Vec = V % 4 == 0 ? 4 : V % 2 == 0 ? 2 : 1;  // values of a lane side by side
-    __shared__ __align__(16) float s_acc[WPR > 1 ? 8 : 1][D];
+    __shared__ __align__(16) float s_acc[8][D];
     __shared__ float s_sum[8], s_max[8];
     __shared__ int s_warp_sum[8];
-    extern __shared__ int s_plan[];  // as large as the batch: the next call's split kernel fits beside this
-    int *s_len = s_plan, *s_prefix = s_plan + p.B;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR;
+    extern __shared__ int s_plan[];  // as large as the batch: the CTA fits beside the split kernels'
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float kNegInf = -__int_as_float(0x7f800000);
-    paged_make_plan<C, 256>(p, s_len, s_prefix, s_warp_sum);
-    const int W = paged_width<C>(p, s_prefix[p.B]), block_rows = min(NQ * p.T, p.Sq) * p.group;
-    const int rows = p.B * p.Sq * p.Hq;
+    paged_make_plan<C, 256>(p, s_plan, s_plan + p.B, s_warp_sum);
+    const int G = p.g * p.rg, k = p.merge_ctas, cta = (int)blockIdx.x / k, sub = (int)blockIdx.x - cta * k;
+    const int rng = cta / G, member = cta - rng * G;
+    const int block_rows = min(NQ * p.T, p.Sq) * p.group;
+    PagedWalk<C> walk;
+    walk.init(p, s_plan, s_plan + p.B, rng, member);
+    PagedSeg seg;
+    bool waited = false;
     grid_launch_dependents();
-    grid_dependency_wait();
-    for (int row = (int)blockIdx.x * Rows + warp / WPR; row < rows; row += (int)gridDim.x * Rows) {
-        const int seq_tok = row / p.Hq, h = row - seq_tok * p.Hq, b = seq_tok / p.Sq, tok = seq_tok - b * p.Sq;
-        const int hk = h / p.group, rb = tok / (NQ * p.T), units = s_prefix[b + 1] - s_prefix[b];
-        const int block = rb / p.rg, e = hk / p.g * p.blocks + block, member = hk % p.g + (rb - block * p.rg) * p.g;
-        const int start = p.groups * p.blocks * s_prefix[b] + e * units;
-        // Rows with one piece or none have been written by the split kernel.  n is the same in all of a
-        // row's warps.
-        const int n = paged_pieces<C>(start, units, W), first = paged_first_piece<C>(start, W);
-        if (n < 2) continue;
-        const int in_block = (tok - rb * NQ * p.T) * p.group + h - hk * p.group;
-        float acc[V], s = 0.f, m = kNegInf;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        for (int c0 = part; c0 < n; c0 += WPR * NP) {
-            float w[NP], v[NP][V], top = m;
-#pragma unroll
-            for (int u = 0; u < NP; ++u) {
-                const int c = c0 + u * WPR;
-                w[u] = kNegInf;
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[u][i] = 0.f;
-                if (c >= n) continue;
-                const size_t at =
-                    ((size_t)member * 2 * p.ranges + paged_slot(p, first + c, c == 0)) * block_rows + in_block;
-                w[u] = p.lse_part[at];
-#pragma unroll
-                for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
-            }
-#pragma unroll
-            for (int u = 0; u < NP; ++u) top = fmaxf(top, w[u]);
-            const float ref = top == kNegInf ? 0.f : top;
-            const float f = ex2_approx((m - ref) * (1.f / kPagedLn2));
-            m = top;
-            s *= f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] *= f;
-#pragma unroll
-            for (int u = 0; u < NP; ++u) {
-                const float x = ex2_approx((w[u] - ref) * (1.f / kPagedLn2));
-                s += x;
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(x, v[u][i], acc[i]);
-            }
+    while (walk.next(p, seg)) {
+        if (!seg.cut) continue;
+        const int n = paged_pieces<C>(walk.start, walk.units, walk.W);
+        const int first = paged_first_piece<C>(walk.start, walk.W), piece = (rng - first) * k + sub;
+        const int tok0 = seg.rb * NQ * p.T;
+        const int rows = min(block_rows, (p.Sq - tok0) * p.group);  // of this row block
+        const int lo = (int)((unsigned)(rows * piece) / (unsigned)(n * k));
+        const int hi = (int)((unsigned)(rows * (piece + 1)) / (unsigned)(n * k));
+        const int share = hi - lo > 4 ? 1 : hi - lo > 2 ? 2 : hi - lo > 1 ? 4 : 8;  // warps of a row
+        const int part = warp & (share - 1);
+        if (!waited) {
+            grid_dependency_wait();
+            waited = true;
         }
-        if constexpr (WPR > 1) {
-            __syncthreads();  // the row before has been read
-#pragma unroll
-            for (int i = 0; i < V; ++i) s_acc[warp][i / Vec * Vec * 32 + lane * Vec + i % Vec] = acc[i];
-            if (lane == 0) {
-                s_sum[warp] = s;
-                s_max[warp] = m;
-            }
-            __syncthreads();
-            if (warp != 0) continue;
-#pragma unroll
-            for (int w = 1; w < WPR; ++w) m = fmaxf(m, s_max[w]);
-            s = 0.f;
+        for (int r0 = lo; r0 < hi; r0 += 8 / share) {
+            const int r = r0 + warp / share;
+            const bool in = r < hi;
+            const size_t base = (size_t)member * 2 * p.ranges * block_rows + (in ? r : lo);
+            float acc[V], s = 0.f, m = kNegInf;
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = 0.f;
-            const float ref = m == kNegInf ? 0.f : m;
+            for (int c0 = part; c0 < n; c0 += share * NP) {
+                float w[NP], v[NP][V], top = m;
 #pragma unroll
-            for (int w = 0; w < WPR; ++w) {
-                const float f = ex2_approx((s_max[w] - ref) * (1.f / kPagedLn2));
-                s += f * s_sum[w];
+                for (int u = 0; u < NP; ++u) {
+                    const int c = c0 + u * share;
+                    w[u] = kNegInf;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    acc[i] = fmaf(f, s_acc[w][i / Vec * Vec * 32 + lane * Vec + i % Vec], acc[i]);
+                    for (int i = 0; i < V; ++i) v[u][i] = 0.f;
+                    if (c >= n) continue;
+                    const size_t at = base + (size_t)paged_slot(p, first + c, c == 0) * block_rows;
+                    w[u] = p.lse_part[at];
+#pragma unroll
+                    for (int i = 0; i < V; i += Vec) load_vec<Vec>(v[u] + i, p.o_part + at * D + i * 32 + lane * Vec);
+                }
+#pragma unroll
+                for (int u = 0; u < NP; ++u) top = fmaxf(top, w[u]);
+                const float ref = top == kNegInf ? 0.f : top;
+                const float f = ex2_approx((m - ref) * (1.f / kPagedLn2));
+                m = top;
+                s *= f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] *= f;
+#pragma unroll
+                for (int u = 0; u < NP; ++u) {
+                    const float x = ex2_approx((w[u] - ref) * (1.f / kPagedLn2));
+                    s += x;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(x, v[u][i], acc[i]);
+                }
             }
-        }
-        const float inv = 1.f / s;  // s == 0: no piece holds a visible key
+            if (share > 1) {
+                __syncthreads();  // the rows before have been read
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = s == 0.f ? 0.f : acc[i] * inv;
-        uint16_t* out = static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * Vec;
+                for (int i = 0; i < V; ++i) s_acc[warp][i / Vec * Vec * 32 + lane * Vec + i % Vec] = acc[i];
+                if (lane == 0) {
+                    s_sum[warp] = s;
+                    s_max[warp] = m;
+                }
+                __syncthreads();
+                if (part != 0) continue;
+                for (int w = 1; w < share; ++w) m = fmaxf(m, s_max[warp + w]);
+                s = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; i += Vec) {
-            if constexpr (Vec == 1)
-                out[i * 32] = float_to16<kBF16>(acc[i]);
-            else if constexpr (Vec == 2)
-                *reinterpret_cast<uint32_t*>(out + i * 32) = pack2<kBF16>(acc[i], acc[i + 1]);
-            else
-                *reinterpret_cast<uint2*>(out + i * 32) =
-                    make_uint2(pack2<kBF16>(acc[i], acc[i + 1]), pack2<kBF16>(acc[i + 2], acc[i + 3]));
+                for (int i = 0; i < V; ++i) acc[i] = 0.f;
+                const float ref = m == kNegInf ? 0.f : m;
+                for (int w = 0; w < share; ++w) {
+                    const float f = ex2_approx((s_max[warp + w] - ref) * (1.f / kPagedLn2));
+                    s += f * s_sum[warp + w];
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        acc[i] = fmaf(f, s_acc[warp + w][i / Vec * Vec * 32 + lane * Vec + i % Vec], acc[i]);
+                }
+            }
+            if (!in) continue;
+            const int tok_l = r / p.group, h = seg.hk * p.group + r - tok_l * p.group, tok = tok0 + tok_l;
+            const float inv = 1.f / s;  // s == 0: no piece holds a visible key
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = s == 0.f ? 0.f : acc[i] * inv;
+            uint16_t* out = static_cast<uint16_t*>(p.o) + (((size_t)seg.b * p.Sq + tok) * p.Hq + h) * D + lane * Vec;
+#pragma unroll
+            for (int i = 0; i < V; i += Vec) {
+                if constexpr (Vec == 1)
+                    out[i * 32] = float_to16<kBF16>(acc[i]);
+                else if constexpr (Vec == 2)
+                    *reinterpret_cast<uint32_t*>(out + i * 32) = pack2<kBF16>(acc[i], acc[i + 1]);
+                else
+                    *reinterpret_cast<uint2*>(out + i * 32) =
+                        make_uint2(pack2<kBF16>(acc[i], acc[i + 1]), pack2<kBF16>(acc[i + 2], acc[i + 3]));
+            }
+            if (p.lse && lane == 0)
+                p.lse[((size_t)seg.b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kPagedLn2;
         }
-        if (p.lse && lane == 0)
-            p.lse[((size_t)b * p.Hq + h) * p.Sq + tok] = s == 0.f ? kNegInf : m + lg2_approx(s) * kPagedLn2;
     }
+    // No CTA may be done before the split kernel is: the next kernel's wait is for this one.
+    if (!waited) grid_dependency_wait();
 }
 
-// CTAs of the merge on an SM: what 256 threads of some 64 registers leave room for beside the split
-// kernel's last CTA.
-constexpr int kPagedMergeCtas = 4;
-
-template <int D, int NQ, int WPR>
-fa_status launch_paged_merge(const PagedDecParams& p, bool bf16, int num_sms, cudaStream_t s) {
+template <int D, int NQ>
+fa_status launch_paged_merge(const PagedDecParams& p, bool bf16, cudaStream_t s) {
     static int attr[64] = {0};
-    if (!prefer_shared((const void*)paged_merge_kernel<D, NQ, WPR, true>,
-                       (const void*)paged_merge_kernel<D, NQ, WPR, false>, attr))
+    if (!prefer_shared((const void*)paged_merge_kernel<D, NQ, true>, (const void*)paged_merge_kernel<D, NQ, false>, attr))
         return FA_ERR_CUDA;
-    const long long rows = (long long)p.B * p.Sq * p.Hq;
-    const unsigned grid =
-        (unsigned)std::min((rows + 8 / WPR - 1) / (8 / WPR), (long long)num_sms * (WPR > 1 ? 8 : kPagedMergeCtas));
+    const unsigned grid = (unsigned)(p.ranges * p.g * p.rg * p.merge_ctas);
     const size_t smem = PagedCfg<D, NQ>::plan_bytes(p.B);
-    return bf16 ? launch_overlapped(paged_merge_kernel<D, NQ, WPR, true>, grid, 256, smem, s, p)
-                : launch_overlapped(paged_merge_kernel<D, NQ, WPR, false>, grid, 256, smem, s, p);
+    return bf16 ? launch_overlapped(paged_merge_kernel<D, NQ, true>, grid, 256, smem, s, p)
+                : launch_overlapped(paged_merge_kernel<D, NQ, false>, grid, 256, smem, s, p);
 }
 
 template <int D, int NQ, bool kBF16>
@@ -1048,6 +1057,8 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     p.whole = most + C::Lead <= C::MinWidth ? 1 : 0;
     p.ranges = (int)std::min((long long)(a.num_sms / G), (units + C::MinWidth - 1) / C::MinWidth);
+    // A row takes a warp two trips to L2, so more rows are taken by more CTAs.
+    p.merge_ctas = std::max(1, std::min(4, std::min(NQ * p.T, p.Sq) * p.group / 16));
     CUtensorMap tq, tk, tv;
     if (!encode_paged_tmap(&tq, a.q, a.bf16, D, a.Hq, a.Sq, a.B, p.group, p.T) ||
         !encode_paged_tmap(&tk, a.k_pages, a.bf16, D, a.Hkv, a.page_size, a.num_pages, 1, p.box_rows) ||
@@ -1056,9 +1067,7 @@ fa_status launch_paged_nq(const PagedDecodeArgs& a, cudaStream_t s) {
     const fa_status st = a.bf16 ? launch_paged_split<D, NQ, true>(tq, tk, tv, p, s)
                                 : launch_paged_split<D, NQ, false>(tq, tk, tv, p, s);
     if (st != FA_OK || p.whole) return st;
-    // Few rows are cut into many pieces: eight warps each.
-    return (long long)a.B * a.Sq * a.Hq <= 8 * a.num_sms ? launch_paged_merge<D, NQ, 8>(p, a.bf16, a.num_sms, s)
-                                                         : launch_paged_merge<D, NQ, 1>(p, a.bf16, a.num_sms, s);
+    return launch_paged_merge<D, NQ>(p, a.bf16, s);
 }
 
 // Two sub-tiles share each key tile where one does not hold a kv head's rows (at D = 256 TMEM has
