@@ -303,6 +303,14 @@ __device__ __forceinline__ float paged_from16(uint32_t x) {
     }
 }
 
+// Sends for a tensor map's box to L2.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
 // Page and row within it of key `key` of sequence b; page -1: none.
 __device__ __forceinline__ int2 paged_place(const PagedDecParams& p, int b, int key) {
     unsigned pi = __umulhi((unsigned)key, p.page_recip);  // the quotient, or one more
@@ -311,7 +319,7 @@ __device__ __forceinline__ int2 paged_place(const PagedDecParams& p, int b, int 
         --pi;
         row += p.page_size;
     }
-    const int page = __ldg(p.table + (size_t)b * p.max_pages + pi);
+    const int page = __ldcg(p.table + (size_t)b * p.max_pages + pi);  // (past L1: it may be read before the wait)
     return make_int2(page >= 0 && page < p.num_pages ? page : -1, row);
 }
 
@@ -446,7 +454,17 @@ __global__ void __launch_bounds__(PagedCfg<D, NQ>::kThreads, 1)
         paged_make_plan<C, C::kThreads>(p, plan_len, plan_prefix, s_warp_sum);
         walk.init(p, plan_len, plan_prefix, rng, member);
         if (producer) more = walk.next(p, s);
-        if (first) grid_dependency_wait();
+        if (first) {
+            // The first tile is sent for to L2, by a table that may yet change too: a guess, which decides
+            // nothing but the lines that go there.
+            if (more) {
+                const int2 guess = fetch(s, s.u0);
+                const int page = __shfl_sync(0xffffffffu, guess.x, box), row = __shfl_sync(0xffffffffu, guess.y, box);
+                if (ahead < DA && page >= 0)
+                    tma_prefetch_4d(warp == C::kProducerWarp ? &tm_k : &tm_v, ahead * 64, s.hk, row, page);
+            }
+            grid_dependency_wait();
+        }
         if (more) ids = fetch(s, s.u0);
         // (every warp by itself: after the wait all see the same lengths)
         bool stale = false;
