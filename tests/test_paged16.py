@@ -173,6 +173,99 @@ def test_window_matches_the_reference(fa, case):
     check(o, lse, q, pool, lambda b, n: paged16.sees_window(n, Sq, left, sinks), 1 / math.sqrt(D), dtype)
 
 
+# The forms for few and for many rows of a kv head, each with several short sequences per CTA.
+# (Sq, Hq, Hkv, D, page, window, sinks, dtype)
+BATCHES = [
+    (1, 4, 1, 128, 16, 600, 4, "bf16"),       # 4 rows
+    (4, 8, 2, 128, 64, 1023, 33, "fp16"),     # 16 rows, the most of one form
+    (17, 2, 2, 128, 32, 500, 1, "bf16"),      # 17, the least of the other
+    (2, 16, 2, 64, 48, -1, 0, "fp16"),
+    (3, 3, 1, 96, 16, 300, 200, "bf16"),
+    (4, 8, 2, 256, 64, 700, 4, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", BATCHES, ids=lambda c: f"sq{c[0]}_h{c[1]}_{c[2]}_d{c[3]}_w{c[5]}_s{c[6]}_{c[7]}")
+def test_many_short_sequences(fa, case):
+    """More sequences than CTAs, of 0 to 1400 keys, under a window and under a tree, over and over:
+    the buffers of one are handed to the next."""
+    Sq, Hq, Hkv, D, page, left, sinks, dtype = case
+    B = 230
+    rng = np.random.default_rng(D + Sq)
+    lens = [int(n) for n in rng.integers(0, 1400, B)]
+    pool = Pool(B, Hkv, D, page, lens, dtype, seed=5).fill()
+    q = queries(pool, B, Sq, Hq, D, dtype)
+    tree = paged16.random_trees(rng, B, Sq)
+    qd, gpu, mask = q.to(DEV), pool.gpu(), torch.from_numpy(paged16.pack_tree(tree)).to(DEV)
+    first = fa.fa_decode_splitkv_paged_window(qd, *gpu, left, sinks=sinks)
+    t_first = fa.fa_decode_splitkv_paged_tree(qd, *gpu, mask)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        again = fa.fa_decode_splitkv_paged_window(qd, *gpu, left, sinks=sinks)
+        t_again = fa.fa_decode_splitkv_paged_tree(qd, *gpu, mask)
+        torch.cuda.synchronize()
+        for a, b in zip((*first, *t_first), (*again, *t_again)):
+            assert torch.equal(a, b)
+    check(*first, q, pool, lambda b, n: paged16.sees_window(n, Sq, left, sinks), 1 / math.sqrt(D), dtype)
+    check(*t_first, q, pool, lambda b, n: paged16.sees_tree(n, Sq, tree[b]), 1 / math.sqrt(D), dtype)
+
+
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("Sq,D", [(2, 64), (4, 128), (8, 128), (5, 96), (3, 256), (40, 128)])
+def test_scores_that_rise_or_fall_along_the_sequence(fa, Sq, D, rising):
+    """Keys that grow, or shrink, by a factor of 200 along the sequence: the references of the softmax
+    are raised again and again, the early keys' weights going to zero, or never."""
+    lens = [1900, 700, 64]
+    pool = Pool(3, 2, D, 32, lens, "bf16", seed=D).fill()
+    t = pool.table.numpy()
+    for b, n in enumerate(lens):
+        for j in range(n):
+            at = j if rising else n - 1 - j
+            pool.cpu[0][int(t[b][j // 32]), j % 32] *= 10.0 * 200.0 ** (at / n - 1)
+    q = queries(pool, 3, Sq, 8, D, "bf16")
+    o, lse = fa.fa_decode_splitkv_paged_window(q.to(DEV), *pool.gpu())
+    torch.cuda.synchronize()
+    check(o, lse, q, pool, lambda b, n: paged16.sees_window(n, Sq, -1, 0), 1 / math.sqrt(D), "bf16")
+
+
+@pytest.mark.parametrize("Sq", [1, 9])
+def test_lengths_outside_the_table_are_clamped(fa, Sq):
+    pool = Pool(3, 2, 128, 16, [64, 0, 33], "bf16", seed=Sq, max_pages=4).fill()
+    q = queries(pool, 3, Sq, 4, 128, "bf16")
+    kp, vp, table, kl = pool.gpu()
+    want = fa.fa_decode_splitkv_paged_window(q.to(DEV), kp, vp, table, kl, 50, sinks=3)
+    wrong = torch.tensor([2 ** 31 - 1, -2 ** 31, 33], dtype=torch.int32, device=DEV)
+    got = fa.fa_decode_splitkv_paged_window(q.to(DEV), kp, vp, table, wrong, 50, sinks=3)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_pages_past_two_to_the_32_values(fa):
+    """Pools of more than 2^32 values each, the sequences' pages at their far ends."""
+    D, Hkv, page, Sq, Hq = 128, 8, 256, 2, 16
+    each = page * Hkv * D
+    pages = 2 ** 32 // each + 8
+    if torch.cuda.mem_get_info()[0] < 5 * pages * each:
+        pytest.skip("not enough memory")
+    small = Pool(2, Hkv, D, page, [700, 300], "bf16", seed=3).fill()
+    kp, vp, table, kl = small.gpu()
+    wide = [torch.empty((pages, page, Hkv, D), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    far = torch.where(table < 4, table, table + (pages - kp.shape[0]))   # most at the far end
+    for big, p in zip(wide, (kp, vp)):
+        big[:4], big[4 - p.shape[0]:] = p[:4], p[4:]
+    new = torch.randn((2, 2, Sq, Hkv, D), generator=small.gen).to(torch.bfloat16).to(DEV)
+    q = queries(small, 2, Sq, Hq, D, "bf16").to(DEV)
+    kp, vp = kp.clone(), vp.clone()
+    for k, v, t in ((kp, vp, table), (*wide, far)):
+        fa.fa_kv_append_paged_rope(new[0], new[1], k, v, t, kl)
+    want = fa.fa_decode_splitkv_paged_window(q, kp, vp, table, kl, 400, sinks=5)
+    got = fa.fa_decode_splitkv_paged_window(q, *wide, far, kl, 400, sinks=5)
+    torch.cuda.synchronize()
+    for big, p in zip(wide, (kp, vp)):
+        assert torch.equal(big[4 - p.shape[0]:].view(torch.int16), p[4:].view(torch.int16))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_pages_outside_the_window_may_be_anything(fa):
     """Table entries of pages with no visible key are out of the pool; a visible key on such a page
     counts as a zero row."""
@@ -309,7 +402,8 @@ def test_append_matches_the_reference(fa, case):
         a = a.double().cpu().numpy()
         same = mag == 0
         assert np.array_equal(a[same], e[same], equal_nan=True)
-        assert (abs(a - e)[~same] <= (U[dtype] * abs(e) + 2.0 ** -22 * mag + TINY[dtype])[~same]).all()
+        a, e, mag = a[~same], e[~same], mag[~same]
+        assert (abs(a - e) <= U[dtype] * abs(e) + 2.0 ** -22 * mag + TINY[dtype]).all()
 
     close(kp, ref[0], mag_k)
     assert np.array_equal(vp.double().cpu().numpy(), ref[1], equal_nan=True)
@@ -348,7 +442,8 @@ def test_append_in_place_drops_and_clamps(fa):
             ref[1][where] = rows[row, Hq + Hkv:]
     got = kp.double().cpu().numpy()
     fin = np.isfinite(ref[0])
-    assert np.array_equal(got[~fin], ref[0][~fin], equal_nan=True) and (abs(got - ref[0])[fin] <= bound[fin]).all()
+    assert np.array_equal(got[~fin], ref[0][~fin], equal_nan=True)
+    assert (abs(got[fin] - ref[0][fin]) <= bound[fin]).all()
     assert np.array_equal(vp.double().cpu().numpy(), ref[1], equal_nan=True)
 
 
