@@ -261,6 +261,7 @@ fa_status fwd_fixed(const void* q, const void* k, const void* v, void* o, float*
     if (B <= 0 || Sq <= 0 || Sk <= 0 || Hq <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
     if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
     if (window_left < -1 || window_right < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
+    if (sinks > 0 && scale <= 0.f) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
     if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
     if (D != 64 && D != 96 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;
@@ -287,6 +288,7 @@ fa_status fwd_varlen(const void* q, const void* k, const void* v, void* o, float
     if (B <= 0 || total_q <= 0 || total_k <= 0 || Hq <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
     if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
     if (window_left < -1 || window_right < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
+    if (sinks > 0 && scale <= 0.f) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return FA_ERR_INVALID_ARG;
     if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
     if (D != 64 && D != 96 && D != 128 && D != 256) return FA_ERR_UNSUPPORTED;

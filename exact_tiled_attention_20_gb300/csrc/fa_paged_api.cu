@@ -59,7 +59,7 @@ fa_status decode(const void* q, const void* k_pages, const void* v_pages, const 
                                      dtype);
     if (chk != FA_OK) return chk;
     if (!q || !o || misaligned(q, 16) || misaligned(o, 16) || misaligned(lse, 4)) return FA_ERR_INVALID_ARG;
-    if (Sq <= 0 || Hq <= 0 || Hq % Hkv != 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+    if (Sq <= 0 || Hq <= 0 || Hq % Hkv != 0 || !std::isfinite(scale) || scale <= 0.f) return FA_ERR_INVALID_ARG;
     if (window_left < -1 || sinks < 0) return FA_ERR_INVALID_ARG;
     if (page_size % 16 != 0 || Sq > 256 || Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
     if ((long long)Sq * Hq * D > 0x7fffffffLL || (long long)B * Sq * Hq > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;

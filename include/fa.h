@@ -122,8 +122,8 @@ FA_API fa_status fa_fwd_varlen(const void *q, const void *k, const void *v, void
  *     j >= i + Sk - Sq - window_left  or  j < sinks.
  * Blocks of keys between the sinks and every row's window are skipped.  What a row does not see is
  * not used for it, NaN and infinities included (rows that see over 2^20 keys excepted, where an
- * infinity or NaN in V of a key that other rows of their block see gives NaN).  sinks >= 0, else
- * FA_ERR_INVALID_ARG.  Where the sinks do not matter (sinks == 0, or window_left == -1 or at least
+ * infinity or NaN in V of a key that other rows of their block see gives NaN).  sinks >= 0, and
+ * scale > 0 if there are any, else FA_ERR_INVALID_ARG.  Where the sinks do not matter (sinks == 0, or window_left == -1 or at least
  * the keys) the call is fa_fwd_window (fa_fwd_varlen); everything else as there.
  */
 FA_API fa_status fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -431,7 +431,8 @@ FA_API size_t fa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, in
  *              device.  Where kv_lens[b] < Sq the drafts before the first key do not exist
  *   workspace  at least fa_decode_paged_workspace_bytes(...) bytes; no initialisation.  Calls that
  *              may overlap on the GPU need one each
- * page_size is a multiple of 16; Sq <= 256; Hq / Hkv <= 128.  A token that sees no key gets O = 0
+ * page_size is a multiple of 16; Sq <= 256; Hq / Hkv <= 128; scale > 0, else FA_ERR_INVALID_ARG.
+ * A token that sees no key gets O = 0
  * and LSE = -inf.  What lies in the pool behind a sequence's last key, and a key hidden from a
  * token, is not used for it, NaN and infinities included.  Keys on a page outside the pool count
  * as zero rows.  Accumulation is fp32; P is rounded to the input dtype before the P.V product; O is

@@ -37,7 +37,8 @@ POOL = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(table=None), INV
 DECODE = POOL + [
     (dict(q=None), INVALID), (dict(q=FAKE + 2), INVALID), (dict(o=None), INVALID), (dict(o=FAKE + 8), INVALID),
     (dict(lse=FAKE + 2), INVALID), (dict(Sq=0), INVALID), (dict(Hq=0), INVALID), (dict(Hq=12), INVALID),
-    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(page=24), UNSUPPORTED),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=-0.1), INVALID), (dict(page=24), UNSUPPORTED),
     (dict(page=1), UNSUPPORTED), (dict(Sq=257), UNSUPPORTED), (dict(Hq=8 * 129), UNSUPPORTED),
     (dict(num_pages=0x7fffffff), UNSUPPORTED), (dict(page=1 << 28, max_pages=1, Hkv=16, Hq=16, D=128), UNSUPPORTED),
     (dict(B=1024, Sq=256, Hq=1 << 13, Hkv=1 << 13), UNSUPPORTED)]

@@ -218,7 +218,8 @@ FAKE = 1 << 20
 
 @pytest.mark.parametrize("change,code", [
     (dict(sinks=-1), 1), (dict(left=-2), 1), (dict(right=-2), 1), (dict(q=None), 1), (dict(k=FAKE + 8), 1),
-    (dict(lse=FAKE + 2), 1), (dict(Sq=0), 1), (dict(Hq=3), 1), (dict(scale=float("nan")), 1), (dict(D=80), 2),
+    (dict(lse=FAKE + 2), 1), (dict(Sq=0), 1), (dict(Hq=3), 1), (dict(scale=float("nan")), 1), (dict(scale=0.0), 1),
+    (dict(scale=-1.0), 1), (dict(D=80), 2),
     (dict(dtype=7), 2), (dict(B=1 << 16, Sq=1 << 16), 2)])
 def test_sinks_refuse(change, code):
     from exact_tiled_attention_20_gb300 import _lib, build
@@ -231,6 +232,7 @@ def test_sinks_refuse(change, code):
 
 @pytest.mark.parametrize("change,code", [
     (dict(sinks=-1), 1), (dict(left=-2), 1), (dict(cu_q=None), 1), (dict(cu_k=FAKE + 2), 1), (dict(total_q=0), 1),
+    (dict(scale=0.0), 1),
     (dict(B=1025), 2), (dict(D=80), 2)])
 def test_packed_sinks_refuse(change, code):
     import ctypes
