@@ -308,6 +308,80 @@ def test_values_that_are_not_finite_reach_those_that_see_them(fa, D, kind):
     assert torch.isfinite(lse[1, :4].cpu()[:, ~hit]).all() and torch.isfinite(lse[1, 4:]).all()
 
 
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("kind", ["nan", "-inf"])
+def test_values_that_are_not_finite_and_few_rows(fa, D, kind):
+    """The same where a kv head has 16 rows, over several tiles and in outputs that are cut and joined."""
+    Sq, Hq, Hkv, lens = 4, 8, 2, [4, 4000]
+    pool = Pool(2, Hkv, D, 32, lens, "bf16", seed=D).fill()
+    t = pool.table
+    for b, n in enumerate(lens):
+        for at, d in ((1, 5), (2, D - 1), (3, 33)):
+            key = n - Sq + at
+            pool.cpu[1][int(t[b][key // 32]), key % 32, 1, d] = float(kind)
+    edge = lens[1] - 3 - 600                                 # the window's first key of token 1
+    pool.cpu[1][int(t[1][edge // 32]), edge % 32, 0, 7] = float(kind)
+    tree = paged16.random_trees(np.random.default_rng(D), 2, Sq)
+    q = queries(pool, 2, Sq, Hq, D, "bf16")
+    mask = torch.from_numpy(paged16.pack_tree(tree)).to(DEV)
+    o, lse = fa.fa_decode_splitkv_paged_window(q.to(DEV), *pool.gpu(), 600, sinks=70)
+    torch.cuda.synchronize()
+    check(o, lse, q, pool, lambda b, n: paged16.sees_window(n, Sq, 600, 70), 1 / math.sqrt(D), "bf16")
+    pool.cpu[1][int(t[1][edge // 32]), edge % 32, 0, 7] = 1.0
+    o, lse = fa.fa_decode_splitkv_paged_tree(q.to(DEV), *pool.gpu(), mask)
+    torch.cuda.synchronize()
+    check(o, lse, q, pool, lambda b, n: paged16.sees_tree(n, Sq, tree[b]), 1 / math.sqrt(D), "bf16")
+    key = lens[1] - Sq + 1
+    pool.cpu[0][int(t[1][key // 32]), key % 32, 0, 2] = math.nan
+    q[1, 0, 7] = math.nan                                    # a query head of the other kv head
+    o, lse = fa.fa_decode_splitkv_paged_tree(q.to(DEV), *pool.gpu(), mask)
+    torch.cuda.synchronize()
+    hit = torch.from_numpy(tree[1][:, 1])
+    o, lse = o[1].cpu(), lse[1].cpu()
+    assert torch.isnan(o[:, :4][hit]).all() and torch.isnan(lse[:4][:, hit]).all()
+    assert torch.isfinite(o[:, :4][~hit]).all() and torch.isfinite(lse[:4][:, ~hit]).all()
+    assert torch.isnan(o[0, 7]).all() and torch.isnan(lse[7, 0])
+    assert torch.isfinite(lse[4:7]).all() and torch.isfinite(lse[7, 1:]).all()
+
+
+def test_two_streams_at_once_and_a_replay_with_few_rows(fa):
+    """Calls on two streams with workspaces of their own do not disturb one another; a captured step
+    follows lengths and a table that moved on."""
+    B, Hq, Hkv, D = 20, 32, 8, 128
+    rng = np.random.default_rng(4)
+    pools = [Pool(B, Hkv, D, 64, [int(n) for n in rng.integers(0, 2500, B)], "bf16", seed=i).fill() for i in range(2)]
+    qs = [queries(p, B, 1, Hq, D, "bf16").to(DEV) for p in pools]
+    gpu = [p.gpu() for p in pools]
+    want = [fa.fa_decode_splitkv_paged_window(q, *g, 500, sinks=4) for q, g in zip(qs, gpu)]
+    torch.cuda.synchronize()
+    n = fa.fa_decode_paged_workspace_bytes(B, 1, Hq, Hkv, D)
+    ws = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[(torch.empty_like(q), torch.empty((B, Hq, 1), device=DEV)) for _ in range(8)] for q in qs]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for i in range(2):
+            fa.fa_decode_splitkv_paged_window(qs[i], *gpu[i], 500, sinks=4, out=outs[i][k][0], lse=outs[i][k][1],
+                                              workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in outs[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+    check(*want[0], qs[0].cpu(), pools[0], lambda b, k: paged16.sees_window(k, 1, 500, 4), 1 / math.sqrt(D), "bf16")
+    graph, o, lse = torch.cuda.CUDAGraph(), *outs[0][0]
+    with torch.cuda.graph(graph):
+        fa.fa_decode_splitkv_paged_window(qs[0], *gpu[0], 500, sinks=4, out=o, lse=lse, workspace=ws[0])
+    for lens in (rng.permutation(pools[0].lens), np.minimum(pools[0].lens, 3), np.zeros(B)):
+        lens = [int(min(a, b)) for a, b in zip(lens, pools[0].lens)]     # rows that hold keys
+        gpu[0][3].copy_(torch.tensor(lens, dtype=torch.int32))
+        o.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        part = Pool.__new__(Pool)
+        part.__dict__.update(pools[0].__dict__, lens=lens)
+        check(o, lse, qs[0].cpu(), part, lambda b, k: paged16.sees_window(k, 1, 500, 4), 1 / math.sqrt(D), "bf16")
+
+
 def test_guards_repeats_and_graphs(fa):
     """Outputs inside larger buffers leave the rest alone; the same call gives the same bits, from
     a captured graph and on another stream too; a replay follows lengths that moved on."""
