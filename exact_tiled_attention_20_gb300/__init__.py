@@ -26,12 +26,11 @@ Importing the package does not load the library; the first call does, and raises
 ``libfa.so`` has not been built.
 """
 from ._lib import (FA_BF16, FA_FP16, FaError, fa_decode_default_splits, fa_decode_paged_workspace_bytes,
-                   fa_decode_splitkv,
-                   fa_decode_splitkv_multi, fa_decode_splitkv_noalloc, fa_decode_splitkv_paged,
+                   fa_decode_splitkv, fa_decode_splitkv_multi, fa_decode_splitkv_noalloc, fa_decode_splitkv_paged,
                    fa_decode_splitkv_paged_fp8, fa_decode_splitkv_paged_tree, fa_decode_splitkv_paged_window,
                    fa_decode_workspace_bytes, fa_fwd, fa_fwd_varlen,
-                   fa_kv_append_paged_fp8, fa_kv_append_paged_rope, fa_kv_read_paged_fp8, fa_last_device_status, fa_selftest_bounded_wait,
-                   fa_status_string, library_path, load)
+                   fa_kv_append_paged_fp8, fa_kv_append_paged_rope, fa_kv_read_paged_fp8, fa_last_device_status,
+                   fa_selftest_bounded_wait, fa_status_string, library_path, load)
 
 __all__ = [
     "FA_BF16", "FA_FP16", "FaError", "fa_fwd", "fa_fwd_varlen", "fa_decode_splitkv", "fa_decode_splitkv_paged",

@@ -859,7 +859,8 @@ def fa_decode_splitkv_paged_window(q, k_pages, v_pages, block_table, kv_lens, wi
     Sq + i, sees the keys j <= p with j >= p - window_left (-1: all) or j < sinks.  workspace as for
     fa_decode_splitkv_paged_tree.  Returns (o like q, lse fp32 [B, Hq, Sq])."""
     return _decode_paged16("fa_decode_splitkv_paged_window", q, k_pages, v_pages, block_table, kv_lens, None,
-                           (min(int(window_left), 2**31 - 1), min(int(sinks), 2**31 - 1)), scale, workspace, out, lse, stream)
+                           (min(int(window_left), 2**31 - 1), min(int(sinks), 2**31 - 1)), scale, workspace, out, lse,
+                           stream)
 
 
 # ---- the forward with sinks, behind fa_fwd and fa_fwd_varlen.

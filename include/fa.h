@@ -1,8 +1,10 @@
 /*
  * fa.h -- C ABI of the exact tiled attention library for NVIDIA GB300 (sm_103a).
  *
- * Two operations, as the source pages define them, and an 8-bit paged KV cache for the
- * second (fa_kv_append_paged_fp8, fa_kv_read_paged_fp8, fa_decode_splitkv_paged_fp8):
+ * Two operations, as the source pages define them, and for the second an 8-bit paged KV cache
+ * (fa_kv_append_paged_fp8, fa_kv_read_paged_fp8, fa_decode_splitkv_paged_fp8) and the operators of
+ * a serving loop over the 16-bit one (fa_kv_append_paged_rope, fa_decode_splitkv_paged_tree,
+ * fa_decode_splitkv_paged_window, with fa_fwd_sinks and fa_fwd_varlen_sinks for its prompts):
  *
  *  fa_fwd             exact attention forward, O = softmax(scale * Q K^T [+ causal mask]) V,
  *                     plus the per-row log-sum-exp.  Page "flash-attention-v100", section
@@ -432,6 +434,9 @@ FA_API size_t fa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, in
  *   workspace  at least fa_decode_paged_workspace_bytes(...) bytes; no initialisation.  Calls that
  *              may overlap on the GPU need one each
  * page_size is a multiple of 16; Sq <= 256; Hq / Hkv <= 128; scale > 0, else FA_ERR_INVALID_ARG.
+ * Sq * Hq * D and B * Sq * Hq are below 2^31, and so are the tiles that a plan may have to count: at
+ * most B * Hkv * ceil(Sq * Hq / Hkv / 64) * (capacity / 64 + 8), by capacities and not by lengths;
+ * past them FA_ERR_UNSUPPORTED.
  * A token that sees no key gets O = 0
  * and LSE = -inf.  What lies in the pool behind a sequence's last key, and a key hidden from a
  * token, is not used for it, NaN and infinities included.  Keys on a page outside the pool count
