@@ -556,3 +556,35 @@ def test_prompt_then_drafts_then_steps(fa):
     pool.lens = kl.cpu().tolist()
     pool.cpu = [kp.cpu(), vp.cpu()]
     check(o, lse, q.cpu(), pool, lambda b, n: paged16.sees_window(n, 1, 63, 4), 1 / math.sqrt(D), "bf16")
+
+
+def test_the_prompt_forward_and_the_decode_agree(fa):
+    """Packed prompts of a fused projection: the append turns queries and keys and fills the cache, the
+    forward with a window and sinks runs over what it turned, and the decode of the last tokens over
+    the cache gives the same."""
+    Hq, Hkv, D, page, left, sinks = 8, 2, 128, 16, 127, 4
+    lens, cu = [300, 2, 77], [0, 300, 302, 379]
+    pool = Pool(3, Hkv, D, page, lens, "bf16", seed=21)
+    kp, vp, table, kl = pool.gpu()
+    qkv = torch.randn((379, Hq + 2 * Hkv, D), generator=pool.gen).to(torch.bfloat16).to(DEV)
+    angle = torch.arange(300, device=DEV)[:, None] * 1000.0 ** -torch.linspace(0, 1, D // 2, device=DEV)
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    k, v = qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    qk = fa.fa_kv_append_paged_rope(k, v, kp, vp, table, kl, angle.cos(), angle.sin(), q=qkv[:, :Hq + Hkv],
+                                    cu_seqlens_new=cud)
+    q, k = (x.contiguous() for x in qk.split((Hq, Hkv), 1))
+    o, lse = fa.fa_fwd_varlen(q, k, v.contiguous(), cud, cud, causal=True, window=(left, 0), sinks=sinks)
+    last = torch.stack([q[n - 2:n] for n in cu[1:]])
+    od, lsed = fa.fa_decode_splitkv_paged_window(last, kp, vp, table, kl, left, sinks=sinks)
+    torch.cuda.synchronize()
+    pool.cpu = [kp.cpu(), vp.cpu()]
+    t, kn, vn = pool.table.numpy(), k.double().cpu().numpy(), v.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        rows = slice(cu[b], cu[b + 1])
+        assert np.array_equal(paged16.cached(pool.np()[0], t, b, n), kn[rows])
+        assert np.array_equal(paged16.cached(pool.np()[1], t, b, n), vn[rows])
+        part = Pool.__new__(Pool)
+        part.__dict__.update(lens=[n], cpu=pool.cpu, table=pool.table[b:b + 1])
+        check(o[None, rows], lse[None, :, rows], q[None, rows].cpu(), part,
+              lambda _, m: paged16.sees_window(m, m, left, sinks), 1 / math.sqrt(D), "bf16")
+    check(od, lsed, last.cpu(), pool, lambda b, n: paged16.sees_window(n, 2, left, sinks), 1 / math.sqrt(D), "bf16")
