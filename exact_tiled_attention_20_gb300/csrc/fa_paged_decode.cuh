@@ -1214,17 +1214,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const int h = s.hk * p.group + h_l;
                 const size_t row = ((size_t)s.b * p.Sq + tok) * p.Hq + h;
                 const size_t part = ((size_t)member * 2 * p.ranges + s.slot) * block_rows + q * p.T * p.group + r;
-                // The warp's live rows are its first ones; in the result they are part or row + ... of the first.
+                // The warp's live rows are its first ones; in the partial result they are part or row + ... of the
+                // first.
                 const int rows = __popc(__ballot_sync(0xffffffffu, live));
                 const uint32_t out = sOut + (uint32_t)warp * (32 * (C::OC + 4) * 4);
-#pragma unroll 1
-                for (int c0 = 0; any && c0 < D; c0 += C::OC) {
-                    uint32_t ov[C::OC];
+                // Lanes of a row and rows at a time, of 32-bit and of 16-bit results.
+                constexpr int LF = C::OC / 4, RF = 32 / LF, LH = C::OC / 8, RH = 32 / LH;
+                uint32_t at[LH];
+#pragma unroll
+                for (int i = 0; i < LH; ++i) at[i] = __shfl_sync(0xffffffffu, (uint32_t)row, i * RH + lane / LH);
+                auto load_o = [&](int c0, uint32_t (&ov)[C::OC]) {
                     if constexpr (C::OC == 32)
                         tmem_ld_32x32b_x32(tO + c0, ov);
                     else
                         tmem_ld_32x32b_x16(tO + c0, ov);
-                    tmem_wait_ld(ov);
+                };
+                auto put_o = [&](int c0, uint32_t (&ov)[C::OC]) {
 #pragma unroll
                     for (int i = 0; i < C::OC; ++i) ov[i] = none ? 0u : __float_as_uint(__uint_as_float(ov[i]) * inv_l);
                     __syncwarp();  // the columns before have been read
@@ -1233,30 +1238,37 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         st_shared_v4(out + (lane * (C::OC + 4) + i) * 4, ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
                     __syncwarp();
                     if (s.cut) {
-                        constexpr int L = C::OC / 4, R = 32 / L;  // lanes of a row, rows at a time
-                        const int rr = lane / L, cc = lane % L * 4;
+                        const int rr = lane / LF, cc = lane % LF * 4;
                         float* to = p.o_part + (part - lane + rr) * D + c0 + cc;
-                        uint32_t w[32 / R][4];
+                        uint32_t w[LF][4];
 #pragma unroll
-                        for (int i = 0; i < 32 / R; ++i) lds128(out + ((i * R + rr) * (C::OC + 4) + cc) * 4, w[i]);
+                        for (int i = 0; i < LF; ++i) lds128(out + ((i * RF + rr) * (C::OC + 4) + cc) * 4, w[i]);
 #pragma unroll
-                        for (int i = 0; i < 32 / R; ++i)
-                            if (i * R + rr < rows) st_global_v4(to + i * R * D, w[i][0], w[i][1], w[i][2], w[i][3]);
+                        for (int i = 0; i < LF; ++i)
+                            if (i * RF + rr < rows) st_global_v4(to + i * RF * D, w[i][0], w[i][1], w[i][2], w[i][3]);
                     } else {
-                        constexpr int L = C::OC / 8, R = 32 / L;
-                        const int rr = lane / L, cc = lane % L * 8;
-                        for (int i = 0; i < rows; i += R) {
-                            const int from = min(i + rr, rows - 1);
-                            const long long at = __shfl_sync(0xffffffffu, (long long)row, from);
-                            if (i + rr >= rows) continue;
-                            uint32_t w[4], x[4];
-                            lds128(out + (from * (C::OC + 4) + cc) * 4, w);
-                            lds128(out + (from * (C::OC + 4) + cc + 4) * 4, x);
-                            auto f = [](uint32_t y) { return __uint_as_float(y); };
-                            st_global_v4(o16 + at * D + c0 + cc, pack2<kBF16>(f(w[0]), f(w[1])), pack2<kBF16>(f(w[2]), f(w[3])),
-                                         pack2<kBF16>(f(x[0]), f(x[1])), pack2<kBF16>(f(x[2]), f(x[3])));
+                        const int rr = lane / LH, cc = lane % LH * 8;
+                        uint32_t w[LH][4], x[LH][4];
+#pragma unroll
+                        for (int i = 0; i < LH; ++i) {
+                            lds128(out + ((i * RH + rr) * (C::OC + 4) + cc) * 4, w[i]);
+                            lds128(out + ((i * RH + rr) * (C::OC + 4) + cc + 4) * 4, x[i]);
                         }
+                        auto f = [](uint32_t y) { return __uint_as_float(y); };
+#pragma unroll
+                        for (int i = 0; i < LH; ++i)
+                            if (i * RH + rr < rows)
+                                st_global_v4(o16 + (size_t)at[i] * D + c0 + cc, pack2<kBF16>(f(w[i][0]), f(w[i][1])),
+                                             pack2<kBF16>(f(w[i][2]), f(w[i][3])), pack2<kBF16>(f(x[i][0]), f(x[i][1])),
+                                             pack2<kBF16>(f(x[i][2]), f(x[i][3])));
                     }
+                };
+#pragma unroll 1
+                for (int c0 = 0; any && c0 < D; c0 += C::OC) {
+                    uint32_t ov[C::OC];
+                    load_o(c0, ov);
+                    tmem_wait_ld(ov);
+                    put_o(c0, ov);
                 }
                 if (odd) {  // other lanes' writes to the row come first
                     __threadfence_block();
