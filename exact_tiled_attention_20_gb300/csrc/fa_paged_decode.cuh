@@ -240,7 +240,9 @@ __device__ __forceinline__ int paged_pieces(int start, int units, int w) {
 }
 // The slot of an entry's piece in range r: a range has at most one piece of an entry that began
 // before it, and one that goes on behind it.
-__device__ __forceinline__ int paged_slot(const PagedDecParams& p, int r, bool first) { return first ? p.ranges + r : r; }
+__device__ __forceinline__ int paged_slot(const PagedDecParams& p, int r, bool first) {
+    return first ? p.ranges + r : r;
+}
 
 struct PagedSeg {
     int b, hk, rb, len;
@@ -1482,7 +1484,8 @@ fa_status launch_paged_cfg(const PagedDecodeArgs& a, cudaStream_t s) {
     if (units > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     p.whole = most + C::Lead <= C::MinWidth ? 1 : 0;
     p.ranges = (int)std::min((long long)(a.num_sms / G), (units + C::MinWidth - 1) / C::MinWidth);
-    // A row takes a warp two trips to L2, so more rows are taken by more CTAs.
+    // A row takes a warp two trips to L2, so more rows are taken by more CTAs.  Measured (us) with at most 3, 4
+    // and 8: 26 drafts of 4 heads 92.9, 92.2, 93.4, 64 drafts 91.5, 87.6, 89.0.
     p.merge_ctas = std::max(1, std::min(4, std::min(NQ * p.T, p.Sq) * p.group / 16));
     CUtensorMap tq, tk, tv;
     if (!encode_paged_tmap(&tq, a.q, a.bf16, D, a.Hq, a.Sq, a.B, p.group, p.T) ||
