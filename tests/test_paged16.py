@@ -588,3 +588,32 @@ def test_the_prompt_forward_and_the_decode_agree(fa):
         check(o[None, rows], lse[None, :, rows], q[None, rows].cpu(), part,
               lambda _, m: paged16.sees_window(m, m, left, sinks), 1 / math.sqrt(D), "bf16")
     check(od, lsed, last.cpu(), pool, lambda b, n: paged16.sees_window(n, 2, left, sinks), 1 / math.sqrt(D), "bf16")
+
+
+@pytest.mark.parametrize("S", [77, 1500])
+def test_append_and_forward_on_one_buffer_without_a_wait(fa, S):
+    """The append turns queries into a buffer that the forward with sinks reads, over and over without a
+    wait or another kernel between them: neither starts on what the other is not done with."""
+    Hq, Hkv, D, n = 8, 2, 128, 12
+    pool = Pool(1, Hkv, D, 16, [S], "bf16", seed=5)
+    kp, vp, table, kl = pool.gpu()
+    rnd = lambda *s: torch.randn(s, generator=pool.gen).to(torch.bfloat16).to(DEV)
+    q, k, v = [rnd(1, S, Hq, D) for _ in range(n)], rnd(1, S, Hkv, D), rnd(1, S, Hkv, D)
+    angle = torch.rand((S, D // 2), device=DEV)
+    cos, sin = angle.cos(), angle.sin()
+    turned, outs = torch.empty_like(q[0]), [torch.empty_like(q[0]) for _ in range(n)]
+    lse = torch.empty((1, Hq, S), device=DEV)
+    for wait in (True, False):
+        want = [o.clone() for o in outs] if not wait else None
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        for i in range(n):
+            fa.fa_kv_append_paged_rope(k, v, kp, vp, table, kl, cos, sin, q=q[i], q_out=turned)
+            if wait:
+                torch.cuda.synchronize()
+            fa.fa_fwd(turned, k, v, causal=True, window=(63, 0), sinks=4, out=outs[i], lse=lse)
+            if wait:
+                torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
