@@ -577,10 +577,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
             grid_dependency_wait();
         }
+        // (every warp by itself: after the wait all see the same lengths; the first are on their way with the
+        // first table entries)
+        const int now = __ldcg(p.kv_lens + min(lane, p.B - 1));
         if (more) ids = fetch(s, s.u0);
-        // (every warp by itself: after the wait all see the same lengths)
-        bool stale = false;
-        for (int b = lane; b < p.B; b += 32) stale |= paged_len(p, b) != plan_len[b];
+        bool stale = min(max(now, 0), p.capacity) != plan_len[min(lane, p.B - 1)];
+        for (int b = lane + 32; b < p.B; b += 32) stale |= paged_len(p, b) != plan_len[b];
         if (!__any_sync(0xffffffffu, stale)) break;
         __syncthreads();
     }
