@@ -233,8 +233,14 @@ extern "C" {
 
 namespace {
 
-// Sinks count where a window that is shorter than the keys ends on the left of them.
-fa_status launch_fwd(FwdArgs& a, int sinks, int keys, cudaStream_t s) {
+// Query i of sq sees the keys i + sk - sq - window_left .. i + sk - sq + window_right of sk, bounds that
+// the kernels compute in 32 bits.  A right side of at least the queries hides no key, nor does a left
+// side of at least the keys, and longer ones are brought down: the first to none, the second to the
+// keys (which keeps the kernel that the call takes).  Sinks count where a window that is shorter than the
+// keys ends on the left of them.
+fa_status launch_fwd(FwdArgs& a, int sinks, int queries, int keys, cudaStream_t s) {
+    if (a.window_right >= queries) a.window_right = -1;
+    if (a.window_left > keys) a.window_left = keys;
     if (sinks > 0 && a.window_left >= 0 && a.window_left < keys) {
         a.sinks = sinks < keys ? sinks : keys;
         switch (a.D) {
@@ -273,7 +279,7 @@ fa_status fwd_fixed(const void* q, const void* k, const void* v, void* o, float*
     FwdArgs a{q, k, v, o, lse, B, Sq, Sk, Hq, Hkv, D, scale, causal, window_left, window_right,
               nullptr, nullptr, 0, 0, dtype == FA_BF16, di.num_sms, di.status};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launch_fwd(a, sinks, Sk, s);
+    return launch_fwd(a, sinks, Sq, Sk, s);
 }
 
 fa_status fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_seqlens_q,
@@ -301,7 +307,7 @@ fa_status fwd_varlen(const void* q, const void* k, const void* v, void* o, float
               cu_seqlens_q, cu_seqlens_k, total_q, total_k, dtype == FA_BF16, di.num_sms,
               di.status};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launch_fwd(a, sinks, total_k, s);
+    return launch_fwd(a, sinks, total_q, total_k, s);
 }
 
 }  // namespace
