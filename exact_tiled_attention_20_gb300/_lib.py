@@ -105,6 +105,13 @@ def fa_selftest_bounded_wait(result, stream=None) -> int:
                                                ctypes.c_void_p(_stream_handle(stream))))
 
 
+def _c_int(x) -> int:
+    """A window's side or a count of sinks as a C int.  ctypes keeps the low 32 bits of a longer
+    number; here it becomes the largest (past every key) or the least (which the library refuses)."""
+    x = int(x)
+    return x if -2**31 <= x < 2**31 else 2**31 - 1 if x > 0 else -2**31
+
+
 def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None,
            return_lse: bool = True, stream=None, window=None, sinks: int = 0):
     """Exact attention forward through fa_fwd (or fa_fwd_window when ``window=(left,
@@ -144,8 +151,8 @@ def fa_fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, 
                                _stream_handle(stream))
         else:
             st = load().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp,
-                                      B, Sq, Sk, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
-                                      int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
+                                      B, Sq, Sk, Hq, Hkv, D, sc, int(bool(causal)), _c_int(window[0]),
+                                      _c_int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_window" if window is not None else "fa_fwd")
     return out, lse
@@ -337,8 +344,8 @@ def fa_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, causal: bool = False,
     with torch.cuda.device(q.device):
         st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B,
-                               total_q, total_k, Hq, Hkv, D, sc, int(bool(causal)), int(window[0]),
-                               int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
+                               total_q, total_k, Hq, Hkv, D, sc, int(bool(causal)), _c_int(window[0]),
+                               _c_int(window[1]), _DTYPE[q.dtype], _stream_handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_varlen")
     return out, lse
@@ -859,7 +866,7 @@ def fa_decode_splitkv_paged_window(q, k_pages, v_pages, block_table, kv_lens, wi
     Sq + i, sees the keys j <= p with j >= p - window_left (-1: all) or j < sinks.  workspace as for
     fa_decode_splitkv_paged_tree.  Returns (o like q, lse fp32 [B, Hq, Sq])."""
     return _decode_paged16("fa_decode_splitkv_paged_window", q, k_pages, v_pages, block_table, kv_lens, None,
-                           (min(int(window_left), 2**31 - 1), min(int(sinks), 2**31 - 1)), scale, workspace, out, lse,
+                           (_c_int(window_left), _c_int(sinks)), scale, workspace, out, lse,
                            stream)
 
 
@@ -902,8 +909,8 @@ def _fwd_sinks(q, k, v, causal, scale, window, sinks, out, lse, return_lse, stre
     left, right = (-1, -1) if window is None else window
     _call_on(device, (_lib or load()).fa_fwd_sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
              None if lse is None else lse.data_ptr(), B, Sq, Sk, Hq, Hkv, D,
-             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, min(int(left), 2**31 - 1),
-             min(int(right), 2**31 - 1), min(int(sinks), 2**31 - 1), _DTYPE[dtype], handle)
+             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, _c_int(left),
+             _c_int(right), _c_int(sinks), _DTYPE[dtype], handle)
     return out, lse
 
 
@@ -918,6 +925,6 @@ def _fwd_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale, window
     out, lse = _outputs(q, dtype, device, out, lse, (Hq, total_q), True, other)
     _call_on(device, (_lib or load()).fa_fwd_varlen_sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
              lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), n[0] - 1, total_q, total_k, Hq, Hkv, D,
-             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, min(int(window[0]), 2**31 - 1),
-             min(int(window[1]), 2**31 - 1), min(int(sinks), 2**31 - 1), _DTYPE[dtype], handle)
+             1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, _c_int(window[0]),
+             _c_int(window[1]), _c_int(sinks), _DTYPE[dtype], handle)
     return out, lse

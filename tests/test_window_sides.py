@@ -46,3 +46,34 @@ def test_packed_sides_past_every_key(fa, D, dtype, sinks):  # noqa: F811
             a, e = cq[b], cq[b + 1]
             check(o[a:e], lse[:, a:e], q[a:e], k[ck[b]:ck[b + 1]], v[ck[b]:ck[b + 1]],
                   sees(nq[b], nk[b], False, left, right, sinks), 1 / math.sqrt(D), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sinks", [0, 4])
+def test_numbers_past_32_bits(fa, sinks):  # noqa: F811
+    """Python's integers do not wrap on their way into the library: a side past every key is one of
+    2**31 - 1, and a number far below zero is refused."""
+    q, k, v = (t.to(DEV) for t in make(1, 300, 300, 2, 1, 128, "bf16", seed=5))
+    cu = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+
+    def fixed(win, n=sinks):
+        return fa.fa_fwd(q, k, v, window=win, sinks=n)
+
+    def packed(win, n=sinks):
+        return fa.fa_fwd_varlen(q[0], k[0], v[0], cu, cu, window=win, sinks=n)
+
+    for call in (fixed, packed):
+        for win, same in (((2 ** 32 + 9, 7), (MAX, 7)), ((50, 2 ** 32), (50, MAX)), ((2 ** 63, 2 ** 70), (MAX, MAX))):
+            a, b = call(win), call(same)
+            torch.cuda.synchronize()
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), win
+        for win in ((-2 ** 32, 0), (5, -2 ** 32 - 1), (-2 ** 33 + 4, -1)):
+            with pytest.raises(fa.FaError):
+                call(win)
+        with pytest.raises(fa.FaError):
+            call((50, 0), -2 ** 32)
+    pages = torch.zeros((3, 16, 1, 128), dtype=torch.bfloat16, device=DEV)
+    table, lens = torch.arange(3, dtype=torch.int32, device=DEV)[None], torch.tensor([40], dtype=torch.int32, device=DEV)
+    for left, n in ((-2 ** 32, 0), (-2 ** 32 - 1, 0), (3, -2 ** 32)):
+        with pytest.raises(fa.FaError):
+            fa.fa_decode_splitkv_paged_window(q[:, :1].contiguous(), pages, pages, table, lens, left, sinks=n)
