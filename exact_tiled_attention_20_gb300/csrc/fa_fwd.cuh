@@ -73,9 +73,8 @@ struct FwdParams {
     int* status;       // sticky device status word
     // Sinks (the kSink instantiations): keys 0 .. sinks - 1 stay visible left of the window.
     int sinks;
-    const void* q;  // what the tensor maps are of
-    const void* k;
-    const void* v;
+    int total_k;    // rows of a sequence's K and V (packed: of all)
+    const void* v;  // [B, Sk, Hkv, D]
     unsigned rcp_qb, rcp_hq, rcp_group;  // reciprocals of num_qb, Hq and group (quotient)
 };
 
@@ -389,58 +388,174 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b) {
     return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
 }
 
-// One query row again, by a warp on its own: O[d] = sum of exp2(s scale log2 e - m) v[d] / l over the
-// row's visible keys, which V's infinities and NaNs behind the mask do not reach.  (The product of
-// a block's P, 0 where masked, and V has 0 * inf = NaN there, for the rows that do not see the
-// key.)  The epilogue calls it for rows that came out not finite although l did.  q, k, v: the row,
-// and key 0 of its sequence and head; dims col0 .. col0 + n - 1 go to the staging buffer's row at
-// `stage` (of index rr), or to `out` where that is 0.
-template <int D, int BM, bool kBF16>
-__device__ __noinline__ void sink_row(const uint16_t* q, const uint16_t* k, const uint16_t* v, long long stride,
-                                      int sinks, int lo, int hi, float scale_log2, float m, float inv_l, int col0,
-                                      int n, uint32_t stage, int rr, uint16_t* out) {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    auto from16 = [](uint16_t x) -> float {
-        if constexpr (kBF16) return __uint_as_float((uint32_t)x << 16);
-        float f;
-        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(x));
-        return f;
-    };
-    float x[V], o[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        x[i] = from16(q[lane + i * 32]);
-        o[i] = 0.f;
+// Infinities and NaNs in V, with sinks.  The product of P, 0 where masked, and V gives 0 * inf = NaN to the
+// rows that do not see the key.  Where a row comes out that is not finite although its sum of
+// weights is, the CTA goes through its tiles again, from the first such one to the last: values of
+// V that are not finite then give way to zeros in shared memory, before the product, and the epilogue adds
+// them to the rows that see them (an infinity or NaN is the sum that it is in, whatever its weight).  So
+// finite inputs cost a test of each output, and others a second pass at most: [2, 8192, 32, 128] with a
+// window of 1023 takes 0.3 ms, with a NaN in one sink 0.5, in a sink of each head 3.3, and 15 where all of
+// V is NaN.
+//
+// In tiles of over kSinkScanKeys keys that is done for the blocks alone that hide a key from some row,
+// which are few: the epilogue reads V's rows of all blocks that were cleaned, 2^19 in 0.2 s at most, while
+// other warps wait for it, which they do for 2 s.  In the blocks that every row sees the product is right as
+// it is, but for an infinity whose weight is 0 in 16 bits.
+constexpr int kSinkScanKeys = 1 << 19;
+
+// The blocks of a tile that are not cleaned: those that hide no key from any row, in long tiles.
+template <class C>
+struct SinkClear {
+    int lo, hi, sinks;  // keys lo .. hi - 1, and before sinks, are seen by every row
+    __device__ __forceinline__ bool has(int n0) const {
+        return n0 + C::BN <= hi && (n0 >= lo || n0 + C::BN <= sinks);
     }
-    sinks = min(sinks, lo);
-    for (int j = sinks > 0 ? 0 : lo; j <= hi; j = j + 1 == sinks ? lo : j + 1) {
-        const long long at = j * stride + lane;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) s = fmaf(x[i], from16(k[at + i * 32]), s);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float w = ex2_approx(fmaf(s, scale_log2, -m));
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(w, from16(v[at + i * 32]), o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int col = lane + 32 * i, sc = col - col0;
-        if (sc < 0 || sc >= n) continue;
-        const uint16_t y = (uint16_t)(pack2<kBF16>(o[i] * inv_l, 0.f) & 0xffffu);
-        if (stage)
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage + (uint32_t)(sc / 64) * (BM * 128) +
-                                                          ((((sc % 64) / 8) ^ (rr & 7)) << 4) + (sc % 8) * 2),
-                         "h"(y)
-                         : "memory");
-        else
-            out[col] = y;
-    }
+};
+
+template <class C>
+__device__ __forceinline__ SinkClear<C> sink_clear(const FwdParams& p, const TileCoord& c) {
+    const int off = c.sk - c.sq;
+    SinkClear<C> clear;
+    clear.lo = min(c.m0 + C::NQ * C::BM, c.sq) - 1 + off - p.win_left;
+    clear.hi = (long long)c.n_kv * C::BN <= kSinkScanKeys ? 0
+               : p.has_hi                                 ? min(c.sk, c.m0 + off + p.hi_off + 1)
+                                                          : c.sk;
+    clear.sinks = p.sinks;
+    return clear;
 }
 
-constexpr int kSinkRowKeys = 1 << 20;  // rows that see more keys are not done again (bounded time)
+template <bool kBF16>
+__device__ __forceinline__ bool sink_nonfinite(uint32_t w) {  // either half of a word
+    constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+    return (((w & 0x7fff7fffu) + (0x8000u - kInf) * 0x10001u) & 0x80008000u) != 0;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ float sink_from16(uint16_t x) {
+    if constexpr (kBF16) return __uint_as_float((uint32_t)x << 16);
+    float f;
+    asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(x));
+    return f;
+}
+
+// V of block j of tile t, at `at`: values that are not finite give way to zeros.  By the warp that issues
+// the products, which has waited for the block, before it does.  (The softmax warps, which have less time
+// to spare, paid for the test in each block alone: 298 -> 314 us for [2, 8192, 32, 128], 268 -> 291 packed.)
+template <class C, bool kBF16>
+__device__ __noinline__ void sink_clean(const FwdParams& p, const VarlenTable* vt, int t, int j, uint32_t at) {
+    const TileCoord c = decode_tile<C, true>(p, vt, t);
+    if (sink_clear<C>(p, c).has(tile_block<true>(c, j) * C::BN)) return;
+#pragma unroll 4
+    for (int i = 0; i < C::kKVBytes / 512; ++i) {
+        const uint32_t a = at + i * 512 + (threadIdx.x & 31) * 16;
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(a)
+                     : "memory");
+        if (sink_nonfinite<kBF16>(w[0]) | sink_nonfinite<kBF16>(w[1]) | sink_nonfinite<kBF16>(w[2]) |
+            sink_nonfinite<kBF16>(w[3])) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] &= (sink_nonfinite<kBF16>(w[k] & 0xffffu) ? 0u : 0xffffu) |
+                        (sink_nonfinite<kBF16>(w[k] & 0xffff0000u) ? 0u : 0xffff0000u);
+            st_shared_v4(a, w[0], w[1], w[2], w[3]);
+        }
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+}
+
+// Adds to a warp's 32 rows of tile t what the cleaned blocks have lost, where `sums` (the row's weights
+// have a finite sum): to dims col0 .. col0 + n - 1 in the staging buffer's rows at `stage`, or in O where that
+// is 0.  A row is a lane's; a lane also has the dims l, l + 32, ... of a key.
+template <class C, bool kBF16>
+__device__ __noinline__ void sink_add(const FwdParams& p, const VarlenTable* vt, int t, bool sums, int col0, int n,
+                                      uint32_t stage) {
+    constexpr int V = C::D / 32, KU = 32 / V;  // values of a key's row a lane has; keys on their way at a time
+    const TileCoord c = decode_tile<C, true>(p, vt, t);
+    const SinkClear<C> clear = sink_clear<C>(p, c);
+    const int lane = threadIdx.x & 31, r0 = threadIdx.x & ~31;  // the warp's first row of the tile's
+    const int row = c.m0 + r0 + lane, off = c.sk - c.sq;
+    const int lo = row + off - p.win_left;
+    const int hi = !sums ? -1 : p.has_hi ? min(c.sk - 1, row + off + p.hi_off) : c.sk - 1;
+    const long long stride = (long long)p.Hkv * C::D, out_stride = (long long)p.Hq * C::D;
+    const uint16_t* v = static_cast<const uint16_t*>(p.v) + ((vt ? 0ll : (long long)c.b * p.Sk) + c.k_base) * stride +
+                        c.hk * C::D;
+    uint16_t* out = static_cast<uint16_t*>(p.o) + (c.o_row0 + c.m0 + r0) * out_stride + c.h * C::D;
+    const int k_end = min(c.sk, p.total_k - c.k_base);  // (keys past the tensor are zeros)
+    const uint32_t live = __ballot_sync(0xffffffffu, hi >= 0);
+    // Adds y, this lane's dim 32 i + l of a key, to the rows of a mask.
+    auto add = [&](uint32_t rows, int i, float y) {
+        const int col = lane + 32 * i, sc = col - col0;
+        if (sc < 0 || sc >= n) return;
+#pragma unroll 1
+        for (; rows; rows &= rows - 1) {
+            const int rr = __ffs((int)rows) - 1, r = (r0 + rr) & (C::BM - 1);
+            const uint32_t at = stage + (uint32_t)(sc / 64) * (C::BM * 128) + (uint32_t)r * 128 +
+                                ((((sc % 64) / 8) ^ (r & 7)) << 4) + (sc % 8) * 2;
+            uint16_t* to = out + rr * out_stride + col;
+            uint16_t o;
+            if (stage)
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(o) : "r"(at) : "memory");
+            else
+                o = *to;
+            o = (uint16_t)(pack2<kBF16>(sink_from16<kBF16>(o) + y, 0.f) & 0xffffu);
+            if (stage)
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(o) : "memory");
+            else
+                *to = o;
+        }
+    };
+    float all[V];  // what every row sees, at once at the end
+#pragma unroll
+    for (int i = 0; i < V; ++i) all[i] = 0.f;
+    __syncwarp();
+    for (int j = 0; j < c.n_kv; ++j) {
+        const int n0 = tile_block<true>(c, j) * C::BN;
+        if (clear.has(n0)) continue;
+        const int end = min(n0 + C::BN, k_end);
+        for (int k0 = max(n0, -c.k_base); k0 < end; k0 += KU) {
+            uint16_t x[KU][V];
+            bool odd = false;
+#pragma unroll
+            for (int u = 0; u < KU; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    x[u][i] = k0 + u < end ? v[(k0 + u) * stride + lane + 32 * i] : (uint16_t)0;
+                    odd |= sink_nonfinite<kBF16>(x[u][i]);
+                }
+            if (!__any_sync(0xffffffffu, odd)) continue;
+            uint32_t some = 0;  // the keys that some rows see and others do not
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                const int k = k0 + u;
+                const uint32_t sees = __ballot_sync(0xffffffffu, k <= hi && (k >= lo || k < p.sinks));
+                if (sees == live) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        all[i] += sink_nonfinite<kBF16>(x[u][i]) ? sink_from16<kBF16>(x[u][i]) : 0.f;
+                } else if (sees && k < end) {
+                    some |= 1u << u;
+                }
+            }
+            for (; some; some &= some - 1) {
+                const int k = k0 + __ffs((int)some) - 1;
+                const uint32_t sees = __ballot_sync(0xffffffffu, k <= hi && (k >= lo || k < p.sinks));
+#pragma unroll 1
+                for (int i = 0; i < V; ++i) {
+                    const uint16_t y = v[k * stride + lane + 32 * i];
+                    if (sink_nonfinite<kBF16>(y)) add(sees, i, sink_from16<kBF16>(y));
+                }
+                __syncwarp();
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (all[i] != 0.f) add(live, i, all[i]);
+    __syncwarp();
+}
 
 // kSinks: 0 for none; 1; or 2 for at most 32, whose block is then a short one (two Q tiles with P over S:
 // [2, 8192, 32, 128], window 1024, 4 sinks 309 -> 295 us; for more sinks the code that this adds costs
@@ -449,7 +564,7 @@ template <class C, bool kBF16, bool kVarlen, bool kSkip = false, int kSinks = 0>
 __global__ void __launch_bounds__(C::kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                  const FwdParams p) {
+                  const __grid_constant__ FwdParams p) {
     using L = typename C::template Layout<kVarlen>;
     constexpr bool kSink = kSinks > 0, kShort = kSinks == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -464,6 +579,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const uint32_t sBar = sStage + L::kStage;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_gen + L::kTileBytes + 8 * C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* redo = reinterpret_cast<int*>(tmem_slot + 2);  // kSink: the first and the last tile to go through again
     VarlenTable* vtab = kVarlen ? reinterpret_cast<VarlenTable*>(tmem_slot + 4) : nullptr;
 
     auto bar = [&](int i) -> uint32_t { return sBar + 8u * (uint32_t)i; };
@@ -482,6 +598,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             mbar_init(bar(i), by_warpgroup ? 4u : 1u);  // one elected arrive per warp
         }
         *abort_flag = 0;
+        if constexpr (kSink) {
+            redo[0] = 0x7fffffff;
+            redo[1] = -1;
+        }
         fence_mbar_init();
     }
     if (warp == C::kMmaWarp) {
@@ -540,12 +660,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     }
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
+    // What the roles count, K/V blocks and tiles with keys: the barriers' phases, which go on through the second pass.
+    uint32_t kv_it = 0, tcount = 0;
+    int tile0 = blockIdx.x;
+    bool again = false;  // kSink: the second pass
+[[maybe_unused]] roles:
     if (warp == C::kProducerWarp) {
         // ------------------------------------------------------------ TMA producer --
         if (lane == 0) {
-            uint32_t kv_it = 0, tcount = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+            for (int t = tile0; t < num_tiles && ok; t += gridDim.x) {
                 const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 if (c.n_kv <= 0) continue;
                 for (int q = 0; q < C::NQ && ok; ++q) {
@@ -602,7 +726,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         {
             constexpr uint32_t idesc_s = make_idesc_f16(128, C::BN, kBF16, false, false);
             constexpr uint32_t idesc_o = make_idesc_f16(128, C::D, kBF16, false, true);
-            uint32_t kv_it = 0, tcount = 0, it = 0;
+            uint32_t it = kv_it;
             bool ok = true;
             auto wait = [&](uint32_t b, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait(b, parity, wc));
@@ -656,6 +780,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 if constexpr (kShort) return j == 0 && c.ns == 1;
                 return false;
             };
+            // The second pass: V of block j of a tile, in stage st, loses what is not finite.
+            auto clean_v = [&](int t, int j, uint32_t st) {
+                if constexpr (kSink) {
+                    if (again) sink_clean<C, kBF16>(p, vtab, t, j, sV + st * C::kKVBytes);
+                }
+            };
             auto slot_of = [&](int q, uint32_t iter) -> uint32_t {
                 return C::NQ == 1 ? (iter & 1u) : (uint32_t)q;
             };
@@ -665,7 +795,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             // read S_q(j) (SFree); P.V_q(j) waits for P_q(j).  Every SFree phase is
             // awaited exactly once: the S issued after block `it` is that of block it + 1,
             // in this tile or as the first block of the next one.
-            for (int t = blockIdx.x; C::kSAhead && t < num_tiles && ok; t += gridDim.x) {
+            for (int t = tile0; C::kSAhead && t < num_tiles && ok; t += gridDim.x) {
                 const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 const int n = c.n_kv;
                 if (n <= 0) continue;
@@ -701,6 +831,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         if (!ok) break;
                     }
                     ok = wait(bar(C::kBarVFull + st), (cur / C::NS) & 1u);
+                    if (ok) clean_v(t, j, st);
                     for (int q = 0; q < C::NQ && ok; ++q) {
                         ok = wait(bar(C::kBarPFull + q), it & 1u);
                         if (ok && j == 0 && tcount > 0)
@@ -715,7 +846,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 kv_it += n;
                 ++tcount;
             }
-            for (int t = blockIdx.x; !C::kSAhead && t < num_tiles && ok; t += gridDim.x) {
+            for (int t = tile0; !C::kSAhead && t < num_tiles && ok; t += gridDim.x) {
                 const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 const int n = c.n_kv;
                 if (n <= 0) continue;
@@ -766,6 +897,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     }
                     ok = wait(bar(C::kBarVFull + st), (cur / C::NS) & 1u);
                     if (!ok) break;
+                    clean_v(t, j, st);
                     for (int q = 0; q < C::NQ && ok; ++q) {
                         ok = wait(bar(C::kBarPFull + q), it & 1u);
                         if (ok && j == 0 && tcount > 0)
@@ -796,7 +928,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
             // Every MMA issued has completed before TMEM and shared memory are released.
             umma_commit_elect(bar(C::kBarFinal));
-            mbar_wait_drain(bar(C::kBarFinal), 0);
+            mbar_wait_drain(bar(C::kBarFinal), again ? 1u : 0u);
             __syncwarp();
         }
     } else if (warp == C::kStoreWarp) {
@@ -816,9 +948,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // use of its warpgroup after that warpgroup's previous one was read, so its parity
         // waits are exact; Staged cannot run ahead of this warp either.
         if (!kVarlen && lane == 0) {
-            uint32_t use = 0;
+            uint32_t use = tcount * (C::NQ * L::kStageRounds);
             bool ok = true;
-            for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+            for (int t = tile0; t < num_tiles && ok; t += gridDim.x) {
                 const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
                 if (c.n_kv <= 0) continue;
                 for (int q = 0; q < C::NQ && ok; ++q) {
@@ -836,6 +968,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         ++use;
                     }
                 }
+                ++tcount;
             }
             bulk_wait_all();  // every store has landed before the kernel ends
         }
@@ -851,11 +984,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by > 2^8
         constexpr int kSC = C::BN / 32;        // 32-column chunks of S per block
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-        uint32_t it = 0, tcount = 0;
-        uint32_t nstaged = 0;  // staging-buffer uses of this warpgroup so far
+        uint32_t it = kv_it;
+        uint32_t nstaged = tcount * L::kStageRounds;  // staging-buffer uses of this warpgroup so far
         bool ok = true;
 
-        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        for (int t = tile0; t < num_tiles && ok; t += gridDim.x) {
             const TileCoord c = decode_tile<C, kSink>(p, vtab, t);
             const int row = c.m0 + q * C::BM + r;
             const int off = c.sk - c.sq;  // bottom-right causal alignment
@@ -1168,27 +1301,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                                      w[4 * v4 + 3]);
                 }
             };
-            // kSink: rows that are not finite again (sink_row), into the staging buffer, whose round
-            // holds columns col0 .. col0 + n - 1, or out to global memory.
-            auto mend_rows = [&](int col0, int n) {
+            // kSink: whether the row's weights have a finite sum.
+            const bool sums = kSink && row_ok && l_run > 0.f && l_run < __int_as_float(0x7f800000);
+            // The second pass: what V's cleaned blocks have lost, to columns col0 .. col0 + n - 1 of the staging
+            // buffer's round, or out to global memory.
+            auto add_odd = [&](int col0, int n) {
                 if constexpr (kSink) {
-                    const bool again = odd && row_ok && l_run > 0.f && l_run < __int_as_float(0x7f800000) &&
-                                       (long long)min(c.sk, p.win_left) + p.sinks <= kSinkRowKeys;
-                    uint32_t todo = __ballot_sync(0xffffffffu, again);
-                    while (todo) {
-                        const int from = __ffs((int)todo) - 1, at = row - lane + from, rr = r - lane + from;
-                        todo &= todo - 1;
-                        const long long q0 = ((c.o_row0 + at) * p.Hq + c.h) * C::D;
-                        const long long k0 = ((p.cu_q ? (long long)c.k_base : (long long)c.b * p.Sk) * p.Hkv + c.hk) * C::D;
-                        sink_row<C::D, C::BM, kBF16>(
-                            static_cast<const uint16_t*>(p.q) + q0, static_cast<const uint16_t*>(p.k) + k0,
-                            static_cast<const uint16_t*>(p.v) + k0, (long long)p.Hkv * C::D, p.sinks,
-                            (int)max((long long)at + off - p.win_left, 0ll),
-                            p.has_hi ? (int)min((long long)c.sk - 1, (long long)at + off + p.hi_off) : c.sk - 1,
-                            p.scale_log2, __shfl_sync(0xffffffffu, m_run, from), __shfl_sync(0xffffffffu, inv_l, from),
-                            col0, n, use_stage ? sStage + (uint32_t)rr * 128 : 0u, rr, static_cast<uint16_t*>(p.o) + q0);
-                    }
-                    __syncwarp();
+                    if (again) sink_add<C, kBF16>(p, vtab, t, sums, col0, n, use_stage ? sStage : 0u);
                 }
             };
             constexpr int kChunksPerRound = L::kStageAtoms * 2;  // 32-column chunks per round
@@ -1212,10 +1331,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         if (!ok) break;
                     }
                     put_chunk(ch * 32, ov[ch]);
-                    if (kSink && ch == C::D / 32 - 1) {  // one round holds the row
-                        __syncwarp();
-                        mend_rows(0, C::D);
-                    }
+                    if (ch == C::D / 32 - 1) add_odd(0, C::D);  // one round holds the row
                     if (use_stage && (ch % kChunksPerRound == kChunksPerRound - 1 || ch == C::D / 32 - 1))
                         stage_done();
                 }
@@ -1232,11 +1348,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     tmem_ld_32x32b_x32(tO + ch * 32, ov);
                     tmem_wait_ld(ov);
                     put_chunk(ch * 32, ov);
-                    if (kSink && (ch % kChunksPerRound == kChunksPerRound - 1 || ch == C::D / 32 - 1)) {
-                        __syncwarp();
-                        mend_rows(ch / kChunksPerRound * kChunksPerRound * 32, kChunksPerRound * 32);
-                        odd = false;
-                    }
+                    if (!use_stage ? ch == C::D / 32 - 1 : ch % kChunksPerRound == kChunksPerRound - 1)
+                        add_odd(use_stage ? (ch - kChunksPerRound + 1) * 32 : 0, use_stage ? kChunksPerRound * 32 : C::D);
                     if (use_stage && (ch % kChunksPerRound == kChunksPerRound - 1 || ch == C::D / 32 - 1))
                         stage_done();
                 }
@@ -1245,15 +1358,30 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::kBarODrained + q));
             }
+            if (kSink && sums && odd && !again) {
+                atomicMin(redo, t);
+                atomicMax(redo + 1, t);
+            }
             if (p.lse && row_ok) {
                 const float lse = none ? kNegInf : (m_run + lg2_approx(l_run)) * 0.69314718055994531f;
                 p.lse[c.lse0 + row] = lse;
             }
         }
+        kv_it = it;
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (kSink) {
+        // Every copy has landed and every product is done: the roles go on as behind any tile.
+        if (!again && redo[1] >= 0 && !*abort_flag) {
+            tc_fence_after();
+            again = true;
+            tile0 = redo[0];
+            num_tiles = redo[1] + 1;
+            goto roles;
+        }
+    }
     if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
@@ -1356,8 +1484,7 @@ fa_status launch_fwd_cfg(const FwdArgs& a, cudaStream_t stream) {
     p.lse = a.lse;
     p.status = a.dev_status;
     p.sinks = a.sinks;
-    p.q = a.q;
-    p.k = a.k;
+    p.total_k = varlen ? a.total_k : a.Sk;
     p.v = a.v;
     p.rcp_qb = reciprocal(p.num_qb);
     p.rcp_hq = reciprocal(a.Hq);

@@ -123,9 +123,9 @@ FA_API fa_status fa_fwd_varlen(const void *q, const void *k, const void *v, void
  *     j <= i + Sk - Sq + window_right  (the right side as without sinks), and
  *     j >= i + Sk - Sq - window_left  or  j < sinks.
  * Blocks of keys between the sinks and every row's window are skipped.  What a row does not see is
- * not used for it, NaN and infinities included (rows that see over 2^20 keys excepted, where an
- * infinity or NaN in V of a key that other rows of their block see gives NaN).  sinks >= 0, and
- * scale > 0 if there are any, else FA_ERR_INVALID_ARG.  Where the sinks do not matter (sinks == 0, or window_left == -1 or at least
+ * not used for it, NaN and infinities included; a V that is not finite and that some row sees costs
+ * a second pass over the tiles around it.  sinks >= 0, and scale > 0 if there are any, else
+ * FA_ERR_INVALID_ARG.  Where the sinks do not matter (sinks == 0, or window_left == -1 or at least
  * the keys) the call is fa_fwd_window (fa_fwd_varlen); everything else as there.
  */
 FA_API fa_status fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
