@@ -515,8 +515,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t* tmem_slot =
         reinterpret_cast<uint32_t*>(smem_raw + (sBar - raw) + 8 * C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    // Of the last two segments the one (counted from 1) whose V held a value that is not finite in a
-    // tile with hidden keys.
+    // Of the last segments those (counted from 1) whose V held a value that is not finite in a tile with
+    // hidden keys.  Sub-tile 0 writes; it may be scanning the tile two segments ahead of the one whose flag
+    // sub-tile 1 has yet to read, and no further: it needs a product behind sub-tile 1's P.
+    constexpr int kOddSlots = 4;
     volatile int* odd_seg = reinterpret_cast<volatile int*>(tmem_slot + 2);
     int* plan_len = reinterpret_cast<int*>(tmem_slot + 8);
     int* plan_prefix = plan_len + p.B;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             mbar_init(bar(i), by_warpgroup ? 4u : 1u);  // one arrive per warp
         }
         *abort_flag = 0;
-        odd_seg[0] = odd_seg[1] = 0;
+        for (int i = 0; i < kOddSlots; ++i) odd_seg[i] = 0;
         fence_mbar_init();
     }
     if (warp == C::kMmaWarp) {
@@ -831,7 +833,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         const uint32_t load = 2 * it + 1, at = sRing + (load % NB) * C::kTileBytes;
                         ok = mbar_wait(bar(C::kBarFull + load % NB), (load / NB) & 1u, wc);
                         if (!ok) break;
-                        if (paged_finite_v<DA, BN, kBF16>(at, t, clear, strip0)) odd_seg[tcount & 1u] = (int)tcount + 1;
+                        if (paged_finite_v<DA, BN, kBF16>(at, t, clear, strip0)) odd_seg[tcount % kOddSlots] = (int)tcount + 1;
                     }
                     ok = mbar_wait(bar(C::kBarSFull + (it & 1u)), (it >> 1) & 1u, wc);
                     if (!ok) break;
@@ -922,7 +924,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 ok = mbar_wait(bar(C::kBarODone + ((it - 1) & 1u)), ((it - 1) >> 1) & 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
-                const bool odd = odd_seg[tcount & 1u] == (int)tcount + 1;
+                const bool odd = odd_seg[tcount % kOddSlots] == (int)tcount + 1;
                 const size_t row0 = (size_t)s.b * p.Sq * p.Hq + s.hk * p.group;
                 const size_t part0 = ((size_t)member * 2 * p.ranges + s.slot) * R;
                 uint32_t o[NR];
@@ -1108,7 +1110,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         const uint32_t load = 2 * it + 1, at = sRing + (load % NB) * C::kTileBytes;
                         ok = mbar_wait(bar(C::kBarFull + load % NB), (load / NB) & 1u, wc);
                         if (!ok) break;
-                        if (paged_finite_v<DA, BN, kBF16>(at, r, clear, strip0)) odd_seg[tcount & 1u] = (int)tcount + 1;
+                        if (paged_finite_v<DA, BN, kBF16>(at, r, clear, strip0)) odd_seg[tcount % kOddSlots] = (int)tcount + 1;
                     }
                     const uint32_t slot = NQ == 1 ? it & 1u : (uint32_t)q;
                     float alpha = 1.f;
@@ -1209,7 +1211,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 ok = mbar_wait(bar(C::kBarODone + q), NQ == 1 ? (it - 1) & 1u : tcount & 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
-                const bool odd = odd_seg[tcount & 1u] == (int)tcount + 1;
+                const bool odd = odd_seg[tcount % kOddSlots] == (int)tcount + 1;
                 float l0, l1;
                 f2_unpack(l2, l0, l1);
                 const float l_run = l0 + l1;
