@@ -354,11 +354,12 @@ static __device__ __noinline__ uint32_t paged_drafts(const PagedDecParams& p, in
     return d & paged_bits(-t, len - 1 - k);
 }
 
-// The strips lo .. hi - 1 of a sequence's tiles hide no key from any token (some of the sinks' may
-// not either, and are masked all the same).
+// The strips of a sequence's tiles that hide no key from any token: lo .. hi - 1, and the first `sinks`,
+// which are all sinks.  The others are few whatever the lengths: the one that the last sinks are in, those
+// where the tokens' windows begin, and those with the tokens' own keys.
 struct PagedClear {
-    int lo, hi;
-    __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
+    int lo, hi, sinks;
+    __device__ __forceinline__ bool has(int i) const { return (i >= lo && i < hi) || i < sinks; }
 };
 
 __device__ __forceinline__ PagedClear paged_clear(const PagedDecParams& p, int len, const PagedStrips& t) {
@@ -366,6 +367,7 @@ __device__ __forceinline__ PagedClear paged_clear(const PagedDecParams& p, int l
     PagedClear c;
     c.lo = p.window_left >= 0 ? (max(len - 1 - p.window_left, 0) + 31) / 32 - t.first + t.sinks : 0;
     c.hi = max(p.tree ? ctx : ctx + 1, 0) / 32 - t.first + t.sinks;
+    c.sinks = min(t.sinks, p.sinks / 32);  // (before t.first: before the first token)
     return c;
 }
 
