@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kv8.cuh"  // launch_overlapped, grid_dependency_wait
@@ -723,7 +724,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         // is what feeds the tensor pipe.  Every lane waits on the barriers itself and the
         // outcome is voted, so the warp stays converged (elect.sync needs all 32 lanes)
         // even when a wait gives up.
-        {
+        //
+        // kSink: the second pass has a copy of the loops of its own, so that the first does not ask in each block
+        // which it is (8 packed prompts 272 -> 247 us; fixed lengths with 100 sinks 330 -> 311).  The fixed-length
+        // kernels of few sinks do ask: there two copies cost the softmax registers (297 -> 311).
+        constexpr bool kTwoCopies = kSink && !(kShort && !kVarlen);
+        auto products = [&](auto second) __attribute__((always_inline)) {
             constexpr uint32_t idesc_s = make_idesc_f16(128, C::BN, kBF16, false, false);
             constexpr uint32_t idesc_o = make_idesc_f16(128, C::D, kBF16, false, true);
             uint32_t it = kv_it;
@@ -782,7 +788,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             };
             // The second pass: V of block j of a tile, in stage st, loses what is not finite.
             auto clean_v = [&](int t, int j, uint32_t st) {
-                if constexpr (kSink) {
+                if constexpr (decltype(second)::value || (kSink && !kTwoCopies)) {
                     if (again) sink_clean<C, kBF16>(p, vtab, t, j, sV + st * C::kKVBytes);
                 }
             };
@@ -930,7 +936,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             umma_commit_elect(bar(C::kBarFinal));
             mbar_wait_drain(bar(C::kBarFinal), again ? 1u : 0u);
             __syncwarp();
-        }
+        };
+        if (kTwoCopies && again)
+            products(std::integral_constant<bool, kTwoCopies>());
+        else
+            products(std::false_type());
     } else if (warp == C::kStoreWarp) {
         if constexpr (kSink) {
             // A call whose CTAs have one tile each lets the next kernel start now, and a longer one as it ends:
