@@ -89,9 +89,10 @@ FA_API fa_status fa_fwd(const void *q, const void *k, const void *v, void *o, fl
  * attention"): query i attends only to keys j with
  *     i + Sk - Sq - window_left <= j <= i + Sk - Sq + window_right,
  * where -1 leaves that side unbounded, as any side past every key does; with causal != 0 the
- * right bound is additionally j <= i + Sk - Sq.  K/V blocks outside every row's window are skipped, not masked.  A row
- * whose window holds no key gets O = 0 and LSE = -inf.  window_left/right >= -1, else
- * FA_ERR_INVALID_ARG; everything else as fa_fwd (which equals window (-1, -1)).
+ * right bound is additionally j <= i + Sk - Sq.  K/V blocks outside every row's window are
+ * skipped, not masked.  A row whose window holds no key gets O = 0 and LSE = -inf.
+ * window_left/right >= -1, else FA_ERR_INVALID_ARG; everything else as fa_fwd (which equals
+ * window (-1, -1)).
  */
 FA_API fa_status fa_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse,
                                int B, int Sq, int Sk, int Hq, int Hkv, int D, float scale,
@@ -461,7 +462,8 @@ FA_API fa_status fa_decode_splitkv_paged_tree(const void *q, const void *k_pages
  * fa_decode_splitkv_paged, within 2 % of its time for long sequences and faster for short ones, from
  * pages of any multiple of 16.  The table entries of pages that hold no visible key may be anything
  * (of these only pages that share 32 aligned keys with a visible one are read at all).
- * window_left >= -1 and sinks >= 0, else FA_ERR_INVALID_ARG; everything else as fa_decode_splitkv_paged_tree.
+ * window_left >= -1 and sinks >= 0, else FA_ERR_INVALID_ARG; everything else as
+ * fa_decode_splitkv_paged_tree.
  */
 FA_API fa_status fa_decode_splitkv_paged_window(const void *q, const void *k_pages,
                                                 const void *v_pages, const int32_t *block_table,
